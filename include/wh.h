@@ -292,6 +292,57 @@ int wh_decode_attention(const wh_bf16 *q, const wh_bf16 *k, const wh_bf16 *v, in
                         wh_bf16 *out, void *workspace, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Attention of a batch whose sequences share long prefixes (the hypotheses of a beam search or
+ * of best-of sampling share their window's cross-attention keys; utterances decoded under one
+ * text prompt share the prompt's self-attention keys).  (The pages decode one hypothesis per
+ * clip: this is an addition of this library.)
+ *
+ * wh_keys describes the keys and values of n_set sets: key t of set i, head h is the 64 values at
+ * k + i * set_stride + t * row_stride + 64 h (likewise v).
+ *   n_keys  device int32 [n_set], or NULL: max_keys for all.  A count outside 0 .. max_keys is
+ *           clamped and recorded as WH_EBOUNDS, which wh_status() then returns.
+ *   weight  device float32 [n_set][n_kv_head][max_keys], or NULL: accumulators of the attention
+ *           weight that every key received.
+ *
+ * wh_prefix_attention: each of batch sequences has n_query queries (its last n_query tokens; 1 in
+ * an ordinary decode step), query row b * n_query + i, head h at q + row * q_stride + 64 h.  Query
+ * head h reads key head h / (n_head / n_kv_head).  Query i of sequence b attends over
+ *   - the prefix keys of its group: prefix set g serves sequences group_start[g] ..
+ *     group_start[g + 1] - 1 (device int32 [n_set + 1], ascending in 0 .. batch; a group may be
+ *     empty, and a sequence outside every group has no prefix), or, with group_start NULL,
+ *     batch / n_set sequences each, in order;
+ *   - its own keys 0 .. n_keys[b] - n_query + i (own->n_set = batch): the cache ends with the keys
+ *     of the n_query tokens, and a query sees no key behind its own;
+ * out = softmax(q k^T / sqrt(64)) v over both, and weight[key] += the sum over the queries (and
+ * over the query heads of a key head) of their softmax weight, for each wh_keys whose weight is
+ * not NULL.  A query that sees no key gives zeros.  Keys at and past a set's count are not read.
+ *   out     device bf16 [batch * n_query][64 n_head]; may not alias the inputs
+ *   prefix or own may be NULL (not both).
+ *   workspace >= wh_prefix_attention_workspace(batch, n_query, n_head, n_kv_head, prefix sets or 0,
+ *           prefix->max_keys or 0, own->max_keys or 0) bytes, 256-byte aligned, contents need not
+ *           be initialised; not shared by concurrent calls.
+ *   row_stride >= 64 n_kv_head, q_stride >= 64 n_head, set_stride >= 0, all multiples of 8; q, k, v,
+ *   out 16-byte aligned; batch, n_set <= 65535, n_query, n_head <= 1024, 1 <= max_keys <= 2^30.
+ * group_start is checked on the device: a group that does not lie in 0 .. batch is cut to it and
+ * recorded as WH_EBOUNDS; the outputs of the sequences concerned are then unspecified.
+ * The same inputs give the same bits (sums have one order).
+ * Errors: WH_EINVAL (also: batch not a multiple of n_set without group_start), WH_ENOSPC, WH_ECUDA.
+ * batch == 0 is a no-op.
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+    const wh_bf16 *k, *v;
+    int64_t row_stride, set_stride;   /* elements */
+    const int *n_keys;
+    float *weight;
+    int n_set, max_keys;
+} wh_keys;
+size_t wh_prefix_attention_workspace(int batch, int n_query, int n_head, int n_kv_head, int n_prefix,
+                                     int max_prefix, int max_own);
+int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch, int n_query, int n_head, int n_kv_head,
+                        const wh_keys *prefix, const int *group_start, const wh_keys *own, wh_bf16 *out,
+                        void *workspace, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------
  * One decoder step for a batch of sequences ("whisper 0.9.0 API", model.nu, wh_decode_step:
  * token tok at position pos, everything before it already in the KV cache, the logits left
  * on the device; wk_addv_row adds the stored position row; setrow writes the token's key and

@@ -295,6 +295,59 @@ def attend_one(q: np.ndarray, k: np.ndarray, v: np.ndarray, n_head: int) -> np.n
 
 
 # ========================================================================================
+# Attention over shared prefixes, and eviction by accumulated weight (additions of the library)
+# ========================================================================================
+def prefix_attention(q, n_query: int, n_head: int, n_kv_head: int, prefix, group_of, own):
+    """Attention of every sequence over its group's prefix and its own keys.
+
+    q [batch * n_query][n_head * 64]; prefix: a list of (k, v), each [n][n_kv_head * 64];
+    group_of: per sequence an index into prefix, or None; own: per sequence a (k, v) or None, its last
+    n_query keys being those of its n_query queries: query i sees the first n - (n_query - 1 - i).
+    Query head h reads key head h // (n_head // n_kv_head).  Returns (out, spread, prefix weights,
+    own weights): out like q, spread = sum p |v| (the scale of rounding errors in p), and per set the
+    softmax weight [n_kv_head][n] that its keys received.  A query that sees no key gives zeros."""
+    q = _f64(q)
+    batch, rep = q.shape[0] // n_query, n_head // n_kv_head
+    out, spread = np.zeros_like(q), np.zeros_like(q)
+    w_pre = [np.zeros((n_kv_head, k.shape[0])) for k, _ in prefix]
+    w_own = [None if o is None else np.zeros((n_kv_head, o[0].shape[0])) for o in own]
+    for b in range(batch):
+        pk, pv = prefix[group_of[b]] if group_of[b] is not None else (np.zeros((0, n_kv_head * 64)),) * 2
+        ok, ov = own[b] if own[b] is not None else (np.zeros((0, n_kv_head * 64)),) * 2
+        k, v = _f64(np.concatenate([pk, ok])), _f64(np.concatenate([pv, ov]))
+        n_pre = pk.shape[0]
+        for i in range(n_query):
+            sees = n_pre + max(0, ok.shape[0] - (n_query - 1 - i))
+            if sees == 0:
+                continue
+            row = b * n_query + i
+            for h in range(n_head):
+                kv, at = slice(64 * (h // rep), 64 * (h // rep) + 64), slice(64 * h, 64 * h + 64)
+                s = k[:sees, kv] @ q[row, at] / 8.0
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                out[row, at] = p @ v[:sees, kv]
+                spread[row, at] = p @ np.abs(v[:sees, kv])
+                if n_pre:
+                    w_pre[group_of[b]][h // rep] += p[:n_pre]
+                if sees > n_pre:
+                    w_own[b][h // rep, :sees - n_pre] += p[n_pre:]
+    return out, spread, w_pre, w_own
+
+
+def cache_evict(weight, budget: int, recent: int) -> np.ndarray:
+    """Which keys of one head stay when n = len(weight) keys are cut to `budget`: the last `recent`
+    and, of the others, the budget - recent of largest weight (of equal ones the lowest index; a NaN
+    counts as less than every number), in ascending order.  All of them while n <= budget."""
+    w = np.asarray(weight, dtype=np.float32)
+    n = w.shape[0]
+    if n <= budget:
+        return np.arange(n)
+    old = sorted(range(n - recent), key=lambda t: (bool(np.isnan(w[t])), 0.0 if np.isnan(w[t]) else -float(w[t]), t))
+    return np.array(sorted(old[:budget - recent]) + list(range(n - recent, n)), dtype=np.int64)
+
+
+# ========================================================================================
 # Upstream front end: 30-s windows of a long clip  [API] main.nu (wh_run); resampling to
 # 16 kHz with a windowed sinc  [README] "Transcribing", "How it is verified"
 # ========================================================================================

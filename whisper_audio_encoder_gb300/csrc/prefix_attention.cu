@@ -1,0 +1,682 @@
+// Attention of a batch whose sequences share long prefixes, and the weight every key receives.
+//
+// Sequence b of group g has n_query queries a head.  Query i attends over the group's prefix keys
+// 0 .. n_g - 1 and over the sequence's own keys 0 .. n_b - (n_query - i), i.e. no key behind its own:
+//   s_t = q . k_t / 8,   p = softmax(s),   o = sum_t p_t v_t,   weight[t] += sum over the queries of p_t
+// A prefix key and value are read once for all the queries of the group (all sequences, queries and
+// query heads of its key head are the rows of one matrix product), not once per sequence.
+#include "common.cuh"
+#include "internal.h"
+
+namespace wh {
+namespace {
+
+constexpr int PA_WARPS = 4;
+constexpr int PA_THREADS = 32 * PA_WARPS;
+constexpr int PA_KEYS = 16;        // keys of one warp step
+constexpr int PM_ROWS = 8;         // rows of one merge block (16 threads a row)
+constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
+constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp
+constexpr float PA_SCALE = 0.125f * 1.4426950408889634f;   // log2(e) / sqrt(64): scores in the exp2 domain
+
+struct PaSet {
+    const __nv_bfloat16 *k, *v;
+    long long row_stride, set_stride;   // elements
+    const int *n_keys;                  // device [n_set] or null (max_keys for all)
+    float *weight;                      // device [n_set][n_kv][max_keys] or null
+    int n_set, max_keys;
+    int splits, chunk;                  // key ranges of one set and keys of a range
+};
+
+struct PaArgs {
+    PaSet pre, own;
+    const __nv_bfloat16 *q;
+    long long q_stride;
+    const int *group_start;   // device [pre.n_set + 1] or null: gsize sequences each
+    int gsize, batch, nq, n_head, n_kv, rep;
+    int slots;                // prefix: row-tile slots of a key head over all groups
+    int own_tiles;            // row tiles of a sequence
+    long long pre_blocks;     // blocks [0, pre_blocks) take prefix work, the rest own keys
+    float *part_o;            // [row][pre.splits + own.splits][64], row = (b nq + i) n_head + h
+    float2 *part_ml;          // [row][pre.splits + own.splits]: running maximum and sum
+    float2 *stats;            // [row]: maximum and 1 / sum (weights only)
+    __nv_bfloat16 *out;       // [batch * nq][64 n_head]
+    int direct;               // one range covers everything a row sees: write out, no merge
+    int *status;
+};
+
+__device__ __forceinline__ int clamp_count(const PaSet &s, int set) {
+    return s.n_keys ? min(max(__ldg(s.n_keys + set), 0), s.max_keys) : s.max_keys;
+}
+
+// Largest g in [0, n) with start[g] * mul / div + g * add <= x, by the whole warp, 32 probes at a time.
+__device__ __forceinline__ int warp_search(const int *start, int n, int mul, int div, int add, long long x) {
+    int lo = 0, len = n;
+    const int lane = threadIdx.x & 31;
+    while (len > 1) {
+        const int step = (len + 31) / 32, i = lane * step;
+        bool le = false;
+        if (i < len) {
+            const int g = lo + i;
+            le = (long long)__ldg(start + g) * mul / div + (long long)g * add <= x;
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, le) | 1u;
+        const int top = (31 - __clz(m)) * step;
+        lo += top;
+        len = min(step, len - top);
+    }
+    return lo;
+}
+
+// Sequences [s, e) of group g, cut to 0 .. batch.
+__device__ __forceinline__ void group_range(const PaArgs &p, int g, int &s, int &e) {
+    if (p.group_start) {
+        s = min(max(__ldg(p.group_start + g), 0), p.batch);
+        e = min(max(__ldg(p.group_start + g + 1), s), p.batch);
+    } else {
+        s = g * p.gsize;
+        e = s + p.gsize;
+    }
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t to_tf32(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+
+// The rows of one work item: queries of sequences first .. (rows / (nq rep)), row r =
+// ((sequence, query), query head of the key head).
+struct Rows {
+    int seq0, n, hk;
+    __device__ __forceinline__ void locate(const PaArgs &p, int r, int &qrow, int &head, int &qi) const {
+        const int per = p.nq * p.rep, s = r / per, w = r - s * per;
+        qi = w / p.rep;
+        qrow = (seq0 + s) * p.nq + qi;
+        head = hk * p.rep + (w - qi * p.rep);
+    }
+};
+
+// Query fragments of rows r0 + g and r0 + g + 8 (g = lane / 4).  The 64 dims of a head are spread over the
+// four lanes of a row as 8c .. 8c+7 and 32+8c .. 32+8c+7 (c = lane % 4), so that a lane's 16-byte loads of a
+// key are its part of four MMA steps; the sum over dims does not mind the order.
+__device__ __forceinline__ void load_q(const PaArgs &p, const Rows &rw, int r0, uint32_t (&a)[4][4]) {
+    const int g = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int r = r0 + g + 8 * half;
+        uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+        if (r < rw.n) {
+            int qrow, head, qi;
+            rw.locate(p, r, qrow, head, qi);
+            const uint4 *s = reinterpret_cast<const uint4 *>(p.q + (long long)qrow * p.q_stride + head * 64) + c;
+            u0 = __ldg(s);
+            u1 = __ldg(s + 4);
+        }
+        a[0][half] = u0.x, a[0][half + 2] = u0.y, a[1][half] = u0.z, a[1][half + 2] = u0.w;
+        a[2][half] = u1.x, a[2][half + 2] = u1.y, a[3][half] = u1.z, a[3][half + 2] = u1.w;
+    }
+}
+
+// Scores of 16 rows x 8 keys: lane (g, c) gives keys 2c, 2c+1 of rows g (0, 1) and g + 8 (2, 3).
+__device__ __forceinline__ void score8(const uint32_t (&a)[4][4], const uint4 &k0, const uint4 &k1, float (&s)[4]) {
+    s[0] = s[1] = s[2] = s[3] = 0.0f;
+    mma_bf16(s, a[0][0], a[0][1], a[0][2], a[0][3], k0.x, k0.y);
+    mma_bf16(s, a[1][0], a[1][1], a[1][2], a[1][3], k0.z, k0.w);
+    mma_bf16(s, a[2][0], a[2][1], a[2][2], a[2][3], k1.x, k1.y);
+    mma_bf16(s, a[3][0], a[3][1], a[3][2], a[3][3], k1.z, k1.w);
+}
+
+template <int RT>
+__global__ void __launch_bounds__(PA_THREADS) k_prefix_attention(const PaArgs p) {
+    constexpr int TR = 16 * RT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    pdl_wait();                // what runs after this kernel's trigger may count on its inputs
+    pdl_launch_dependents();
+    // ---- which rows, which keys ----
+    const bool is_pre = blockIdx.x < p.pre_blocks;
+    Rows rw;
+    int set, split, r0;
+    if (is_pre) {
+        unsigned x = blockIdx.x;
+        const int slot = x % p.slots;
+        x /= p.slots;
+        rw.hk = x % p.n_kv;
+        split = x / p.n_kv;
+        const int per = p.nq * p.rep;
+        int s, e;
+        if (p.group_start) {
+            if (rw.hk == 0 && split == 0 && slot < p.pre.n_set && threadIdx.x == 0) {   // report bad groups once
+                const int a = __ldg(p.group_start + slot), b = __ldg(p.group_start + slot + 1);
+                if (a < 0 || b < a || b > p.batch) atomicCAS(p.status, 0, WH_EBOUNDS);
+            }
+            // group g's tiles take slots start[g] per / TR + g and up: they end before group g + 1's
+            set = warp_search(p.group_start, p.pre.n_set, per, TR, 1, slot);
+            group_range(p, set, s, e);
+            r0 = (slot - (int)((long long)s * per / TR) - set) * TR;
+        } else {
+            const int tiles = (p.gsize * per + TR - 1) / TR;
+            set = slot / tiles;
+            group_range(p, set, s, e);
+            r0 = (slot - set * tiles) * TR;
+        }
+        rw.seq0 = s;
+        rw.n = (e - s) * per;
+        if (r0 < 0 || r0 >= rw.n) return;
+    } else {
+        long long x = blockIdx.x - p.pre_blocks;
+        const int tile = x % p.own_tiles;
+        x /= p.own_tiles;
+        rw.hk = x % p.n_kv;
+        x /= p.n_kv;
+        split = x % p.own.splits;
+        set = x / p.own.splits;
+        rw.seq0 = set;
+        rw.n = p.nq * p.rep;
+        r0 = tile * TR;
+    }
+    const PaSet &ks = is_pre ? p.pre : p.own;
+    const int nk = clamp_count(ks, set);
+    if (ks.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && threadIdx.x == 0 && __ldg(ks.n_keys + set) != nk)
+        atomicCAS(p.status, 0, WH_EBOUNDS);
+    const int k0 = split * ks.chunk, k1 = min(nk, k0 + ks.chunk);
+    if (k0 >= k1 && !p.direct) return;   // nothing here: the merge knows
+
+    uint32_t qa[RT][4][4];
+    int lim[RT][2];   // own keys: the first key that a row does not see
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        load_q(p, rw, r0 + 16 * t, qa[t]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            lim[t][half] = nk;
+            if (!is_pre) {
+                int qrow, head, qi;
+                rw.locate(p, min(r0 + 16 * t + g + 8 * half, rw.n - 1), qrow, head, qi);
+                lim[t][half] = nk - (p.nq - 1 - qi);
+            }
+        }
+    }
+    const int full = is_pre ? nk : nk - (p.nq - 1);   // every row sees the keys before this one
+
+    float m[RT][2], l[RT][2], o[RT][8][4];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        m[t][0] = m[t][1] = -INFINITY;
+        l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
+    }
+    const __nv_bfloat16 *kb = ks.k + (long long)set * ks.set_stride + rw.hk * 64 + 8 * c;
+    const __nv_bfloat16 *vb = ks.v + (long long)set * ks.set_stride + rw.hk * 64 + 8 * g;
+
+    // keys t + g, t + 8 + g for the scores; values t + 2c, t + 2c + 1, t + 8 + 2c, t + 9 + 2c; zeros past the range
+    auto load = [&](int t, uint4 (&kr)[2][2], uint4 (&vr)[2][2]) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int tk = t + 8 * j + g;
+            kr[j][0] = kr[j][1] = make_uint4(0, 0, 0, 0);
+            if (tk < k1) {
+                const uint4 *s = reinterpret_cast<const uint4 *>(kb + (long long)tk * ks.row_stride);
+                kr[j][0] = __ldg(s);
+                kr[j][1] = __ldg(s + 4);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tv = t + 8 * j + 2 * c + i;
+                vr[j][i] = make_uint4(0, 0, 0, 0);
+                if (tv < k1) vr[j][i] = __ldg(reinterpret_cast<const uint4 *>(vb + (long long)tv * ks.row_stride));
+            }
+        }
+    };
+    uint4 kr[2][2], vr[2][2];
+    int t0 = k0 + warp * PA_KEYS;
+    load(t0, kr, vr);
+    for (; t0 < k1; t0 += PA_WARPS * PA_KEYS) {
+        uint4 kn[2][2], vn[2][2];
+        load(t0 + PA_WARPS * PA_KEYS, kn, vn);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            float s[2][4];
+            score8(qa[t], kr[0][0], kr[0][1], s[0]);
+            score8(qa[t], kr[1][0], kr[1][1], s[1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[j][i] *= PA_SCALE;
+            if (t0 + PA_KEYS > min(k1, full)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = t0 + 8 * j + 2 * c + (i & 1);
+                        if (key >= min(k1, lim[t][i >> 1])) s[j][i] = -INFINITY;
+                    }
+            }
+            float mx[2], mn[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                mx[half] = fmaxf(fmaxf(s[0][2 * half], s[0][2 * half + 1]), fmaxf(s[1][2 * half], s[1][2 * half + 1]));
+                mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
+                mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
+                mn[half] = fmaxf(m[t][half], mx[half]);
+            }
+            if (__any_sync(0xffffffffu, mn[0] > m[t][0] || mn[1] > m[t][1])) {   // some row's maximum moved
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float f = m[t][half] == -INFINITY ? 0.0f : ex2_approx(m[t][half] - mn[half]);
+                    l[t][half] *= f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        o[t][j][2 * half] *= f;
+                        o[t][j][2 * half + 1] *= f;
+                    }
+                    m[t][half] = mn[half];
+                }
+            }
+            const float ms[2] = {m[t][0] == -INFINITY ? 0.0f : m[t][0], m[t][1] == -INFINITY ? 0.0f : m[t][1]};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t pt[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = ex2_approx(s[j][i] - ms[i >> 1]);
+                    l[t][i >> 1] += e;
+                    pt[i] = to_tf32(e);   // 11 bits of mantissa: an eighth of the output's rounding
+                }
+                const uint32_t a0[4] = {vr[j][0].x, vr[j][0].y, vr[j][0].z, vr[j][0].w};
+                const uint32_t a1[4] = {vr[j][1].x, vr[j][1].y, vr[j][1].z, vr[j][1].w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    mma_tf32(o[t][2 * w], pt[0], pt[2], pt[1], pt[3], a0[w] << 16, a1[w] << 16);
+                    mma_tf32(o[t][2 * w + 1], pt[0], pt[2], pt[1], pt[3], a0[w] & 0xffff0000u, a1[w] & 0xffff0000u);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                kr[j][i] = kn[j][i];
+                vr[j][i] = vn[j][i];
+            }
+    }
+
+    // ---- merge the warps ----
+    __shared__ float so[PA_WARPS][TR][68];
+    __shared__ float2 sml[PA_WARPS][TR];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float ls = l[t][half];
+            ls += __shfl_xor_sync(0xffffffffu, ls, 1);
+            ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+            const int r = 16 * t + g + 8 * half;
+            if (c == 0) sml[warp][r] = make_float2(m[t][half], ls);
+            // dims 16c + j (first column of n-tile j) and 16c + 8 + j (second)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float *d = &so[warp][r][16 * c + 8 * i];
+                *reinterpret_cast<float4 *>(d) = make_float4(o[t][0][2 * half + i], o[t][1][2 * half + i],
+                                                             o[t][2][2 * half + i], o[t][3][2 * half + i]);
+                *reinterpret_cast<float4 *>(d + 4) = make_float4(o[t][4][2 * half + i], o[t][5][2 * half + i],
+                                                                 o[t][6][2 * half + i], o[t][7][2 * half + i]);
+            }
+        }
+    __syncthreads();
+    const int ns = p.pre.splits + p.own.splits, part = is_pre ? split : p.pre.splits + split;
+    for (int i = threadIdx.x; i < TR * 8; i += PA_THREADS) {
+        const int r = i >> 3, d0 = 8 * (i & 7);
+        if (r0 + r >= rw.n) break;
+        float mt = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < PA_WARPS; ++w) mt = fmaxf(mt, sml[w][r].x);
+        float lt = 0.0f, v[8] = {};
+#pragma unroll
+        for (int w = 0; w < PA_WARPS; ++w) {
+            const float2 ml = sml[w][r];
+            const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mt);
+            lt = fmaf(ml.y, f, lt);
+            const float4 x = *reinterpret_cast<const float4 *>(&so[w][r][d0]);
+            const float4 y = *reinterpret_cast<const float4 *>(&so[w][r][d0 + 4]);
+            v[0] = fmaf(x.x, f, v[0]), v[1] = fmaf(x.y, f, v[1]), v[2] = fmaf(x.z, f, v[2]), v[3] = fmaf(x.w, f, v[3]);
+            v[4] = fmaf(y.x, f, v[4]), v[5] = fmaf(y.y, f, v[5]), v[6] = fmaf(y.z, f, v[6]), v[7] = fmaf(y.w, f, v[7]);
+        }
+        int qrow, head, qi;
+        rw.locate(p, r0 + r, qrow, head, qi);
+        const long long row = (long long)qrow * p.n_head + head;
+        if (p.direct) {
+            const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;   // a query that sees no key: zeros
+            *reinterpret_cast<uint4 *>(p.out + row * 64 + d0) =
+                make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                           pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
+            if (p.stats && d0 == 0) p.stats[row] = make_float2(mt == -INFINITY ? 0.0f : mt, inv);
+        } else {
+            float4 *d = reinterpret_cast<float4 *>(p.part_o + (row * ns + part) * 64 + d0);
+            d[0] = make_float4(v[0], v[1], v[2], v[3]);
+            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+            if (d0 == 0) p.part_ml[row * ns + part] = make_float2(mt, lt);
+        }
+    }
+}
+
+// o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the ranges of a row that hold keys, in order.
+__global__ void __launch_bounds__(16 * PM_ROWS) k_prefix_merge(const PaArgs p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long rows = (long long)p.batch * p.nq * p.n_head;
+    const long long row = (long long)blockIdx.x * PM_ROWS + (threadIdx.x >> 4);
+    const int lane = threadIdx.x & 15;
+    const int b = (int)(min(row, rows - 1) / ((long long)p.nq * p.n_head));
+    int np = 0, no = 0;
+    if (p.pre.n_set > 0) {
+        int g = -1;
+        if (p.group_start) {
+            // (the two rows of a warp may belong to different sequences: search one after the other)
+            const int b0 = __shfl_sync(0xffffffffu, b, 0), b1 = __shfl_sync(0xffffffffu, b, 16);
+            const int g0 = warp_search(p.group_start, p.pre.n_set, 1, 1, 0, b0);
+            const int g1 = b1 == b0 ? g0 : warp_search(p.group_start, p.pre.n_set, 1, 1, 0, b1);
+            const int gg = (threadIdx.x & 16) ? g1 : g0;
+            int s, e;
+            group_range(p, gg, s, e);
+            if (b >= s && b < e) g = gg;
+        } else if (b / p.gsize < p.pre.n_set) {
+            g = b / p.gsize;
+        }
+        if (g >= 0) np = (clamp_count(p.pre, g) + p.pre.chunk - 1) / p.pre.chunk;
+    }
+    if (p.own.n_set > 0) no = (clamp_count(p.own, b) + p.own.chunk - 1) / p.own.chunk;
+    const int ns = p.pre.splits + p.own.splits;
+    const float2 *ml = p.part_ml + min(row, rows - 1) * ns;
+    const uint32_t half = 0xffffu << (threadIdx.x & 16);
+    // ranges that hold keys: 0 .. np-1 of the prefix, then 0 .. no-1 of the sequence's own
+    float m = -INFINITY;
+    for (int i = lane; i < np + no; i += 16) m = fmaxf(m, __ldcg(&ml[i < np ? i : p.pre.splits + i - np].x));
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, x, 16));
+    float l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 *po = reinterpret_cast<const float4 *>(p.part_o + min(row, rows - 1) * ns * 64) + lane;
+#pragma unroll 4
+    for (int i = 0; i < np + no; ++i) {
+        const int s = i < np ? i : p.pre.splits + i - np;
+        const float2 x = __ldcg(ml + s);
+        const float4 v = __ldcg(po + s * 16);
+        const float f = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - m);
+        l = fmaf(x.y, f, l);
+        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+    }
+    if (row >= rows) return;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint2 *>(p.out + row * 64 + 4 * lane) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (p.stats && lane == 0) p.stats[row] = make_float2(m == -INFINITY ? 0.0f : m, inv);
+}
+
+// weight[t] += sum over the set's queries of 2^(s_t - m) / l: the scores again, with every row's final
+// maximum and sum.  One warp holds 32 keys and goes through the rows 16 at a time, so each sum has one
+// fixed order.
+__global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p, int own) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const PaSet &ks = own ? p.own : p.pre;
+    Rows rw;
+    rw.hk = blockIdx.y;
+    const int set = blockIdx.z;
+    const int t0 = (blockIdx.x * PW_WARPS + (threadIdx.x >> 5)) * PW_KEYS;
+    const int nk = clamp_count(ks, set);
+    if (t0 >= nk) {
+        pdl_wait();   // on every path: a kernel after this one counts on the merge's end too
+        return;
+    }
+    int s0 = set, e0 = set + 1;
+    if (!own) group_range(p, set, s0, e0);
+    rw.seq0 = s0;
+    rw.n = (e0 - s0) * p.nq * p.rep;
+    const __nv_bfloat16 *kb = ks.k + (long long)set * ks.set_stride + rw.hk * 64 + 8 * c;
+    uint4 kr[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int tk = t0 + 8 * j + g;
+        kr[j][0] = kr[j][1] = make_uint4(0, 0, 0, 0);
+        if (tk < nk) {
+            const uint4 *s = reinterpret_cast<const uint4 *>(kb + (long long)tk * ks.row_stride);
+            kr[j][0] = __ldg(s);
+            kr[j][1] = __ldg(s + 4);
+        }
+    }
+    pdl_wait();
+    float acc[4][2] = {};
+    for (int r0 = 0; r0 < rw.n; r0 += 16) {
+        uint32_t qa[4][4];
+        load_q(p, rw, r0, qa);
+        float2 st[2];
+        int lim[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            st[half] = make_float2(0.0f, 0.0f);
+            lim[half] = 0;   // rows past the last: no key
+            if (r0 + g + 8 * half < rw.n) {
+                int qrow, head, qi;
+                rw.locate(p, r0 + g + 8 * half, qrow, head, qi);
+                st[half] = __ldcg(p.stats + (long long)qrow * p.n_head + head);
+                lim[half] = own ? nk - (p.nq - 1 - qi) : nk;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float s[4];
+            score8(qa, kr[j][0], kr[j][1], s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = t0 + 8 * j + 2 * c + (i & 1);
+                const float e = ex2_approx(s[i] * PA_SCALE - st[i >> 1].x);
+                if (key < lim[i >> 1]) acc[j][i & 1] = fmaf(e, st[i >> 1].y, acc[j][i & 1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float a = acc[j][i];
+            a += __shfl_xor_sync(0xffffffffu, a, 4);
+            a += __shfl_xor_sync(0xffffffffu, a, 8);
+            a += __shfl_xor_sync(0xffffffffu, a, 16);
+            const int key = t0 + 8 * j + 2 * c + i;
+            if (g == 0 && key < nk) ks.weight[((long long)set * p.n_kv + rw.hk) * ks.max_keys + key] += a;
+        }
+}
+
+size_t up256p(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Key ranges of a set: as many as fill the device (4 blocks on each of GB300's 152 SMs), none shorter
+// than 64 keys.
+constexpr long long PA_BLOCKS = 4 * 152;
+void split_keys(PaSet &s, long long items) {
+    s.splits = s.chunk = 0;
+    if (s.n_set <= 0) return;
+    long long n = (PA_BLOCKS + items - 1) / items;
+    const long long most = (s.max_keys + 63) / 64;
+    n = n < 1 ? 1 : (n > most ? most : n);
+    s.chunk = (int)(((s.max_keys + n - 1) / n + 63) / 64 * 64);
+    s.splits = (s.max_keys + s.chunk - 1) / s.chunk;
+}
+
+struct PaPlan {
+    int rt;
+    size_t part_o, part_ml, stats, total;
+};
+
+// Row tiles, key ranges and the workspace's layout, from host-known sizes only.
+PaPlan plan(PaArgs &a) {
+    PaPlan pl;
+    const long long per = (long long)a.nq * a.rep, all = a.batch * per;
+    const long long rows_a_set = a.pre.n_set > 0 ? (all + a.pre.n_set - 1) / a.pre.n_set : per;
+    pl.rt = rows_a_set > 16 ? 2 : 1;
+    const int tr = 16 * pl.rt;
+    a.slots = 0;
+    if (a.pre.n_set > 0)
+        a.slots = (int)(a.gsize == 0 ? a.pre.n_set + all / tr : a.pre.n_set * ((a.gsize * per + tr - 1) / tr));
+    a.own_tiles = (int)((per + tr - 1) / tr);
+    split_keys(a.pre, (long long)a.slots * a.n_kv);
+    split_keys(a.own, (long long)a.own.n_set * a.n_kv * a.own_tiles);
+    const size_t rows = (size_t)a.batch * a.nq * a.n_head, ns = (size_t)a.pre.splits + a.own.splits;
+    a.direct = ns == 1 && (a.pre.n_set == 0 || a.gsize > 0);
+    size_t off = 0;
+    pl.part_o = off;  off += a.direct ? 0 : up256p(rows * ns * 64 * 4);
+    pl.part_ml = off; off += a.direct ? 0 : up256p(rows * ns * 8);
+    pl.stats = off;   off += up256p(rows * 8);
+    pl.total = off < 256 ? 256 : off;
+    return pl;
+}
+
+bool fits(const void *p, size_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int check_keys(const wh_keys *s, int n_kv, PaSet *o) {
+    *o = PaSet{};
+    if (!s) return WH_OK;
+    if (s->n_set < 1 || s->n_set > 65535 || s->max_keys < 1 || s->max_keys > (1 << 30)) return WH_EINVAL;
+    if (s->row_stride < 64LL * n_kv || s->row_stride % 8 != 0 || s->set_stride < 0 || s->set_stride % 8 != 0)
+        return WH_EINVAL;
+    if (!fits(s->k, 16) || !fits(s->v, 16) || (s->n_keys && !fits(s->n_keys, 4)) || (s->weight && !fits(s->weight, 4)))
+        return WH_EINVAL;
+    o->k = reinterpret_cast<const __nv_bfloat16 *>(s->k);
+    o->v = reinterpret_cast<const __nv_bfloat16 *>(s->v);
+    o->row_stride = s->row_stride;
+    o->set_stride = s->set_stride;
+    o->n_keys = s->n_keys;
+    o->weight = s->weight;
+    o->n_set = s->n_set;
+    o->max_keys = s->max_keys;
+    return WH_OK;
+}
+
+bool shape_ok(int batch, int n_query, int n_head, int n_kv) {
+    return batch >= 0 && batch <= 65535 && n_query >= 1 && n_query <= 1024 && n_head >= 1 && n_head <= 1024 &&
+           n_kv >= 1 && n_head % n_kv == 0 && (long long)batch * n_query * n_head <= 0x7fffffffLL;
+}
+
+int launch(PaArgs &a, uint8_t *ws, size_t ws_bytes, cudaStream_t s) {
+    const PaPlan pl = plan(a);
+    if (ws_bytes < pl.total) return WH_ENOSPC;
+    a.part_o = reinterpret_cast<float *>(ws + pl.part_o);
+    a.part_ml = reinterpret_cast<float2 *>(ws + pl.part_ml);
+    a.stats = a.pre.weight || a.own.weight ? reinterpret_cast<float2 *>(ws + pl.stats) : nullptr;
+    a.pre_blocks = (long long)a.slots * a.n_kv * a.pre.splits;
+    const long long blocks = a.pre_blocks + (long long)a.own_tiles * a.n_kv * a.own.splits * a.own.n_set;
+    const long long rows = (long long)a.batch * a.nq * a.n_head;
+    if (blocks > 0x7fffffffLL) return WH_EINVAL;
+    if (pl.rt == 1)
+        k_prefix_attention<1><<<(unsigned)blocks, PA_THREADS, 0, s>>>(a);
+    else
+        k_prefix_attention<2><<<(unsigned)blocks, PA_THREADS, 0, s>>>(a);
+    count_launch();
+    if (cudaGetLastError() != cudaSuccess) return WH_ECUDA;
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    lc.stream = s;
+    if (!a.direct) {
+        lc.gridDim = dim3((unsigned)((rows + PM_ROWS - 1) / PM_ROWS));
+        lc.blockDim = dim3(16 * PM_ROWS);
+        if (cudaLaunchKernelEx(&lc, k_prefix_merge, a) != cudaSuccess) return WH_ECUDA;
+        count_launch();
+    }
+    for (int own = 0; own < 2; ++own) {
+        const PaSet &ks = own ? a.own : a.pre;
+        if (!ks.weight) continue;
+        lc.gridDim = dim3((ks.max_keys + PW_WARPS * PW_KEYS - 1) / (PW_WARPS * PW_KEYS), a.n_kv, ks.n_set);
+        lc.blockDim = dim3(32 * PW_WARPS);
+        if (cudaLaunchKernelEx(&lc, k_prefix_weight, a, own) != cudaSuccess) return WH_ECUDA;
+        count_launch();
+    }
+    return cudaGetLastError() == cudaSuccess ? WH_OK : WH_ECUDA;
+}
+
+}  // namespace
+}  // namespace wh
+
+using namespace wh;
+
+extern "C" size_t wh_prefix_attention_workspace(int batch, int n_query, int n_head, int n_kv_head, int n_prefix,
+                                                int max_prefix, int max_own) {
+    if (!shape_ok(batch, n_query, n_head, n_kv_head) || batch == 0 || n_prefix < 0 || n_prefix > 65535 ||
+        max_prefix < 0 || max_prefix > (1 << 30) || max_own < 0 || max_own > (1 << 30))
+        return 0;
+    PaArgs a = {};
+    a.batch = batch;
+    a.nq = n_query;
+    a.n_head = n_head;
+    a.n_kv = n_kv_head;
+    a.rep = n_head / n_kv_head;
+    a.pre.n_set = max_prefix > 0 ? n_prefix : 0;
+    a.pre.max_keys = max_prefix;
+    a.own.n_set = max_own > 0 ? batch : 0;
+    a.own.max_keys = max_own;
+    size_t most = plan(a).total;   // groups of any size
+    if (a.pre.n_set > 0 && batch % a.pre.n_set == 0) {
+        a.gsize = batch / a.pre.n_set;
+        const size_t t = plan(a).total;
+        most = t > most ? t : most;
+    }
+    return most;
+}
+
+extern "C" int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch, int n_query, int n_head,
+                                   int n_kv_head, const wh_keys *prefix, const int *group_start, const wh_keys *own,
+                                   wh_bf16 *out, void *workspace, size_t ws_bytes, void *stream) {
+    if (!shape_ok(batch, n_query, n_head, n_kv_head) || q_stride < 64LL * n_head || q_stride % 8 != 0) return WH_EINVAL;
+    if (!prefix && !own) return WH_EINVAL;
+    PaArgs a = {};
+    if (int rc = check_keys(prefix, n_kv_head, &a.pre)) return rc;
+    if (int rc = check_keys(own, n_kv_head, &a.own)) return rc;
+    if (own && own->n_set != batch && batch > 0) return WH_EINVAL;
+    if (group_start && (!prefix || !fits(group_start, 4))) return WH_EINVAL;
+    if (prefix && !group_start && batch % prefix->n_set != 0) return WH_EINVAL;
+    if (batch == 0) return WH_OK;
+    if (!fits(q, 16) || !fits(out, 16) || !fits(workspace, 256)) return WH_EINVAL;
+    a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    a.q_stride = q_stride;
+    a.group_start = group_start;
+    a.gsize = prefix && !group_start ? batch / prefix->n_set : 0;
+    a.batch = batch;
+    a.nq = n_query;
+    a.n_head = n_head;
+    a.n_kv = n_kv_head;
+    a.rep = n_head / n_kv_head;
+    a.out = reinterpret_cast<__nv_bfloat16 *>(out);
+    {
+        PaArgs sized = a;   // argument errors come before anything touches the device
+        if (ws_bytes < plan(sized).total) return WH_ENOSPC;
+    }
+    DevCtl ctl;
+    int num_sms = 0;
+    if (int rc = device_ctl(&ctl, &num_sms)) return rc;
+    a.status = ctl.status;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    trace_begin(TR_DEC_ATTN, s);
+    const int rc = launch(a, static_cast<uint8_t *>(workspace), ws_bytes, s);
+    const double pairs = (a.pre.n_set > 0 ? (double)batch * a.pre.max_keys : 0.0) +
+                         (a.own.n_set > 0 ? (double)batch * a.own.max_keys : 0.0);
+    trace_end(TR_DEC_ATTN, s, pairs * n_query * n_head * 256.0,
+              256.0 * n_kv_head * ((double)a.pre.n_set * a.pre.max_keys + (double)a.own.n_set * a.own.max_keys));
+    return rc;
+}

@@ -57,6 +57,11 @@ class wh_dec_weights(ctypes.Structure):
                 ("lnf_g", _p), ("lnf_b", _p)]
 
 
+class wh_keys(ctypes.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("row_stride", ctypes.c_int64), ("set_stride", ctypes.c_int64), ("n_keys", _p),
+                ("weight", _p), ("n_set", ctypes.c_int), ("max_keys", ctypes.c_int)]
+
+
 class wh_trace_stat(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int), ("total_ms", ctypes.c_double),
                 ("flops", ctypes.c_double), ("bytes", ctypes.c_double)]
@@ -96,6 +101,10 @@ def lib():
         "wh_decode_attention_workspace": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int]),
         "wh_decode_attention": (ctypes.c_int, [_p, _p, _p, ctypes.c_int64, ctypes.c_int64, _p, ctypes.c_int,
                                                ctypes.c_int, ctypes.c_int, _p, _p, ctypes.c_size_t, _p]),
+        "wh_prefix_attention_workspace": (ctypes.c_size_t, [ctypes.c_int] * 7),
+        "wh_prefix_attention": (ctypes.c_int, [_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                               ctypes.c_int, ctypes.POINTER(wh_keys), _p, ctypes.POINTER(wh_keys), _p,
+                                               _p, ctypes.c_size_t, _p]),
         "wh_decode_step_workspace": (ctypes.c_size_t, [ctypes.POINTER(wh_dec_config), ctypes.c_int]),
         "wh_decode_step": (ctypes.c_int, [_p, _p, ctypes.c_int, ctypes.POINTER(wh_dec_config),
                                           ctypes.POINTER(wh_dec_weights), _p, _p, _p, ctypes.c_int, _p, _p, _p,
@@ -255,6 +264,92 @@ def wh_decode_attention(q, k, v, row_stride, seq_stride, max_keys, n_head, n_key
     rc = lib().wh_decode_attention(_ptr(q), _ptr(k), _ptr(v), row_stride, seq_stride, _ptr(n_keys), max_keys, batch,
                                    n_head, _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "wh_decode_attention")
+    return out
+
+
+def _need(ok, what):
+    if not ok:
+        raise WhError(WH_EINVAL, what)
+
+
+class Keys:
+    """The keys and values of n_set sets (the C struct wh_keys) as views of torch tensors.
+
+    k, v: bf16 CUDA [n_set][max_keys][>= 64 n_kv_head], equal strides, last dimension contiguous
+    (slices of wh_prepare_cross's [K | V] rows and of a decoder's caches are fine); n_keys: int32
+    [n_set] or None (max_keys for all); weight: float32 [n_set][n_kv_head][max_keys] or None, the
+    accumulated attention weight of every key.  Holds the tensors it points to."""
+
+    def __init__(self, k, v, n_keys=None, weight=None):
+        import torch
+        _need(k.dim() == 3 and k.shape == v.shape and k.stride() == v.stride() and k.stride(2) == 1 and
+              k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16, "Keys: k, v bf16 [n_set][max_keys][d], equal strides")
+        n_set, max_keys, d = k.shape
+        dev = k.device
+        _need(dev.type == "cuda" and v.device == dev, "Keys: k and v must be on one CUDA device")
+        _need(n_keys is None or (n_keys.dtype == torch.int32 and n_keys.shape == (n_set,) and n_keys.is_contiguous() and
+                                 n_keys.device == dev), "Keys: n_keys int32 [n_set]")
+        _need(weight is None or (weight.dtype == torch.float32 and weight.dim() == 3 and weight.shape[0] == n_set and
+                                 weight.shape[2] == max_keys and weight.is_contiguous() and weight.device == dev),
+              "Keys: weight float32 [n_set][n_kv_head][max_keys]")
+        self.k, self.v, self.n_keys, self.weight, self.device = k, v, n_keys, weight, dev
+        # (the stride of a dimension of size one is never used)
+        self.c = wh_keys(k.data_ptr(), v.data_ptr(), k.stride(1) if max_keys > 1 else d, k.stride(0) if n_set > 1 else 0,
+                         None if n_keys is None else n_keys.data_ptr(), None if weight is None else weight.data_ptr(),
+                         n_set, max_keys)
+
+    def _check(self, n_kv_head, device, what):
+        _need(self.k.shape[2] >= 64 * n_kv_head, f"{what}: rows shorter than 64 n_kv_head")
+        _need(self.weight is None or self.weight.shape[1] == n_kv_head, f"{what}: weight [n_set][n_kv_head][max_keys]")
+        _need(self.device == device, f"{what}: tensors on different devices")
+
+
+def _on_device(device, stream):
+    """(context, stream handle) for a launch on `device`, whatever the current device is."""
+    import contextlib
+
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    here = torch.cuda.current_device() == device.index
+    return contextlib.nullcontext() if here else torch.cuda.device(device), ctypes.c_void_p(s.cuda_stream)
+
+
+def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_start=None, n_query=1, out=None,
+                        workspace=None, stream=None):
+    """Attention of a batch over the shared prefix of each sequence's group and over the sequence's
+    own keys.  q: bf16 [batch * n_query][64 n_head] (any row stride); prefix, own: Keys or None;
+    group_start: int32 device [prefix sets + 1] or None (equal groups in order).  Adds the attention
+    weight of every key to prefix.weight / own.weight where given.  Returns bf16
+    [batch * n_query][64 n_head]."""
+    import torch
+    what = "wh_prefix_attention"
+    _need(q.dim() == 2 and q.dtype == torch.bfloat16 and q.device.type == "cuda" and q.stride(1) == 1 and n_head >= 1 and
+          q.shape[1] >= 64 * n_head and n_query >= 1 and q.shape[0] % n_query == 0, f"{what}: q bf16 [batch * n_query][64 n_head]")
+    rows = q.shape[0]
+    batch, dev = rows // n_query, q.device
+    n_kv_head = n_head if n_kv_head is None else n_kv_head
+    for keys in (prefix, own):
+        if keys is not None:
+            keys._check(n_kv_head, dev, what)
+    _need(group_start is None or (prefix is not None and group_start.dtype == torch.int32 and group_start.device == dev and
+                                  group_start.is_contiguous() and group_start.shape == (prefix.c.n_set + 1,)),
+          f"{what}: group_start int32 [prefix sets + 1]")
+    if out is None:
+        out = torch.empty(rows, 64 * n_head, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out.dtype == torch.bfloat16 and out.shape == (rows, 64 * n_head) and out.is_contiguous() and
+              out.device == dev, f"{what}: out bf16 [batch * n_query][64 n_head]")
+    if workspace is None:
+        need = lib().wh_prefix_attention_workspace(batch, n_query, n_head, n_kv_head, prefix.c.n_set if prefix else 0,
+                                                   prefix.c.max_keys if prefix else 0, own.c.max_keys if own else 0)
+        workspace = torch.empty(max(256, need), dtype=torch.uint8, device=dev)
+    ctx, s = _on_device(dev, stream)
+    with ctx:
+        rc = lib().wh_prefix_attention(q.data_ptr(), q.stride(0) if rows > 1 else 64 * n_head, batch, n_query, n_head,
+                                       n_kv_head, ctypes.byref(prefix.c) if prefix else None, _ptr(group_start),
+                                       ctypes.byref(own.c) if own else None, out.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), s)
+    _check(rc, what)
     return out
 
 
