@@ -343,6 +343,33 @@ int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch, int n_que
                         void *workspace, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Eviction from caches by accumulated attention weight (an addition of this library).  Every head
+ * of every set of `cache` keeps, when the set holds n > budget keys, its last `recent` keys and of
+ * the others the budget - recent whose weight is largest (of equal ones those of lowest index; a
+ * NaN counts as less than every number), in their order, as keys 0 .. budget - 1; a set of
+ * n <= budget keys keeps them all.  Each head keeps its own keys, so rows of the result mix keys of
+ * different positions: the keys must carry whatever they need of their position (a decoder's
+ * stored positions are added before the projections).  The accumulators move with their keys.
+ *   cache   weight must not be NULL; the accumulators are wh_prefix_attention's
+ *   out     where the kept keys, values and weights go (n_set as cache's, max_keys >= min(budget,
+ *           cache->max_keys), weight not NULL, memory apart from cache's; its n_keys is not read),
+ *           or NULL: within the cache.  Rows at and past the new count are left as they were.
+ *   n_out   device int32 [n_set]: the new counts, min(n, budget); may be cache->n_keys
+ *   kept    device int32 [n_set][n_kv_head][budget] or NULL: the former index of every key that
+ *           stays; entries past the new count are left as they were
+ *   0 <= recent <= budget, 1 <= budget <= 2^30; within a wh_keys no two sets and no keys and values
+ *   may overlap (sets one after the other or side by side in a row; [K | V] rows are fine).
+ *   workspace >= wh_cache_evict_workspace(n_set, n_kv_head, budget) bytes, 256-byte aligned, contents
+ *           need not be initialised; not shared by concurrent calls.
+ * A count outside 0 .. max_keys is clamped and recorded as WH_EBOUNDS.  All layers' caches
+ * [n_layer][batch][...] are n_layer * batch sets of one call.
+ * Errors: WH_EINVAL, WH_ENOSPC, WH_ECUDA.
+ * ------------------------------------------------------------------------------------ */
+size_t wh_cache_evict_workspace(int n_set, int n_kv_head, int budget);
+int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, int recent, const wh_keys *out, int *n_out,
+                   int *kept, void *workspace, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------
  * One decoder step for a batch of sequences ("whisper 0.9.0 API", model.nu, wh_decode_step:
  * token tok at position pos, everything before it already in the KV cache, the logits left
  * on the device; wk_addv_row adds the stored position row; setrow writes the token's key and

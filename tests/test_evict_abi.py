@@ -1,0 +1,74 @@
+"""wh_cache_evict rejects bad arguments on the host before it touches a device (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+from whisper_audio_encoder_gb300 import build, wh
+
+FAKE, P = ctypes.c_void_p(1 << 30), 1 << 30          # never dereferenced
+ROWS = 3 * 100 * 128                                  # elements of the caches below
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return wh.lib()
+
+
+def _keys(at=P, **kw):
+    base = dict(k=at, v=at + 2 * ROWS, row_stride=128, set_stride=12800, n_keys=None, weight=at + 4 * ROWS, n_set=3,
+                max_keys=100)
+    base.update(kw)
+    return wh.wh_keys(*[base[f] for f, _ in wh.wh_keys._fields_])
+
+
+def _call(L, cache=None, n_kv=2, budget=40, recent=8, out=None, n_out=FAKE, kept=None, ws=FAKE, ws_bytes=1 << 40):
+    return L.wh_cache_evict(None if cache is None else ctypes.byref(cache), n_kv, budget, recent,
+                            None if out is None else ctypes.byref(out), n_out, kept, ws, ws_bytes, None)
+
+
+def test_rejects_bad_arguments(L):
+    bad = [dict(budget=0), dict(budget=-1), dict(recent=-1), dict(recent=41), dict(n_kv=0), dict(n_kv=3), dict(n_out=None),
+           dict(n_out=ctypes.c_void_p(P + 1)), dict(kept=ctypes.c_void_p(P + 2)), dict(ws=None), dict(ws=ctypes.c_void_p(P + 16))]
+    for kw in bad:
+        assert _call(L, _keys(), **kw) == wh.WH_EINVAL, kw
+    assert _call(L) == wh.WH_EINVAL
+    for kw in (dict(k=None), dict(v=None), dict(weight=None), dict(k=P + 8), dict(n_keys=P + 1), dict(n_set=0),
+               dict(n_set=65536), dict(max_keys=0), dict(row_stride=120), dict(row_stride=132), dict(set_stride=-8),
+               dict(set_stride=12801)):
+        assert _call(L, _keys(**kw)) == wh.WH_EINVAL, kw
+
+
+def test_rejects_what_shares_memory(L):
+    assert _call(L, _keys(set_stride=0)) == wh.WH_EINVAL              # sets on top of each other
+    assert _call(L, _keys(set_stride=12800 - 128)) == wh.WH_EINVAL
+    assert _call(L, _keys(v=P)) == wh.WH_EINVAL                       # keys and values the same memory
+    assert _call(L, _keys(v=P + 2 * 64)) == wh.WH_EINVAL              # or a head apart
+    far = P + (1 << 24)
+    assert _call(L, _keys(), out=_keys(at=far, n_set=2)) == wh.WH_EINVAL
+    assert _call(L, _keys(), out=_keys(at=far, max_keys=39)) == wh.WH_EINVAL
+    assert _call(L, _keys(), out=_keys(at=far, weight=None)) == wh.WH_EINVAL
+    assert _call(L, _keys(), out=_keys()) == wh.WH_EINVAL             # the cache itself: out = NULL says that
+    assert _call(L, _keys(), out=_keys(at=far, k=P + 256)) == wh.WH_EINVAL
+    assert _call(L, _keys(), out=_keys(at=far, weight=P + 4 * ROWS)) == wh.WH_EINVAL
+
+
+def test_workspace(L):
+    need = L.wh_cache_evict_workspace(3, 2, 40)
+    assert need >= 3 * 4 + 3 * 2 * 40 * 4
+    assert _call(L, _keys(), ws_bytes=need - 1) == wh.WH_ENOSPC
+    for args in ((0, 2, 40), (3, 0, 40), (3, 2, 0)):
+        assert L.wh_cache_evict_workspace(*args) == 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device path")
+def test_layouts_that_are_fine(L):
+    far = P + (1 << 24)
+    fine = [_keys(), _keys(v=P + 2 * 128, row_stride=256, set_stride=25600),          # [K | V] rows
+            _keys(row_stride=384, set_stride=128, v=P + 2 * 3 * 384 * 100),           # sets side by side in a row
+            _keys(n_set=1, set_stride=0)]
+    for keys in fine:
+        assert _call(L, keys) == wh.WH_ENODEV
+    assert _call(L, _keys(), out=_keys(at=far, max_keys=40)) == wh.WH_ENODEV
+    assert _call(L, _keys(max_keys=30), budget=40, out=_keys(at=far, max_keys=30)) == wh.WH_ENODEV

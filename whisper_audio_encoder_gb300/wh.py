@@ -105,6 +105,9 @@ def lib():
         "wh_prefix_attention": (ctypes.c_int, [_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                ctypes.c_int, ctypes.POINTER(wh_keys), _p, ctypes.POINTER(wh_keys), _p,
                                                _p, ctypes.c_size_t, _p]),
+        "wh_cache_evict_workspace": (ctypes.c_size_t, [ctypes.c_int] * 3),
+        "wh_cache_evict": (ctypes.c_int, [ctypes.POINTER(wh_keys), ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                          ctypes.POINTER(wh_keys), _p, _p, _p, ctypes.c_size_t, _p]),
         "wh_decode_step_workspace": (ctypes.c_size_t, [ctypes.POINTER(wh_dec_config), ctypes.c_int]),
         "wh_decode_step": (ctypes.c_int, [_p, _p, ctypes.c_int, ctypes.POINTER(wh_dec_config),
                                           ctypes.POINTER(wh_dec_weights), _p, _p, _p, ctypes.c_int, _p, _p, _p,
@@ -351,6 +354,35 @@ def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_
                                        workspace.numel() * workspace.element_size(), s)
     _check(rc, what)
     return out
+
+
+def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, workspace=None, stream=None):
+    """Cuts every head of every set of `cache` (Keys with weight) to `budget` keys: the last `recent`
+    and the older ones of largest accumulated weight, in order.  They go to `out` (Keys with weight)
+    or, without one, to the front of the cache itself.  kept: optional int32
+    [n_set][n_kv_head][budget], the former index of every key that stays.  Returns the new counts:
+    out.n_keys or cache.n_keys, updated, or a new int32 [n_set] where that is None."""
+    import torch
+    what = "wh_cache_evict"
+    to = cache if out is None else out
+    dev, n_set = cache.device, cache.c.n_set
+    for keys in (cache, to):
+        keys._check(n_kv_head, dev, what)
+        _need(keys.weight is not None, f"{what}: Keys without weight")
+    _need(budget >= 1, f"{what}: budget >= 1")
+    _need(kept is None or (kept.dtype == torch.int32 and kept.shape == (n_set, n_kv_head, budget) and kept.is_contiguous()
+                           and kept.device == dev), f"{what}: kept int32 [n_set][n_kv_head][budget]")
+    n_out = to.n_keys if to.n_keys is not None else torch.empty(n_set, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(256, lib().wh_cache_evict_workspace(n_set, n_kv_head, budget)), dtype=torch.uint8,
+                                device=dev)
+    ctx, s = _on_device(dev, stream)
+    with ctx:
+        rc = lib().wh_cache_evict(ctypes.byref(cache.c), n_kv_head, budget, recent,
+                                  None if out is None else ctypes.byref(out.c), n_out.data_ptr(), _ptr(kept),
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    _check(rc, what)
+    return n_out
 
 
 def wh_status(stream=None) -> int:
