@@ -98,6 +98,9 @@ int cast_bf16_launch(const float *x, long long n, void *y, cudaStream_t s);
 int pack_conv_weight_launch(const void *w, int c_out, int c_in, void *wp, cudaStream_t s);
 int selftest_timeout_launch(const DevCtl &ctl, cudaStream_t s);
 
+// ---- attention over shared prefixes (prefix_attention.cu) ----------------------------------
+int prefix_attention_prepare();   // once per device: shared-memory attributes
+
 // ---- decoder step (decode_step.cu) ---------------------------------------------------------
 int dec_gemm_prepare();   // once per device: shared-memory attributes of the step's GEMMs
 

@@ -14,6 +14,10 @@ namespace {
 constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = 32 * PA_WARPS;
 constexpr int PA_KEYS = 16;        // keys of one warp step
+constexpr int PA_STAGES = 4;       // warp steps in flight
+constexpr int PA_STEP_BYTES = 2 * PA_KEYS * 128;                     // keys and values of one warp step
+constexpr int PA_RING = PA_STAGES * PA_STEP_BYTES;                   // of one warp
+constexpr int PA_SMEM = PA_WARPS * PA_RING;
 constexpr int PM_ROWS = 8;         // rows of one merge block (16 threads a row)
 constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
 constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp
@@ -99,6 +103,21 @@ __device__ __forceinline__ uint32_t to_tf32(float x) {
     return r;
 }
 
+// 16 bytes global -> shared, the last 16 - bytes of them zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
 // The rows of one work item: queries of sequences first .. (rows / (nq rep)), row r =
 // ((sequence, query), query head of the key head).
 struct Rows {
@@ -142,7 +161,7 @@ __device__ __forceinline__ void score8(const uint32_t (&a)[4][4], const uint4 &k
 }
 
 template <int RT>
-__global__ void __launch_bounds__(PA_THREADS) k_prefix_attention(const PaArgs p) {
+__global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs p) {
     constexpr int TR = 16 * RT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();                // what runs after this kernel's trigger may count on its inputs
@@ -221,34 +240,51 @@ __global__ void __launch_bounds__(PA_THREADS) k_prefix_attention(const PaArgs p)
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
     }
-    const __nv_bfloat16 *kb = ks.k + (long long)set * ks.set_stride + rw.hk * 64 + 8 * c;
-    const __nv_bfloat16 *vb = ks.v + (long long)set * ks.set_stride + rw.hk * 64 + 8 * g;
-
-    // keys t + g, t + 8 + g for the scores; values t + 2c, t + 2c + 1, t + 8 + 2c, t + 9 + 2c; zeros past the range
-    auto load = [&](int t, uint4 (&kr)[2][2], uint4 (&vr)[2][2]) {
+    // Each warp copies its steps of 16 keys and values into a ring of its own, PA_STAGES - 1 ahead: four rows
+    // of 128 bytes an instruction, zeros past the range.  The 16-byte pieces of a row are permuted (keys: by
+    // the row's lowest bit, values: by the next two) so that the fragment reads below meet no bank twice.
+    extern __shared__ __align__(128) uint8_t ring_all[];
+    const uint32_t ring = smem_u32(ring_all) + warp * PA_RING;
+    const int crow = lane >> 3, piece = lane & 7;
+    const __nv_bfloat16 *kb = ks.k + (long long)set * ks.set_stride + rw.hk * 64 + 8 * piece;
+    const __nv_bfloat16 *vb = ks.v + (long long)set * ks.set_stride + rw.hk * 64 + 8 * piece;
+    auto fetch = [&](int t, int slot) {
+        if (t < k1) {
+            const uint32_t dk = ring + slot * PA_STEP_BYTES, dv = dk + PA_KEYS * 128;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int tk = t + 8 * j + g;
-            kr[j][0] = kr[j][1] = make_uint4(0, 0, 0, 0);
-            if (tk < k1) {
-                const uint4 *s = reinterpret_cast<const uint4 *>(kb + (long long)tk * ks.row_stride);
-                kr[j][0] = __ldg(s);
-                kr[j][1] = __ldg(s + 4);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int tv = t + 8 * j + 2 * c + i;
-                vr[j][i] = make_uint4(0, 0, 0, 0);
-                if (tv < k1) vr[j][i] = __ldg(reinterpret_cast<const uint4 *>(vb + (long long)tv * ks.row_stride));
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * i + crow;
+                const long long at = (long long)min(t + r, k1 - 1) * ks.row_stride;
+                const uint32_t bytes = t + r < k1 ? 16u : 0u;
+                cp_async16(dk + r * 128 + ((piece ^ ((r & 1) << 2)) << 4), kb + at, bytes);
+                cp_async16(dv + r * 128 + ((piece ^ (r & 6)) << 4), vb + at, bytes);
             }
         }
+        cp_async_commit();
     };
-    uint4 kr[2][2], vr[2][2];
-    int t0 = k0 + warp * PA_KEYS;
-    load(t0, kr, vr);
-    for (; t0 < k1; t0 += PA_WARPS * PA_KEYS) {
-        uint4 kn[2][2], vn[2][2];
-        load(t0 + PA_WARPS * PA_KEYS, kn, vn);
+    constexpr int STRIDE = PA_WARPS * PA_KEYS;
+    int t0 = k0 + warp * PA_KEYS, slot = 0;
+#pragma unroll
+    for (int i = 0; i < PA_STAGES - 1; ++i) fetch(t0 + i * STRIDE, i);
+    for (; t0 < k1; t0 += STRIDE) {
+        cp_async_wait<PA_STAGES - 2>();
+        __syncwarp();   // every lane's copies of this step have landed, and every lane is done with the last one
+        fetch(t0 + (PA_STAGES - 1) * STRIDE, slot == 0 ? PA_STAGES - 1 : slot - 1);
+        // keys g, 8 + g for the scores; values 2c, 2c + 1, 8 + 2c, 9 + 2c
+        const uint32_t sk = ring + slot * PA_STEP_BYTES, sv = sk + PA_KEYS * 128;
+        uint4 kr[2][2], vr[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t kk = sk + (8 * j + g) * 128;
+            kr[j][0] = lds128(kk + ((c ^ ((g & 1) << 2)) << 4));
+            kr[j][1] = lds128(kk + (((c + 4) ^ ((g & 1) << 2)) << 4));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * j + 2 * c + i;
+                vr[j][i] = lds128(sv + r * 128 + ((g ^ (r & 6)) << 4));
+            }
+        }
+        slot = slot == PA_STAGES - 1 ? 0 : slot + 1;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             float s[2][4];
@@ -307,18 +343,13 @@ __global__ void __launch_bounds__(PA_THREADS) k_prefix_attention(const PaArgs p)
                 }
             }
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                kr[j][i] = kn[j][i];
-                vr[j][i] = vn[j][i];
-            }
     }
 
     // ---- merge the warps ----
-    __shared__ float so[PA_WARPS][TR][68];
+    __syncthreads();   // the rings are done with (no copy is in flight: the last groups were empty)
+    auto *so = reinterpret_cast<float(*)[TR][68]>(ring_all);
     __shared__ float2 sml[PA_WARPS][TR];
+    static_assert(sizeof(float) * PA_WARPS * TR * 68 <= PA_SMEM, "the merge's rows fit in the rings");
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -504,13 +535,13 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
 
 size_t up256p(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Key ranges of a set: as many as fill the device (4 blocks on each of GB300's 152 SMs), none shorter
+// Key ranges of a set: as many as are resident at once (3 blocks on each of GB300's 152 SMs), none shorter
 // than 64 keys.
-constexpr long long PA_BLOCKS = 4 * 152;
+constexpr long long PA_BLOCKS = 3 * 152;
 void split_keys(PaSet &s, long long items) {
     s.splits = s.chunk = 0;
     if (s.n_set <= 0) return;
-    long long n = (PA_BLOCKS + items - 1) / items;
+    long long n = PA_BLOCKS / items;
     const long long most = (s.max_keys + 63) / 64;
     n = n < 1 ? 1 : (n > most ? most : n);
     s.chunk = (int)(((s.max_keys + n - 1) / n + 63) / 64 * 64);
@@ -582,9 +613,9 @@ int launch(PaArgs &a, uint8_t *ws, size_t ws_bytes, cudaStream_t s) {
     const long long rows = (long long)a.batch * a.nq * a.n_head;
     if (blocks > 0x7fffffffLL) return WH_EINVAL;
     if (pl.rt == 1)
-        k_prefix_attention<1><<<(unsigned)blocks, PA_THREADS, 0, s>>>(a);
+        k_prefix_attention<1><<<(unsigned)blocks, PA_THREADS, PA_SMEM, s>>>(a);
     else
-        k_prefix_attention<2><<<(unsigned)blocks, PA_THREADS, 0, s>>>(a);
+        k_prefix_attention<2><<<(unsigned)blocks, PA_THREADS, PA_SMEM, s>>>(a);
     count_launch();
     if (cudaGetLastError() != cudaSuccess) return WH_ECUDA;
     cudaLaunchConfig_t lc = {};
@@ -612,6 +643,15 @@ int launch(PaArgs &a, uint8_t *ws, size_t ws_bytes, cudaStream_t s) {
 }
 
 }  // namespace
+
+int prefix_attention_prepare() {
+    return cudaFuncSetAttribute(k_prefix_attention<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM) == cudaSuccess &&
+                   cudaFuncSetAttribute(k_prefix_attention<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM) ==
+                       cudaSuccess
+               ? WH_OK
+               : WH_ECUDA;
+}
+
 }  // namespace wh
 
 using namespace wh;

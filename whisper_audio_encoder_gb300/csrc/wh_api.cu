@@ -60,6 +60,7 @@ int ensure_device(DevState **out) {
         if (int rc = attention_prepare()) return rc;
         if (int rc = resample_prepare()) return rc;
         if (int rc = dec_gemm_prepare()) return rc;
+        if (int rc = prefix_attention_prepare()) return rc;
         st.status = static_cast<int *>(p);
         st.ready = true;
     }
