@@ -2,9 +2,10 @@
 
 Tolerances, counted from the roundings:
 - out: its bf16 rounding, 2^-8 |ref|; the softmax weights enter the value product with 11 bits of
-  mantissa (half a step: 2^-11) and fp32 scores, an error of at most (2^-11 + 2^-12) sum p |v|: a score
-  of 64 products in fp32 is off by at most 64 2^-24 sum |q k| / 8 < 2^-13.5 for the inputs here
-  (sum |q k| < 180), and so is the maximum's part.
+  mantissa (half a step: 2^-11) where a prefix has at most 16 rows (queries x query heads of a key head)
+  on average, with 8 bits (half a step: 2^-8) where it has more, an error of at most that times
+  sum p |v|; and fp32 scores, 2^-12 sum p |v|: a score of 64 products in fp32 is off by at most
+  64 2^-24 sum |q k| / 8 < 2^-13.5 for the inputs here (sum |q k| < 180), and so is the maximum's part.
 - weights: each weight is off by twice the score's error (its own and the sum's), 2^-12.5, plus the
   exponential's 2^-22, relative; sums of up to 400 rows add 400 2^-24 < 2^-15.
 """
@@ -24,6 +25,10 @@ def _lib():
         pytest.skip("needs a GPU")
     build.build()
     wh.lib()
+
+
+def out_tol(ref, spread, rows_a_prefix=0):
+    return 2.0 ** -8 * np.abs(ref) + ((2.0 ** -8 if rows_a_prefix > 16 else 2.0 ** -11) + 2.0 ** -12) * spread
 
 
 def _bf(rng, *shape):
@@ -87,7 +92,8 @@ class Case:
         ref, spread, wp, wo = R.prefix_attention(self.q, self.nq, self.H, self.KV, self.pre or [], self.group_of(),
                                                  self.own or [None] * self.B)
         got = out.float().cpu().numpy()
-        bad = ~(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * spread)
+        rows = -(-self.B * self.nq * (self.H // self.KV) // len(self.pre)) if self.pre else 0
+        bad = ~(np.abs(got - ref) <= out_tol(ref, spread, rows))
         assert not bad.any(), f"{bad.sum()} of {bad.size} outside; worst {np.nanmax(np.abs(got - ref)):.3e}"
         for what, ws, keys in (("pre", wp, self.pk), ("own", wo, self.ok)):
             if what not in self.w0:
@@ -118,6 +124,11 @@ CASES = {
                                          weigh=True),
     "queries that see nothing": dict(n_head=4, n_kv=2, nq=5, n_own=[0, 1, 3, 5, 9], cap_own=20, weigh=True),
     "queries that see only the prefix": dict(n_head=2, n_kv=2, nq=3, groups=[2], n_pre=[7], n_own=[0, 1]),
+    "32 rows, ranges": dict(n_head=2, n_kv=2, nq=1, groups=[32], n_pre=[9001], weigh=True),
+    "64 rows": dict(n_head=2, n_kv=2, nq=1, groups=[64, 64, 61], n_pre=[128, 127, 129], cap_pre=131),
+    "65 rows, short prefixes": dict(n_head=3, n_kv=3, nq=1, groups=[65, 65, 65, 65], n_pre=[0, 1, 2, 300], n_own=[i % 3 for i in range(260)]),
+    "128 rows, ranges": dict(n_head=4, n_kv=2, nq=2, groups=[32], n_pre=[5003], n_own=[2] * 32, weigh=True),
+    "300 and 3 rows": dict(n_head=2, n_kv=2, nq=1, groups=[300, 3], n_pre=[1000, 515], weigh=True),
     "many queries": dict(n_head=2, n_kv=1, nq=41, groups=[1, 2], n_pre=[50, 77], n_own=[41, 43, 100], weigh=True),
     "wide group": dict(n_head=2, n_kv=1, nq=1, groups=[201], n_pre=[333], n_own=[i % 7 for i in range(201)], weigh=True),
 }
@@ -145,10 +156,11 @@ def test_sequences_outside_every_group_have_no_prefix():
     assert torch.all(out[[1, 6]] == 0)                # no prefix, no keys
 
 
-def test_prepare_cross_rows_and_strided_queries():
+@pytest.mark.parametrize("beams", [4, 20, 40])
+def test_prepare_cross_rows_and_strided_queries(beams):
     """[K | V] rows of wh_prepare_cross, one set per window, and queries inside wider rows."""
     rng = np.random.default_rng(5)
-    H, d, n_ctx, beams = 6, 384, 77, 4
+    H, d, n_ctx = 6, 384, 77
     kv = _bf(rng, 3, n_ctx, 2 * d)
     wide = _dev(_bf(rng, 3 * beams, 3 * d))
     q = wide[:, d:2 * d]
@@ -156,29 +168,50 @@ def test_prepare_cross_rows_and_strided_queries():
     out = wh.wh_prefix_attention(q, H, prefix=wh.Keys(kvd[..., :d], kvd[..., d:]))
     ref, spread, _, _ = R.prefix_attention(q.float().cpu().numpy(), 1, H, H, [(x[:, :d], x[:, d:]) for x in kv],
                                            [b // beams for b in range(3 * beams)], [None] * 3 * beams)
-    assert np.all(np.abs(out.float().cpu().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * spread)
+    assert np.all(np.abs(out.float().cpu().numpy() - ref) <= out_tol(ref, spread, beams))
 
 
-def test_offsets_past_32_bits():
+@pytest.mark.parametrize("beams", [3, 20])
+@pytest.mark.parametrize("layout", ["one set for all groups", "sets beside each other", "odd set stride"])
+def test_set_strides(layout, beams):
+    rng = np.random.default_rng(15)
+    H, d, n, sets = 2, 128, 200, 3
+    if layout == "one set for all groups":
+        k, v = (_dev(_bf(rng, 1, n, d)).expand(sets, n, d) for _ in range(2))
+    elif layout == "sets beside each other":
+        k, v = (_dev(_bf(rng, n, sets, d)).transpose(0, 1) for _ in range(2))
+    else:
+        k, v = (_dev(_bf(rng, sets * (n * d + 8))).as_strided((sets, n, d), (n * d + 8, d, 1)) for _ in range(2))
+    q = _bf(rng, sets * beams, d)
+    out = wh.wh_prefix_attention(_dev(q), H, prefix=wh.Keys(k, v))
+    host = lambda x: x.float().cpu().numpy()  # noqa: E731
+    ref, spread, _, _ = R.prefix_attention(q, 1, H, H, list(zip(host(k), host(v))), [b // beams for b in range(sets * beams)],
+                                           [None] * sets * beams)
+    assert np.all(np.abs(host(out) - ref) <= out_tol(ref, spread, beams))
+
+
+@pytest.mark.parametrize("beams", [3, 20])
+def test_offsets_past_32_bits(beams):
     rng = np.random.default_rng(6)
     n, stride = 130, 1 << 25                             # the last key starts 4.3e9 elements in
     if torch.cuda.mem_get_info()[0] < 3 * n * stride * 2:
         pytest.skip("needs 18 GB of device memory")
-    k, v, q = _bf(rng, n, 128), _bf(rng, n, 128), _bf(rng, 3, 128)
+    k, v, q = _bf(rng, n, 128), _bf(rng, n, 128), _bf(rng, beams, 128)
     big = torch.empty(n * stride, dtype=torch.bfloat16, device="cuda").as_strided((1, n, 256), (0, stride, 1))
     big[0, :, :128], big[0, :, 128:] = _dev(k), _dev(v)
     out = wh.wh_prefix_attention(_dev(q), 2, prefix=wh.Keys(big[..., :128], big[..., 128:]))
-    ref, spread, _, _ = R.prefix_attention(q, 1, 2, 2, [(k, v)], [0] * 3, [None] * 3)
-    assert np.all(np.abs(out.float().cpu().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * spread)
+    ref, spread, _, _ = R.prefix_attention(q, 1, 2, 2, [(k, v)], [0] * beams, [None] * beams)
+    assert np.all(np.abs(out.float().cpu().numpy() - ref) <= out_tol(ref, spread, beams))
 
 
-def test_same_bits_again_with_a_dirty_workspace_on_another_stream():
-    kw = dict(n_head=4, n_kv=2, nq=3, groups=[5, 9, 2], n_pre=[700, 64, 3], n_own=[i + 3 for i in range(16)], weigh=True)
+@pytest.mark.parametrize("nq", [1, 3, 17])
+def test_same_bits_again_with_a_dirty_workspace_on_another_stream(nq):
+    kw = dict(n_head=4, n_kv=2, nq=nq, groups=[5, 9, 2], n_pre=[700, 64, 3], n_own=[i + 3 for i in range(16)], weigh=True)
     a = Case(7, **kw)
     x = a.run()
     wp, wo = a.pk.weight.clone(), a.ok.weight.clone()
     b = Case(7, **kw)
-    need = wh.lib().wh_prefix_attention_workspace(16, 3, 4, 2, 3, 700, 18)
+    need = wh.lib().wh_prefix_attention_workspace(16, nq, 4, 2, 3, 700, 18)
     ws = torch.full((need // 4,), float("nan"), device="cuda")
     torch.cuda.synchronize()
     s = torch.cuda.Stream()

@@ -735,6 +735,19 @@ int make_tmap(CUtensorMap *m, CUtensorMapDataType dt, int esize, const void *ptr
 int make_tmap_bf16(CUtensorMap *m, const void *ptr, long long rows, int cols, int ld, int box_rows) {
     return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, rows, cols, ld, 64, box_rows);
 }
+// 3-D bf16 tensor map: cols x rows x sets (strides row_ld and set_ld elements), box 64 x box_rows x 1, as above.
+int make_tmap_bf16_sets(CUtensorMap *m, const void *ptr, int cols, long long rows, long long row_ld, long long sets,
+                        long long set_ld, int box_rows) {
+    if (int rc = tmap_encoder_ready()) return rc;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)sets};
+    cuuint64_t strides[2] = {(cuuint64_t)row_ld * 2, (cuuint64_t)set_ld * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, 1u};
+    cuuint32_t es[3] = {1u, 1u, 1u};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? WH_OK : WH_EINVAL;
+}
 int make_tmap_f32(CUtensorMap *m, const void *ptr, long long rows, int cols, int ld, int box_rows) {
     return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ptr, rows, cols, ld, 32, box_rows);
 }

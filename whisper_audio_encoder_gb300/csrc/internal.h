@@ -47,6 +47,9 @@ inline size_t gemm_sk_ticket_bytes(long long M, int N) { return (size_t)gemm_sk_
 // 2-D bf16 TMA descriptor: rows x cols (row stride ld elements), box 64 x box_rows, 128-byte
 // swizzle, zero fill outside.  Returns a WH_* code.
 int make_tmap_bf16(CUtensorMap *m, const void *ptr, long long rows, int cols, int ld, int box_rows);
+// The same over `sets` matrices set_ld elements apart (box 64 x box_rows x 1).
+int make_tmap_bf16_sets(CUtensorMap *m, const void *ptr, int cols, long long rows, long long row_ld, long long sets,
+                        long long set_ld, int box_rows);
 // The same for fp32 with a 32-column (128-byte) box.
 int make_tmap_f32(CUtensorMap *m, const void *ptr, long long rows, int cols, int ld, int box_rows);
 

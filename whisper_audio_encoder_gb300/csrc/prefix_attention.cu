@@ -5,14 +5,14 @@
 //   s_t = q . k_t / 8,   p = softmax(s),   o = sum_t p_t v_t,   weight[t] += sum over the queries of p_t
 // A prefix key and value are read once for all the queries of the group (all sequences, queries and
 // query heads of its key head are the rows of one matrix product), not once per sequence.
-#include "common.cuh"
-#include "internal.h"
+#include "prefix_attention.cuh"
 
 namespace wh {
 namespace {
 
 constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = 32 * PA_WARPS;
+constexpr int PA_TILE = 16;        // rows of a block
 constexpr int PA_KEYS = 16;        // keys of one warp step
 constexpr int PA_STAGES = 4;       // warp steps in flight
 constexpr int PA_STEP_BYTES = 2 * PA_KEYS * 128;                     // keys and values of one warp step
@@ -21,68 +21,6 @@ constexpr int PA_SMEM = PA_WARPS * PA_RING;
 constexpr int PM_ROWS = 8;         // rows of one merge block (16 threads a row)
 constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
 constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp
-constexpr float PA_SCALE = 0.125f * 1.4426950408889634f;   // log2(e) / sqrt(64): scores in the exp2 domain
-
-struct PaSet {
-    const __nv_bfloat16 *k, *v;
-    long long row_stride, set_stride;   // elements
-    const int *n_keys;                  // device [n_set] or null (max_keys for all)
-    float *weight;                      // device [n_set][n_kv][max_keys] or null
-    int n_set, max_keys;
-    int splits, chunk;                  // key ranges of one set and keys of a range
-};
-
-struct PaArgs {
-    PaSet pre, own;
-    const __nv_bfloat16 *q;
-    long long q_stride;
-    const int *group_start;   // device [pre.n_set + 1] or null: gsize sequences each
-    int gsize, batch, nq, n_head, n_kv, rep;
-    int slots;                // prefix: row-tile slots of a key head over all groups
-    int own_tiles;            // row tiles of a sequence
-    long long pre_blocks;     // blocks [0, pre_blocks) take prefix work, the rest own keys
-    float *part_o;            // [row][pre.splits + own.splits][64], row = (b nq + i) n_head + h
-    float2 *part_ml;          // [row][pre.splits + own.splits]: running maximum and sum
-    float2 *stats;            // [row]: maximum and 1 / sum (weights only)
-    __nv_bfloat16 *out;       // [batch * nq][64 n_head]
-    int direct;               // one range covers everything a row sees: write out, no merge
-    int *status;
-};
-
-__device__ __forceinline__ int clamp_count(const PaSet &s, int set) {
-    return s.n_keys ? min(max(__ldg(s.n_keys + set), 0), s.max_keys) : s.max_keys;
-}
-
-// Largest g in [0, n) with start[g] * mul / div + g * add <= x, by the whole warp, 32 probes at a time.
-__device__ __forceinline__ int warp_search(const int *start, int n, int mul, int div, int add, long long x) {
-    int lo = 0, len = n;
-    const int lane = threadIdx.x & 31;
-    while (len > 1) {
-        const int step = (len + 31) / 32, i = lane * step;
-        bool le = false;
-        if (i < len) {
-            const int g = lo + i;
-            le = (long long)__ldg(start + g) * mul / div + (long long)g * add <= x;
-        }
-        const uint32_t m = __ballot_sync(0xffffffffu, le) | 1u;
-        const int top = (31 - __clz(m)) * step;
-        lo += top;
-        len = min(step, len - top);
-    }
-    return lo;
-}
-
-// Sequences [s, e) of group g, cut to 0 .. batch.
-__device__ __forceinline__ void group_range(const PaArgs &p, int g, int &s, int &e) {
-    if (p.group_start) {
-        s = min(max(__ldg(p.group_start + g), 0), p.batch);
-        e = min(max(__ldg(p.group_start + g + 1), s), p.batch);
-    } else {
-        s = g * p.gsize;
-        e = s + p.gsize;
-    }
-}
-
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -118,18 +56,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     return v;
 }
 
-// The rows of one work item: queries of sequences first .. (rows / (nq rep)), row r =
-// ((sequence, query), query head of the key head).
-struct Rows {
-    int seq0, n, hk;
-    __device__ __forceinline__ void locate(const PaArgs &p, int r, int &qrow, int &head, int &qi) const {
-        const int per = p.nq * p.rep, s = r / per, w = r - s * per;
-        qi = w / p.rep;
-        qrow = (seq0 + s) * p.nq + qi;
-        head = hk * p.rep + (w - qi * p.rep);
-    }
-};
-
 // Query fragments of rows r0 + g and r0 + g + 8 (g = lane / 4).  The 64 dims of a head are spread over the
 // four lanes of a row as 8c .. 8c+7 and 32+8c .. 32+8c+7 (c = lane % 4), so that a lane's 16-byte loads of a
 // key are its part of four MMA steps; the sum over dims does not mind the order.
@@ -160,11 +86,11 @@ __device__ __forceinline__ void score8(const uint32_t (&a)[4][4], const uint4 &k
     mma_bf16(s, a[3][0], a[3][1], a[3][2], a[3][3], k1.z, k1.w);
 }
 
-template <int RT>
 __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs p) {
-    constexpr int TR = 16 * RT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    pdl_wait();                // what runs after this kernel's trigger may count on its inputs
+    // What runs after this kernel's trigger may count on its inputs.  Beside k_prefix_tc, which waited for
+    // them, it only makes sure that that kernel has ended before it does itself.
+    if (!p.beside_tc) pdl_wait();
     pdl_launch_dependents();
     // ---- which rows, which keys ----
     const bool is_pre = blockIdx.x < p.pre_blocks;
@@ -176,26 +102,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         x /= p.slots;
         rw.hk = x % p.n_kv;
         split = x / p.n_kv;
-        const int per = p.nq * p.rep;
-        int s, e;
-        if (p.group_start) {
-            if (rw.hk == 0 && split == 0 && slot < p.pre.n_set && threadIdx.x == 0) {   // report bad groups once
-                const int a = __ldg(p.group_start + slot), b = __ldg(p.group_start + slot + 1);
-                if (a < 0 || b < a || b > p.batch) atomicCAS(p.status, 0, WH_EBOUNDS);
-            }
-            // group g's tiles take slots start[g] per / TR + g and up: they end before group g + 1's
-            set = warp_search(p.group_start, p.pre.n_set, per, TR, 1, slot);
-            group_range(p, set, s, e);
-            r0 = (slot - (int)((long long)s * per / TR) - set) * TR;
-        } else {
-            const int tiles = (p.gsize * per + TR - 1) / TR;
-            set = slot / tiles;
-            group_range(p, set, s, e);
-            r0 = (slot - set * tiles) * TR;
-        }
-        rw.seq0 = s;
-        rw.n = (e - s) * per;
-        if (r0 < 0 || r0 >= rw.n) return;
+        if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw)) return;
     } else {
         long long x = blockIdx.x - p.pre_blocks;
         const int tile = x % p.own_tiles;
@@ -206,40 +113,33 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         set = x / p.own.splits;
         rw.seq0 = set;
         rw.n = p.nq * p.rep;
-        r0 = tile * TR;
+        r0 = tile * PA_TILE;
     }
     const PaSet &ks = is_pre ? p.pre : p.own;
     const int nk = clamp_count(ks, set);
     if (ks.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && threadIdx.x == 0 && __ldg(ks.n_keys + set) != nk)
-        atomicCAS(p.status, 0, WH_EBOUNDS);
+        set_status(p.ctl, WH_EBOUNDS);
     const int k0 = split * ks.chunk, k1 = min(nk, k0 + ks.chunk);
-    if (k0 >= k1 && !p.direct) return;   // nothing here: the merge knows
+    if (k0 >= k1 && !p.direct) {   // nothing here: the merge knows
+        if (p.beside_tc) pdl_wait();
+        return;
+    }
 
-    uint32_t qa[RT][4][4];
-    int lim[RT][2];   // own keys: the first key that a row does not see
+    uint32_t qa[4][4];
+    int lim[2];   // own keys: the first key that a row does not see
+    load_q(p, rw, r0, qa);
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        load_q(p, rw, r0 + 16 * t, qa[t]);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            lim[t][half] = nk;
-            if (!is_pre) {
-                int qrow, head, qi;
-                rw.locate(p, min(r0 + 16 * t + g + 8 * half, rw.n - 1), qrow, head, qi);
-                lim[t][half] = nk - (p.nq - 1 - qi);
-            }
+    for (int half = 0; half < 2; ++half) {
+        lim[half] = nk;
+        if (!is_pre) {
+            int qrow, head, qi;
+            rw.locate(p, min(r0 + g + 8 * half, rw.n - 1), qrow, head, qi);
+            lim[half] = nk - (p.nq - 1 - qi);
         }
     }
     const int full = is_pre ? nk : nk - (p.nq - 1);   // every row sees the keys before this one
 
-    float m[RT][2], l[RT][2], o[RT][8][4];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        m[t][0] = m[t][1] = -INFINITY;
-        l[t][0] = l[t][1] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
-    }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, o[8][4] = {};
     // Each warp copies its steps of 16 keys and values into a ring of its own, PA_STAGES - 1 ahead: four rows
     // of 128 bytes an instruction, zeros past the range.  The 16-byte pieces of a row are permuted (keys: by
     // the row's lowest bit, values: by the next two) so that the fragment reads below meet no bank twice.
@@ -285,93 +185,88 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
             }
         }
         slot = slot == PA_STAGES - 1 ? 0 : slot + 1;
+        float s[2][4];
+        score8(qa, kr[0][0], kr[0][1], s[0]);
+        score8(qa, kr[1][0], kr[1][1], s[1]);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            float s[2][4];
-            score8(qa[t], kr[0][0], kr[0][1], s[0]);
-            score8(qa[t], kr[1][0], kr[1][1], s[1]);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][i] *= PA_SCALE;
+        if (t0 + PA_KEYS > min(k1, full)) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[j][i] *= PA_SCALE;
-            if (t0 + PA_KEYS > min(k1, full)) {
+                for (int i = 0; i < 4; ++i) {
+                    const int key = t0 + 8 * j + 2 * c + (i & 1);
+                    if (key >= min(k1, lim[i >> 1])) s[j][i] = -INFINITY;
+                }
+        }
+        float mx[2], mn[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = t0 + 8 * j + 2 * c + (i & 1);
-                        if (key >= min(k1, lim[t][i >> 1])) s[j][i] = -INFINITY;
-                    }
-            }
-            float mx[2], mn[2];
+        for (int half = 0; half < 2; ++half) {
+            mx[half] = fmaxf(fmaxf(s[0][2 * half], s[0][2 * half + 1]), fmaxf(s[1][2 * half], s[1][2 * half + 1]));
+            mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
+            mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
+            mn[half] = fmaxf(m[half], mx[half]);
+        }
+        if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {   // some row's maximum moved
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                mx[half] = fmaxf(fmaxf(s[0][2 * half], s[0][2 * half + 1]), fmaxf(s[1][2 * half], s[1][2 * half + 1]));
-                mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
-                mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
-                mn[half] = fmaxf(m[t][half], mx[half]);
+                const float f = m[half] == -INFINITY ? 0.0f : ex2_approx(m[half] - mn[half]);
+                l[half] *= f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    o[j][2 * half] *= f;
+                    o[j][2 * half + 1] *= f;
+                }
+                m[half] = mn[half];
             }
-            if (__any_sync(0xffffffffu, mn[0] > m[t][0] || mn[1] > m[t][1])) {   // some row's maximum moved
+        }
+        const float ms[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const float f = m[t][half] == -INFINITY ? 0.0f : ex2_approx(m[t][half] - mn[half]);
-                    l[t][half] *= f;
+        for (int j = 0; j < 2; ++j) {
+            uint32_t pt[4];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        o[t][j][2 * half] *= f;
-                        o[t][j][2 * half + 1] *= f;
-                    }
-                    m[t][half] = mn[half];
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float e = ex2_approx(s[j][i] - ms[i >> 1]);
+                l[i >> 1] += e;
+                pt[i] = to_tf32(e);   // 11 bits of mantissa: an eighth of the output's rounding
             }
-            const float ms[2] = {m[t][0] == -INFINITY ? 0.0f : m[t][0], m[t][1] == -INFINITY ? 0.0f : m[t][1]};
+            const uint32_t a0[4] = {vr[j][0].x, vr[j][0].y, vr[j][0].z, vr[j][0].w};
+            const uint32_t a1[4] = {vr[j][1].x, vr[j][1].y, vr[j][1].z, vr[j][1].w};
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t pt[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = ex2_approx(s[j][i] - ms[i >> 1]);
-                    l[t][i >> 1] += e;
-                    pt[i] = to_tf32(e);   // 11 bits of mantissa: an eighth of the output's rounding
-                }
-                const uint32_t a0[4] = {vr[j][0].x, vr[j][0].y, vr[j][0].z, vr[j][0].w};
-                const uint32_t a1[4] = {vr[j][1].x, vr[j][1].y, vr[j][1].z, vr[j][1].w};
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    mma_tf32(o[t][2 * w], pt[0], pt[2], pt[1], pt[3], a0[w] << 16, a1[w] << 16);
-                    mma_tf32(o[t][2 * w + 1], pt[0], pt[2], pt[1], pt[3], a0[w] & 0xffff0000u, a1[w] & 0xffff0000u);
-                }
+            for (int w = 0; w < 4; ++w) {
+                mma_tf32(o[2 * w], pt[0], pt[2], pt[1], pt[3], a0[w] << 16, a1[w] << 16);
+                mma_tf32(o[2 * w + 1], pt[0], pt[2], pt[1], pt[3], a0[w] & 0xffff0000u, a1[w] & 0xffff0000u);
             }
         }
     }
 
     // ---- merge the warps ----
     __syncthreads();   // the rings are done with (no copy is in flight: the last groups were empty)
-    auto *so = reinterpret_cast<float(*)[TR][68]>(ring_all);
-    __shared__ float2 sml[PA_WARPS][TR];
-    static_assert(sizeof(float) * PA_WARPS * TR * 68 <= PA_SMEM, "the merge's rows fit in the rings");
+    auto *so = reinterpret_cast<float(*)[PA_TILE][68]>(ring_all);
+    __shared__ float2 sml[PA_WARPS][PA_TILE];
+    static_assert(sizeof(float) * PA_WARPS * PA_TILE * 68 <= PA_SMEM, "the merge's rows fit in the rings");
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int half = 0; half < 2; ++half) {
+        float ls = l[half];
+        ls += __shfl_xor_sync(0xffffffffu, ls, 1);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+        const int r = g + 8 * half;
+        if (c == 0) sml[warp][r] = make_float2(m[half], ls);
+        // dims 16c + j (first column of n-tile j) and 16c + 8 + j (second)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float ls = l[t][half];
-            ls += __shfl_xor_sync(0xffffffffu, ls, 1);
-            ls += __shfl_xor_sync(0xffffffffu, ls, 2);
-            const int r = 16 * t + g + 8 * half;
-            if (c == 0) sml[warp][r] = make_float2(m[t][half], ls);
-            // dims 16c + j (first column of n-tile j) and 16c + 8 + j (second)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float *d = &so[warp][r][16 * c + 8 * i];
-                *reinterpret_cast<float4 *>(d) = make_float4(o[t][0][2 * half + i], o[t][1][2 * half + i],
-                                                             o[t][2][2 * half + i], o[t][3][2 * half + i]);
-                *reinterpret_cast<float4 *>(d + 4) = make_float4(o[t][4][2 * half + i], o[t][5][2 * half + i],
-                                                                 o[t][6][2 * half + i], o[t][7][2 * half + i]);
-            }
+        for (int i = 0; i < 2; ++i) {
+            float *d = &so[warp][r][16 * c + 8 * i];
+            *reinterpret_cast<float4 *>(d) = make_float4(o[0][2 * half + i], o[1][2 * half + i],
+                                                         o[2][2 * half + i], o[3][2 * half + i]);
+            *reinterpret_cast<float4 *>(d + 4) = make_float4(o[4][2 * half + i], o[5][2 * half + i],
+                                                             o[6][2 * half + i], o[7][2 * half + i]);
         }
+    }
     __syncthreads();
-    const int ns = p.pre.splits + p.own.splits, part = is_pre ? split : p.pre.splits + split;
-    for (int i = threadIdx.x; i < TR * 8; i += PA_THREADS) {
+    const int part = is_pre ? split : p.pre.splits + split;
+    for (int i = threadIdx.x; i < PA_TILE * 8; i += PA_THREADS) {
         const int r = i >> 3, d0 = 8 * (i & 7);
         if (r0 + r >= rw.n) break;
         float mt = -INFINITY;
@@ -388,22 +283,9 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
             v[0] = fmaf(x.x, f, v[0]), v[1] = fmaf(x.y, f, v[1]), v[2] = fmaf(x.z, f, v[2]), v[3] = fmaf(x.w, f, v[3]);
             v[4] = fmaf(y.x, f, v[4]), v[5] = fmaf(y.y, f, v[5]), v[6] = fmaf(y.z, f, v[6]), v[7] = fmaf(y.w, f, v[7]);
         }
-        int qrow, head, qi;
-        rw.locate(p, r0 + r, qrow, head, qi);
-        const long long row = (long long)qrow * p.n_head + head;
-        if (p.direct) {
-            const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;   // a query that sees no key: zeros
-            *reinterpret_cast<uint4 *>(p.out + row * 64 + d0) =
-                make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
-                           pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
-            if (p.stats && d0 == 0) p.stats[row] = make_float2(mt == -INFINITY ? 0.0f : mt, inv);
-        } else {
-            float4 *d = reinterpret_cast<float4 *>(p.part_o + (row * ns + part) * 64 + d0);
-            d[0] = make_float4(v[0], v[1], v[2], v[3]);
-            d[1] = make_float4(v[4], v[5], v[6], v[7]);
-            if (d0 == 0) p.part_ml[row * ns + part] = make_float2(mt, lt);
-        }
+        finish_row(p, rw, r0 + r, part, d0, mt, lt, v);
     }
+    if (p.beside_tc) pdl_wait();
 }
 
 // o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the ranges of a row that hold keys, in order.
@@ -535,37 +417,42 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
 
 size_t up256p(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Key ranges of a set: as many as are resident at once (3 blocks on each of GB300's 152 SMs), none shorter
-// than 64 keys.
-constexpr long long PA_BLOCKS = 3 * 152;
-void split_keys(PaSet &s, long long items) {
+// Key ranges of a set: as many as are resident at once, in whole steps of a block.
+constexpr long long PA_BLOCKS = 3 * 152;   // k_prefix_attention: 3 blocks on each of GB300's 152 SMs
+constexpr long long PT_BLOCKS = 2 * 152;   // k_prefix_tc: 2 on each
+constexpr int PT_MIN_ROWS = 16;
+void split_keys(PaSet &s, long long items, long long blocks, int step) {
     s.splits = s.chunk = 0;
     if (s.n_set <= 0) return;
-    long long n = PA_BLOCKS / items;
-    const long long most = (s.max_keys + 63) / 64;
+    long long n = blocks / items;
+    const long long most = (s.max_keys + step - 1) / step;
     n = n < 1 ? 1 : (n > most ? most : n);
-    s.chunk = (int)(((s.max_keys + n - 1) / n + 63) / 64 * 64);
+    s.chunk = (int)(((s.max_keys + n - 1) / n + step - 1) / step * step);
     s.splits = (s.max_keys + s.chunk - 1) / s.chunk;
 }
 
 struct PaPlan {
-    int rt;
+    bool tc;   // the prefix part runs on the tcgen05 kernel
     size_t part_o, part_ml, stats, total;
 };
 
 // Row tiles, key ranges and the workspace's layout, from host-known sizes only.
-PaPlan plan(PaArgs &a) {
+PaPlan plan(PaArgs &a, bool may_tc) {
     PaPlan pl;
     const long long per = (long long)a.nq * a.rep, all = a.batch * per;
-    const long long rows_a_set = a.pre.n_set > 0 ? (all + a.pre.n_set - 1) / a.pre.n_set : per;
-    pl.rt = rows_a_set > 16 ? 2 : 1;
-    const int tr = 16 * pl.rt;
+    const long long rows_a_set = a.pre.n_set > 0 ? (all + a.pre.n_set - 1) / a.pre.n_set : 0;
+    pl.tc = may_tc && rows_a_set > PT_MIN_ROWS;
+    a.tile = !pl.tc ? PA_TILE : rows_a_set > 64 ? 128 : rows_a_set > 32 ? 64 : 32;
     a.slots = 0;
     if (a.pre.n_set > 0)
-        a.slots = (int)(a.gsize == 0 ? a.pre.n_set + all / tr : a.pre.n_set * ((a.gsize * per + tr - 1) / tr));
-    a.own_tiles = (int)((per + tr - 1) / tr);
-    split_keys(a.pre, (long long)a.slots * a.n_kv);
-    split_keys(a.own, (long long)a.own.n_set * a.n_kv * a.own_tiles);
+        a.slots = (int)(a.gsize == 0 ? a.pre.n_set + all / a.tile
+                                     : a.pre.n_set * ((a.gsize * per + a.tile - 1) / a.tile));
+    a.own_tiles = (int)((per + PA_TILE - 1) / PA_TILE);
+    if (pl.tc)
+        split_keys(a.pre, (long long)a.slots * a.n_kv, PT_BLOCKS, PT_KEYS);
+    else
+        split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, PA_WARPS * PA_KEYS);
+    split_keys(a.own, (long long)a.own.n_set * a.n_kv * a.own_tiles, PA_BLOCKS, PA_WARPS * PA_KEYS);
     const size_t rows = (size_t)a.batch * a.nq * a.n_head, ns = (size_t)a.pre.splits + a.own.splits;
     a.direct = ns == 1 && (a.pre.n_set == 0 || a.gsize > 0);
     size_t off = 0;
@@ -602,29 +489,35 @@ bool shape_ok(int batch, int n_query, int n_head, int n_kv) {
            n_kv >= 1 && n_head % n_kv == 0 && (long long)batch * n_query * n_head <= 0x7fffffffLL;
 }
 
-int launch(PaArgs &a, uint8_t *ws, size_t ws_bytes, cudaStream_t s) {
-    const PaPlan pl = plan(a);
-    if (ws_bytes < pl.total) return WH_ENOSPC;
+int launch(PaArgs &a, const PaPlan &pl, const PtMaps &maps, uint8_t *ws, cudaStream_t s) {
     a.part_o = reinterpret_cast<float *>(ws + pl.part_o);
     a.part_ml = reinterpret_cast<float2 *>(ws + pl.part_ml);
     a.stats = a.pre.weight || a.own.weight ? reinterpret_cast<float2 *>(ws + pl.stats) : nullptr;
-    a.pre_blocks = (long long)a.slots * a.n_kv * a.pre.splits;
-    const long long blocks = a.pre_blocks + (long long)a.own_tiles * a.n_kv * a.own.splits * a.own.n_set;
+    const long long pre_blocks = (long long)a.slots * a.n_kv * a.pre.splits;
+    const long long own_blocks = (long long)a.own_tiles * a.n_kv * a.own.splits * a.own.n_set;
     const long long rows = (long long)a.batch * a.nq * a.n_head;
-    if (blocks > 0x7fffffffLL) return WH_EINVAL;
-    if (pl.rt == 1)
-        k_prefix_attention<1><<<(unsigned)blocks, PA_THREADS, PA_SMEM, s>>>(a);
-    else
-        k_prefix_attention<2><<<(unsigned)blocks, PA_THREADS, PA_SMEM, s>>>(a);
-    count_launch();
-    if (cudaGetLastError() != cudaSuccess) return WH_ECUDA;
+    if (pre_blocks + own_blocks > 0x7fffffffLL) return WH_EINVAL;
     cudaLaunchConfig_t lc = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
-    lc.numAttrs = 1;
     lc.stream = s;
+    if (pl.tc && pre_blocks > 0) {
+        if (int rc = prefix_tc_launch(a, maps, s)) return rc;
+        a.beside_tc = 1;
+        lc.numAttrs = 1;   // own keys beside the prefix blocks' last ones
+    }
+    a.pre_blocks = pl.tc ? 0 : pre_blocks;
+    if (a.pre_blocks + own_blocks > 0) {
+        lc.gridDim = dim3((unsigned)(a.pre_blocks + own_blocks));
+        lc.blockDim = dim3(PA_THREADS);
+        lc.dynamicSmemBytes = PA_SMEM;
+        if (cudaLaunchKernelEx(&lc, k_prefix_attention, a) != cudaSuccess) return WH_ECUDA;
+        count_launch();
+        lc.dynamicSmemBytes = 0;
+    }
+    lc.numAttrs = 1;
     if (!a.direct) {
         lc.gridDim = dim3((unsigned)((rows + PM_ROWS - 1) / PM_ROWS));
         lc.blockDim = dim3(16 * PM_ROWS);
@@ -645,11 +538,9 @@ int launch(PaArgs &a, uint8_t *ws, size_t ws_bytes, cudaStream_t s) {
 }  // namespace
 
 int prefix_attention_prepare() {
-    return cudaFuncSetAttribute(k_prefix_attention<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM) == cudaSuccess &&
-                   cudaFuncSetAttribute(k_prefix_attention<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM) ==
-                       cudaSuccess
-               ? WH_OK
-               : WH_ECUDA;
+    if (cudaFuncSetAttribute(k_prefix_attention, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM) != cudaSuccess)
+        return WH_ECUDA;
+    return prefix_tc_prepare();
 }
 
 }  // namespace wh
@@ -671,10 +562,12 @@ extern "C" size_t wh_prefix_attention_workspace(int batch, int n_query, int n_he
     a.pre.max_keys = max_prefix;
     a.own.n_set = max_own > 0 ? batch : 0;
     a.own.max_keys = max_own;
-    size_t most = plan(a).total;   // groups of any size
-    if (a.pre.n_set > 0 && batch % a.pre.n_set == 0) {
-        a.gsize = batch / a.pre.n_set;
-        const size_t t = plan(a).total;
+    // the largest of: groups of any size or equal ones, the prefix part on either kernel
+    size_t most = 0;
+    const bool equal = a.pre.n_set > 0 && batch % a.pre.n_set == 0;
+    for (int i = 0; i < (equal ? 4 : 2); ++i) {
+        a.gsize = i < 2 ? 0 : batch / a.pre.n_set;
+        const size_t t = plan(a, i & 1).total;
         most = t > most ? t : most;
     }
     return most;
@@ -703,17 +596,20 @@ extern "C" int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch
     a.n_kv = n_kv_head;
     a.rep = n_head / n_kv_head;
     a.out = reinterpret_cast<__nv_bfloat16 *>(out);
-    {
-        PaArgs sized = a;   // argument errors come before anything touches the device
-        if (ws_bytes < plan(sized).total) return WH_ENOSPC;
-    }
+    PaPlan pl = plan(a, true);
+    if (ws_bytes < pl.total) return WH_ENOSPC;
     DevCtl ctl;
     int num_sms = 0;
     if (int rc = device_ctl(&ctl, &num_sms)) return rc;
-    a.status = ctl.status;
+    a.ctl = ctl;
+    PtMaps maps;
+    if (pl.tc && prefix_tc_maps(a, &maps) != WH_OK) {   // strides that a tensor map cannot hold
+        pl = plan(a, false);
+        if (ws_bytes < pl.total) return WH_ENOSPC;
+    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     trace_begin(TR_DEC_ATTN, s);
-    const int rc = launch(a, static_cast<uint8_t *>(workspace), ws_bytes, s);
+    const int rc = launch(a, pl, maps, static_cast<uint8_t *>(workspace), s);
     const double pairs = (a.pre.n_set > 0 ? (double)batch * a.pre.max_keys : 0.0) +
                          (a.own.n_set > 0 ? (double)batch * a.own.max_keys : 0.0);
     trace_end(TR_DEC_ATTN, s, pairs * n_query * n_head * 256.0,

@@ -1,0 +1,382 @@
+// The shared-prefix part of wh_prefix_attention on the tcgen05 tensor cores, for groups of many rows.
+//
+// A block takes up to 128 rows (queries of a group's sequences and of a key head's query heads) and a range
+// of the prefix's keys, in steps of 128 keys:
+//   S = Q K^T      tcgen05.mma M = 128, N = 128, K = 64 into TMEM, Q and the TMA-loaded K in shared memory
+//   P = 2^(S - m)  one row a thread: read from TMEM, running maximum and sum, bf16 pairs back into TMEM
+//   O += P V       tcgen05.mma M = 128, N = 64, K = 128, P from TMEM, V as loaded (MN-major), O in TMEM
+// With 32 or 64 rows the matrix product's 128 lanes hold 4 or 2 copies of them, each taking a quarter or
+// half of the keys' columns (its P is zero elsewhere): the exponentials, not the padded products, are what
+// takes time, and so none is spent on padding.  The copies are merged at the end like key ranges.
+// O is rescaled only when a row's maximum has grown by more than 2^8.
+// P is rounded to bf16 because both operands of the product have one type: half a step is 2^-9 of a weight
+// or less, as much as the output's own rounding, and averages out over the keys.
+//
+// Warp 0 loads (TMA), warp 1 issues the products, warps 2 .. 5 are the rows' (warp w reads the TMEM lanes
+// 32 (w % 4) and up).  Two blocks are resident on an SM, so one's softmax runs beside the other's products.
+// Every wait is bounded; when one runs out the block records WH_ETIMEOUT and winds down.
+#include "prefix_attention.cuh"
+
+namespace wh {
+namespace {
+
+constexpr int PT_THREADS = 192, PT_STAGES = 3;
+constexpr int TILE_BYTES = 128 * 128;                       // 128 rows of 64 bf16
+constexpr int OFF_RING = TILE_BYTES;                        // Q first
+constexpr int OFF_BARS = OFF_RING + PT_STAGES * 2 * TILE_BYTES;
+constexpr int PT_SMEM = OFF_BARS + 1024;                    // two blocks fill an SM's shared memory
+constexpr uint32_t PT_COLS = 256;                           // S [0, 128), O [128, 192), P [192, 256)
+constexpr int SO_ROW = 68;                                  // floats a row of the epilogue's staging
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// V as the MN-major operand: rows = keys (the K dimension), one 128-byte swizzle atom of 64 dims along N,
+// 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(1024 >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+__device__ __forceinline__ void rows_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <int COPIES>
+__global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_constant__ PtMaps tm, const PaArgs p) {
+    constexpr int TILE = 128 / COPIES, COLS = 128 / COPIES;   // rows of the block, columns a thread takes
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *sQ = smem, *sKV = smem + OFF_RING;   // stage s: K at s * 32 KB, V 16 KB behind it
+    uint64_t *kv_full = reinterpret_cast<uint64_t *>(smem + OFF_BARS);
+    uint64_t *kv_empty = kv_full + PT_STAGES;
+    uint64_t *s_full = kv_empty + PT_STAGES;
+    uint64_t *s_free = s_full + 1;
+    uint64_t *p_full = s_free + 1;
+    uint64_t *o_full = p_full + 1;
+    uint64_t *drain = o_full + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();   // what runs after this kernel's trigger may count on its inputs
+    pdl_launch_dependents();
+    Rows rw;
+    int set, r0;
+    const int slot = blockIdx.x % p.slots;
+    rw.hk = (blockIdx.x / p.slots) % p.n_kv;
+    const int split = blockIdx.x / p.slots / p.n_kv;
+    if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw)) return;
+    const int nk = clamp_count(p.pre, set);
+    if (p.pre.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && threadIdx.x == 0 && __ldg(p.pre.n_keys + set) != nk)
+        set_status(p.ctl, WH_EBOUNDS);
+    const int k0 = split * p.pre.chunk, k1 = min(nk, k0 + p.pre.chunk);
+    const int a = threadIdx.x - 64;   // the row warps' TMEM lane is 32 (warp % 4) + lane
+    if (k0 >= k1) {                   // no keys: zeros if this is all there is, else the merge knows
+        if (p.direct) {
+            const float none[8] = {};
+            for (int i = threadIdx.x; i < TILE * 8; i += PT_THREADS)
+                if (r0 + (i >> 3) < rw.n) finish_row(p, rw, r0 + (i >> 3), split, 8 * (i & 7), -INFINITY, 0.0f, none);
+        }
+        return;
+    }
+    if ((smem_u32(smem) & 1023u) != 0) {   // the swizzled tiles must lie on 1024-byte boundaries
+        if (threadIdx.x == 0) set_status(p.ctl, WH_EBOUNDS);
+        return;
+    }
+    const int nt = (k1 - k0 + PT_KEYS - 1) / PT_KEYS;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < PT_STAGES; ++s) {
+            mbar_init(kv_full + s, 1);
+            mbar_init(kv_empty + s, 1);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(s_free, 4);
+        mbar_init(p_full, 4);
+        mbar_init(o_full, 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm.k);
+        tma_prefetch_desc(&tm.v);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, PT_COLS);
+        tmem_relinquish();
+    }
+    if (warp >= 2) {
+        // matrix row a holds row a % TILE, 128-byte swizzled as the products read it
+        const int r = r0 + (a % TILE);
+        uint4 u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = make_uint4(0, 0, 0, 0);
+        if (r < rw.n) {
+            int qrow, head, qi;
+            rw.locate(p, r, qrow, head, qi);
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (long long)qrow * p.q_stride + head * 64);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = __ldg(src + i);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(sQ + a * 128 + ((i ^ (a & 7)) << 4)) = u[i];
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t issued = 0, last_parity = 0;
+            const int z = tm.one_set ? 0 : set;
+            for (int j = 0; j < nt; ++j) {
+                const int s = j % PT_STAGES;
+                const uint32_t ph = (j / PT_STAGES) & 1u;
+                if (*abort_flag || !mbar_wait(kv_empty + s, ph ^ 1u, p.ctl)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                uint8_t *kb = sKV + s * 2 * TILE_BYTES;
+                mbar_arrive_expect_tx(kv_full + s, 2 * TILE_BYTES);
+                tma_load_3d(kb, &tm.k, kv_full + s, rw.hk * 64, k0 + j * PT_KEYS, z);
+                tma_load_3d(kb + TILE_BYTES, &tm.v, kv_full + s, rw.hk * 64, k0 + j * PT_KEYS, z);
+                issued |= 1u << s;
+                last_parity = (last_parity & ~(1u << s)) | (ph << s);
+            }
+            // no copy of this block may still be in flight when it exits
+            for (int s = 0; s < PT_STAGES; ++s)
+                if ((issued >> s) & 1u) mbar_wait(kv_full + s, (last_parity >> s) & 1u, p.ctl);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t IDESC_S = idesc_bf16_f32(128, PT_KEYS);
+            constexpr uint32_t IDESC_O = idesc_bf16_f32(128, 64) | (1u << 16);   // V is MN-major
+            const uint32_t skv = smem_u32(sKV);
+            const uint64_t qd = sdesc_sw128(smem_u32(sQ));
+            auto issue_s = [&](int s) {
+                const uint64_t kd = sdesc_sw128(skv + s * 2 * TILE_BYTES);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16(tmem, qd + (uint64_t)(2 * kk), kd + (uint64_t)(2 * kk), IDESC_S, kk != 0);
+                umma_commit(s_full);
+            };
+            bool ok = !*abort_flag && mbar_wait(kv_full, 0, p.ctl);
+            if (ok) {
+                tc_fence_after();
+                issue_s(0);
+            }
+            for (int j = 0; ok && j < nt; ++j) {
+                if (j + 1 < nt) {   // the next scores as soon as this step's have been read
+                    ok = !*abort_flag && mbar_wait(kv_full + (j + 1) % PT_STAGES, ((j + 1) / PT_STAGES) & 1u, p.ctl) &&
+                         mbar_wait(s_free, j & 1u, p.ctl);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s((j + 1) % PT_STAGES);
+                }
+                ok = !*abort_flag && mbar_wait(p_full, j & 1u, p.ctl);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t vb = skv + (j % PT_STAGES) * 2 * TILE_BYTES + TILE_BYTES;
+#pragma unroll
+                for (int kk = 0; kk < PT_KEYS / 16; ++kk)
+                    umma_bf16_tmem_a(tmem + 128u, tmem + 192u + 8u * kk, sdesc_sw128_mn(vb + kk * 2048), IDESC_O,
+                                     (j | kk) != 0);
+                umma_commit(o_full);
+                umma_commit(kv_empty + j % PT_STAGES);
+            }
+            if (!ok) *abort_flag = 1;
+            umma_commit(drain);
+            mbar_wait(drain, 0, p.ctl);
+        }
+    } else {
+        const int q = warp & 3, at = 32 * q + lane;      // TMEM lane = matrix row
+        const int col0 = (at / TILE) * COLS;              // the columns of this copy
+        const uint32_t lanes = (uint32_t)(32 * q) << 16;
+        const uint32_t tS = tmem + lanes + (uint32_t)col0, tO = tmem + lanes + 128u, tP = tmem + lanes + 192u;
+        if (COPIES > 1) {   // the other copies' columns of P stay zero
+            const uint32_t zero[32] = {};
+            tmem_st32(tP, zero);
+            tmem_st32(tP + 32u, zero);
+            tmem_wait_st();
+        }
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < nt; ++j) {
+            ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(s_full, j & 1u, p.ctl));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t sv[COLS / 32][32];
+#pragma unroll
+            for (int i = 0; i < COLS / 32; ++i) tmem_ld32(tS + 32u * i, sv[i]);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_free);   // S may now be overwritten
+            const int valid = k1 - k0 - j * PT_KEYS;   // keys of this step inside the range
+            if (valid < PT_KEYS) {
+#pragma unroll
+                for (int i = 0; i < COLS / 32; ++i)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (col0 + 32 * i + k >= valid) sv[i][k] = 0xff800000u;   // -inf
+                // values past the range may be anything, NaN too, and 0 * NaN is NaN: clear them
+                ok = __all_sync(0xffffffffu, mbar_wait(kv_full + j % PT_STAGES, (j / PT_STAGES) & 1u, p.ctl));
+                if (!ok) break;
+                if (a >= valid) {
+                    uint4 *row = reinterpret_cast<uint4 *>(sKV + (j % PT_STAGES) * 2 * TILE_BYTES + TILE_BYTES + a * 128);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            float pm[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pm[k] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < COLS / 32; ++i)
+#pragma unroll
+                for (int k = 0; k < 32; k += 2)
+                    pm[(k >> 1) & 3] = max3(pm[(k >> 1) & 3], __uint_as_float(sv[i][k]), __uint_as_float(sv[i][k + 1]));
+            const float m_new = fmaxf(m, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));
+            if (j == 0) {
+                m = m_new;
+            } else {
+                // the product of the step before is done: O is stable and P may be overwritten
+                ok = __all_sync(0xffffffffu, mbar_wait(o_full, (j - 1) & 1u, p.ctl));
+                if (!ok) break;
+                tc_fence_after();
+                const bool need = (m_new - m) * PA_SCALE > 8.0f;
+                if (__any_sync(0xffffffffu, need)) {
+                    float f = 1.0f;
+                    if (need) {
+                        f = ex2_approx((m - m_new) * PA_SCALE);
+                        l *= f;
+                        m = m_new;
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t v[32];
+                        tmem_ld32(tO + 32u * half, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                        tmem_st32(tO + 32u * half, v);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            const float mc = m == -INFINITY ? 0.0f : m * PA_SCALE;
+            const uint64_t scale2 = f2_pack(PA_SCALE, PA_SCALE), minus2 = f2_pack(-mc, -mc);
+            uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+            for (int i = 0; i < COLS / 32; ++i) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float x0, x1;
+                    f2_unpack(fma_f2(f2_pack(__uint_as_float(sv[i][2 * k]), __uint_as_float(sv[i][2 * k + 1])), scale2, minus2),
+                              x0, x1);
+                    const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+                    sum2[k & 1] = add_f2(sum2[k & 1], f2_pack(e0, e1));
+                    pk[k] = pack_bf16(e0, e1);
+                }
+                tmem_st16(tP + (uint32_t)(col0 / 2 + 16 * i), pk);
+            }
+            float x0, x1;
+            f2_unpack(add_f2(sum2[0], sum2[1]), x0, x1);
+            l += x0 + x1;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full);
+        }
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full, (nt - 1) & 1u, p.ctl));
+        if (!ok) *abort_flag = 1;
+        tc_fence_after();
+        // every product is done, so the ring is free: stage O, merge the copies, write whole rows
+        float *so = reinterpret_cast<float *>(sKV);
+        float2 *sml = reinterpret_cast<float2 *>(sKV + 128 * SO_ROW * 4);
+        if (ok) {
+            sml[at] = make_float2(m == -INFINITY ? m : m * PA_SCALE, l);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t v[32];
+                tmem_ld32(tO + 32u * half, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4 *>(so + at * SO_ROW + 32 * half + 4 * i) =
+                        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+        }
+        rows_bar();
+        if (!*abort_flag) {
+            for (int i = a; i < TILE * 8; i += 128) {
+                const int r = i >> 3, d0 = 8 * (i & 7);
+                if (r0 + r >= rw.n) break;
+                float mt = -INFINITY, lt = 0.0f, v[8] = {};
+#pragma unroll
+                for (int c = 0; c < COPIES; ++c) mt = fmaxf(mt, sml[r + TILE * c].x);
+#pragma unroll
+                for (int c = 0; c < COPIES; ++c) {
+                    const float2 ml = sml[r + TILE * c];
+                    const float f = COPIES == 1 ? 1.0f : ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mt);
+                    lt = fmaf(ml.y, f, lt);
+#pragma unroll
+                    for (int k = 0; k < 8; k += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(so + (r + TILE * c) * SO_ROW + d0 + k);
+                        v[k] = fmaf(x.x, f, v[k]), v[k + 1] = fmaf(x.y, f, v[k + 1]);
+                        v[k + 2] = fmaf(x.z, f, v[k + 2]), v[k + 3] = fmaf(x.w, f, v[k + 3]);
+                    }
+                }
+                finish_row(p, rw, r0 + r, split, d0, mt, lt, v);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, PT_COLS);
+    }
+}
+
+template <int COPIES>
+int set_attr() {
+    return cudaFuncSetAttribute(k_prefix_tc<COPIES>, cudaFuncAttributeMaxDynamicSharedMemorySize, PT_SMEM) == cudaSuccess
+               ? WH_OK
+               : WH_ECUDA;
+}
+
+}  // namespace
+
+int prefix_tc_prepare() { return set_attr<1>() | set_attr<2>() | set_attr<4>(); }
+
+int prefix_tc_maps(const PaArgs &a, PtMaps *m) {
+    m->one_set = a.pre.n_set == 1 || a.pre.set_stride == 0;
+    const long long sets = m->one_set ? 1 : a.pre.n_set;
+    const long long set_ld = m->one_set ? a.pre.row_stride : a.pre.set_stride;   // (not used with one set)
+    if (int rc = make_tmap_bf16_sets(&m->k, a.pre.k, 64 * a.n_kv, a.pre.max_keys, a.pre.row_stride, sets, set_ld, PT_KEYS))
+        return rc;
+    return make_tmap_bf16_sets(&m->v, a.pre.v, 64 * a.n_kv, a.pre.max_keys, a.pre.row_stride, sets, set_ld, PT_KEYS);
+}
+
+int prefix_tc_launch(const PaArgs &a, const PtMaps &m, cudaStream_t s) {
+    const unsigned blocks = (unsigned)((long long)a.slots * a.n_kv * a.pre.splits);
+    if (a.tile == 128)
+        k_prefix_tc<1><<<blocks, PT_THREADS, PT_SMEM, s>>>(m, a);
+    else if (a.tile == 64)
+        k_prefix_tc<2><<<blocks, PT_THREADS, PT_SMEM, s>>>(m, a);
+    else
+        k_prefix_tc<4><<<blocks, PT_THREADS, PT_SMEM, s>>>(m, a);
+    count_launch();
+    return cudaGetLastError() == cudaSuccess ? WH_OK : WH_ECUDA;
+}
+
+}  // namespace wh
