@@ -12,15 +12,19 @@
 // P is rounded to bf16 because both operands of the product have one type: half a step is 2^-9 of a weight
 // or less, as much as the output's own rounding, and averages out over the keys.
 //
-// Warp 0 loads (TMA), warp 1 issues the products, warps 2 .. 5 are the rows' (warp w reads the TMEM lanes
-// 32 (w % 4) and up).  Two blocks are resident on an SM, so one's softmax runs beside the other's products.
+// Warp 0 loads (TMA), warp 1 issues the products (2 and 3 idle), warps 4 .. 7 are the rows' (warp w reads the
+// TMEM lanes 32 (w % 4) and up).  Two blocks are resident on an SM, so one's softmax runs beside the other's products.
 // Every wait is bounded; when one runs out the block records WH_ETIMEOUT and winds down.
 #include "prefix_attention.cuh"
 
 namespace wh {
 namespace {
 
-constexpr int PT_THREADS = 192, PT_STAGES = 3;
+constexpr int PT_THREADS = 256, PT_STAGES = 3;
+// Register split (setmaxnreg): two blocks of 256 threads launch at 128 a thread; the first warpgroup (loads,
+// products) drops to 40, the rows' rises to 208 and holds a row's 128 scores: 128 x (40 + 208) <= 256 x 128.
+constexpr int REG_LOW = 40, REG_HIGH = 208;
+static_assert(128 * (REG_LOW + REG_HIGH) <= PT_THREADS * 128, "register split exceeds the launch total");
 constexpr int TILE_BYTES = 128 * 128;                       // 128 rows of 64 bf16
 constexpr int OFF_RING = TILE_BYTES;                        // Q first
 constexpr int OFF_BARS = OFF_RING + PT_STAGES * 2 * TILE_BYTES;
@@ -74,7 +78,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
     if (p.pre.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && threadIdx.x == 0 && __ldg(p.pre.n_keys + set) != nk)
         set_status(p.ctl, WH_EBOUNDS);
     const int k0 = split * p.pre.chunk, k1 = min(nk, k0 + p.pre.chunk);
-    const int a = threadIdx.x - 64;   // the row warps' TMEM lane is 32 (warp % 4) + lane
+    const int a = threadIdx.x - 128;   // the rows' threads: TMEM lane and matrix row
     if (k0 >= k1) {                   // no keys: zeros if this is all there is, else the merge knows
         if (p.direct) {
             const float none[8] = {};
@@ -108,7 +112,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
         tmem_alloc(tmem_slot, PT_COLS);
         tmem_relinquish();
     }
-    if (warp >= 2) {
+    if (warp >= 4) {
         // matrix row a holds row a % TILE, 128-byte swizzled as the products read it
         const int r = r0 + (a % TILE);
         uint4 u[8];
@@ -130,7 +134,9 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 0) {
+    if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
+      if (warp == 0) {
         if (lane == 0) {
             uint32_t issued = 0, last_parity = 0;
             const int z = tm.one_set ? 0 : set;
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
             for (int s = 0; s < PT_STAGES; ++s)
                 if ((issued >> s) & 1u) mbar_wait(kv_full + s, (last_parity >> s) & 1u, p.ctl);
         }
-    } else if (warp == 1) {
+      } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t IDESC_S = idesc_bf16_f32(128, PT_KEYS);
             constexpr uint32_t IDESC_O = idesc_bf16_f32(128, 64) | (1u << 16);   // V is MN-major
@@ -193,10 +199,11 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
             umma_commit(drain);
             mbar_wait(drain, 0, p.ctl);
         }
+      }
     } else {
-        const int q = warp & 3, at = 32 * q + lane;      // TMEM lane = matrix row
-        const int col0 = (at / TILE) * COLS;              // the columns of this copy
-        const uint32_t lanes = (uint32_t)(32 * q) << 16;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HIGH));
+        const int col0 = (a / TILE) * COLS;   // the columns of this copy
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + (uint32_t)col0, tO = tmem + lanes + 128u, tP = tmem + lanes + 192u;
         if (COPIES > 1) {   // the other copies' columns of P stay zero
             const uint32_t zero[32] = {};
@@ -302,7 +309,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
         float *so = reinterpret_cast<float *>(sKV);
         float2 *sml = reinterpret_cast<float2 *>(sKV + 128 * SO_ROW * 4);
         if (ok) {
-            sml[at] = make_float2(m == -INFINITY ? m : m * PA_SCALE, l);
+            sml[a] = make_float2(m == -INFINITY ? m : m * PA_SCALE, l);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t v[32];
@@ -310,7 +317,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4 *>(so + at * SO_ROW + 32 * half + 4 * i) =
+                    *reinterpret_cast<uint4 *>(so + a * SO_ROW + 32 * half + 4 * i) =
                         make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
         }
