@@ -18,6 +18,7 @@ constexpr int PA_STAGES = 4;       // warp steps in flight
 constexpr int PA_STEP_BYTES = 2 * PA_KEYS * 128;                     // keys and values of one warp step
 constexpr int PA_RING = PA_STAGES * PA_STEP_BYTES;                   // of one warp
 constexpr int PA_SMEM = PA_WARPS * PA_RING;
+constexpr int SO_ROW = 68;         // floats a row of the warps' staged results
 constexpr int PM_ROWS = 8;         // rows of one merge block (16 threads a row)
 constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
 constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp
@@ -93,7 +94,10 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     if (!p.beside_tc) pdl_wait();
     pdl_launch_dependents();
     // ---- which rows, which keys ----
+    // A work item is done by `wpi` neighbouring warps: all four for a prefix, p.own_wpi for own keys.
     const bool is_pre = blockIdx.x < p.pre_blocks;
+    const int wpi = is_pre ? PA_WARPS : p.own_wpi, iw = warp & (wpi - 1);
+    const bool first = iw == 0 && lane == 0;
     Rows rw;
     int set, split, r0;
     if (is_pre) {
@@ -104,7 +108,11 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         split = x / p.n_kv;
         if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw)) return;
     } else {
-        long long x = blockIdx.x - p.pre_blocks;
+        long long x = (blockIdx.x - p.pre_blocks) * (PA_WARPS / wpi) + warp / wpi;
+        if (x >= p.own_items) {
+            if (p.beside_tc) pdl_wait();
+            return;
+        }
         const int tile = x % p.own_tiles;
         x /= p.own_tiles;
         rw.hk = x % p.n_kv;
@@ -117,7 +125,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     }
     const PaSet &ks = is_pre ? p.pre : p.own;
     const int nk = clamp_count(ks, set);
-    if (ks.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && threadIdx.x == 0 && __ldg(ks.n_keys + set) != nk)
+    if (ks.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && first && __ldg(ks.n_keys + set) != nk)
         set_status(p.ctl, WH_EBOUNDS);
     const int k0 = split * ks.chunk, k1 = min(nk, k0 + ks.chunk);
     if (k0 >= k1 && !p.direct) {   // nothing here: the merge knows
@@ -148,28 +156,38 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     const int crow = lane >> 3, piece = lane & 7;
     const __nv_bfloat16 *kb = ks.k + (long long)set * ks.set_stride + rw.hk * 64 + 8 * piece;
     const __nv_bfloat16 *vb = ks.v + (long long)set * ks.set_stride + rw.hk * 64 + 8 * piece;
+    const long long step4 = 4 * ks.row_stride;   // four rows on
     auto fetch = [&](int t, int slot) {
         if (t < k1) {
-            const uint32_t dk = ring + slot * PA_STEP_BYTES, dv = dk + PA_KEYS * 128;
+            const uint32_t dk = ring + slot * PA_STEP_BYTES + crow * 128 + ((piece ^ ((crow & 1) << 2)) << 4);
+            const uint32_t dv = ring + slot * PA_STEP_BYTES + PA_KEYS * 128 + crow * 128;
+            const long long at = (long long)(t + crow) * ks.row_stride;
+            const __nv_bfloat16 *k = kb + at, *v = vb + at;
+            if (t + PA_KEYS <= k1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 4 * i + crow;
-                const long long at = (long long)min(t + r, k1 - 1) * ks.row_stride;
-                const uint32_t bytes = t + r < k1 ? 16u : 0u;
-                cp_async16(dk + r * 128 + ((piece ^ ((r & 1) << 2)) << 4), kb + at, bytes);
-                cp_async16(dv + r * 128 + ((piece ^ (r & 6)) << 4), vb + at, bytes);
+                for (int i = 0; i < 4; ++i, k += step4, v += step4) {
+                    cp_async16(dk + i * 512, k, 16u);
+                    cp_async16(dv + i * 512 + ((piece ^ ((4 * i + crow) & 6)) << 4), v, 16u);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i, k += step4, v += step4) {
+                    const bool in = t + 4 * i + crow < k1;
+                    cp_async16(dk + i * 512, in ? k : kb, in ? 16u : 0u);
+                    cp_async16(dv + i * 512 + ((piece ^ ((4 * i + crow) & 6)) << 4), in ? v : vb, in ? 16u : 0u);
+                }
             }
         }
         cp_async_commit();
     };
-    constexpr int STRIDE = PA_WARPS * PA_KEYS;
-    int t0 = k0 + warp * PA_KEYS, slot = 0;
+    const int stride = wpi * PA_KEYS;
+    int t0 = k0 + iw * PA_KEYS, slot = 0;
 #pragma unroll
-    for (int i = 0; i < PA_STAGES - 1; ++i) fetch(t0 + i * STRIDE, i);
-    for (; t0 < k1; t0 += STRIDE) {
+    for (int i = 0; i < PA_STAGES - 1; ++i) fetch(t0 + i * stride, i);
+    for (; t0 < k1; t0 += stride) {
         cp_async_wait<PA_STAGES - 2>();
         __syncwarp();   // every lane's copies of this step have landed, and every lane is done with the last one
-        fetch(t0 + (PA_STAGES - 1) * STRIDE, slot == 0 ? PA_STAGES - 1 : slot - 1);
+        fetch(t0 + (PA_STAGES - 1) * stride, slot == 0 ? PA_STAGES - 1 : slot - 1);
         // keys g, 8 + g for the scores; values 2c, 2c + 1, 8 + 2c, 9 + 2c
         const uint32_t sk = ring + slot * PA_STEP_BYTES, sv = sk + PA_KEYS * 128;
         uint4 kr[2][2], vr[2][2];
@@ -242,44 +260,44 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         }
     }
 
-    // ---- merge the warps ----
-    __syncthreads();   // the rings are done with (no copy is in flight: the last groups were empty)
-    auto *so = reinterpret_cast<float(*)[PA_TILE][68]>(ring_all);
+    // ---- merge the item's warps ----
+    // (each writes over its own ring; no copy is in flight, the last groups were empty)
     __shared__ float2 sml[PA_WARPS][PA_TILE];
-    static_assert(sizeof(float) * PA_WARPS * PA_TILE * 68 <= PA_SMEM, "the merge's rows fit in the rings");
+    auto so = [&](int w, int r) { return reinterpret_cast<float *>(ring_all + w * PA_RING) + r * SO_ROW; };
+    static_assert(sizeof(float) * PA_TILE * SO_ROW <= PA_RING, "a warp's rows fit in its ring");
+    __syncwarp();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         float ls = l[half];
         ls += __shfl_xor_sync(0xffffffffu, ls, 1);
         ls += __shfl_xor_sync(0xffffffffu, ls, 2);
         const int r = g + 8 * half;
+        if (r0 + r >= rw.n) continue;
         if (c == 0) sml[warp][r] = make_float2(m[half], ls);
         // dims 16c + j (first column of n-tile j) and 16c + 8 + j (second)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float *d = &so[warp][r][16 * c + 8 * i];
-            *reinterpret_cast<float4 *>(d) = make_float4(o[0][2 * half + i], o[1][2 * half + i],
-                                                         o[2][2 * half + i], o[3][2 * half + i]);
-            *reinterpret_cast<float4 *>(d + 4) = make_float4(o[4][2 * half + i], o[5][2 * half + i],
-                                                             o[6][2 * half + i], o[7][2 * half + i]);
+            float *d = so(warp, r) + 16 * c + 8 * i;
+            *reinterpret_cast<float4 *>(d) =
+                make_float4(o[0][2 * half + i], o[1][2 * half + i], o[2][2 * half + i], o[3][2 * half + i]);
+            *reinterpret_cast<float4 *>(d + 4) =
+                make_float4(o[4][2 * half + i], o[5][2 * half + i], o[6][2 * half + i], o[7][2 * half + i]);
         }
     }
-    __syncthreads();
-    const int part = is_pre ? split : p.pre.splits + split;
-    for (int i = threadIdx.x; i < PA_TILE * 8; i += PA_THREADS) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpi), "r"(32 * wpi) : "memory");
+    const int part = is_pre ? split : p.pre.splits + split, w0 = warp - iw;
+    const int todo = 8 * min(PA_TILE, rw.n - r0);
+    for (int i = 32 * iw + lane; i < todo; i += 32 * wpi) {
         const int r = i >> 3, d0 = 8 * (i & 7);
-        if (r0 + r >= rw.n) break;
         float mt = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < PA_WARPS; ++w) mt = fmaxf(mt, sml[w][r].x);
+        for (int w = 0; w < wpi; ++w) mt = fmaxf(mt, sml[w0 + w][r].x);
         float lt = 0.0f, v[8] = {};
-#pragma unroll
-        for (int w = 0; w < PA_WARPS; ++w) {
-            const float2 ml = sml[w][r];
+        for (int w = 0; w < wpi; ++w) {
+            const float2 ml = sml[w0 + w][r];
             const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mt);
             lt = fmaf(ml.y, f, lt);
-            const float4 x = *reinterpret_cast<const float4 *>(&so[w][r][d0]);
-            const float4 y = *reinterpret_cast<const float4 *>(&so[w][r][d0 + 4]);
+            const float4 x = *reinterpret_cast<const float4 *>(so(w0 + w, r) + d0);
+            const float4 y = *reinterpret_cast<const float4 *>(so(w0 + w, r) + d0 + 4);
             v[0] = fmaf(x.x, f, v[0]), v[1] = fmaf(x.y, f, v[1]), v[2] = fmaf(x.z, f, v[2]), v[3] = fmaf(x.w, f, v[3]);
             v[4] = fmaf(y.x, f, v[4]), v[5] = fmaf(y.y, f, v[5]), v[6] = fmaf(y.z, f, v[6]), v[7] = fmaf(y.w, f, v[7]);
         }
@@ -452,7 +470,13 @@ PaPlan plan(PaArgs &a, bool may_tc) {
         split_keys(a.pre, (long long)a.slots * a.n_kv, PT_BLOCKS, PT_KEYS);
     else
         split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, PA_WARPS * PA_KEYS);
-    split_keys(a.own, (long long)a.own.n_set * a.n_kv * a.own_tiles, PA_BLOCKS, PA_WARPS * PA_KEYS);
+    // own keys: one warp an item when that fills the device, more warps, then key ranges, when it does not
+    const long long items = (long long)a.own.n_set * a.n_kv * a.own_tiles;
+    a.own_wpi = PA_WARPS;
+    while (a.own_wpi > 1 && (items * a.own_wpi > PA_BLOCKS * PA_WARPS || (a.own_wpi - 1) * PA_KEYS >= a.own.max_keys))
+        a.own_wpi /= 2;
+    split_keys(a.own, items, PA_BLOCKS * (PA_WARPS / a.own_wpi), a.own_wpi * PA_KEYS);
+    a.own_items = items * a.own.splits;
     const size_t rows = (size_t)a.batch * a.nq * a.n_head, ns = (size_t)a.pre.splits + a.own.splits;
     a.direct = ns == 1 && (a.pre.n_set == 0 || a.gsize > 0);
     size_t off = 0;
@@ -494,7 +518,7 @@ int launch(PaArgs &a, const PaPlan &pl, const PtMaps &maps, uint8_t *ws, cudaStr
     a.part_ml = reinterpret_cast<float2 *>(ws + pl.part_ml);
     a.stats = a.pre.weight || a.own.weight ? reinterpret_cast<float2 *>(ws + pl.stats) : nullptr;
     const long long pre_blocks = (long long)a.slots * a.n_kv * a.pre.splits;
-    const long long own_blocks = (long long)a.own_tiles * a.n_kv * a.own.splits * a.own.n_set;
+    const long long own_blocks = (a.own_items * a.own_wpi + PA_WARPS - 1) / PA_WARPS;
     const long long rows = (long long)a.batch * a.nq * a.n_head;
     if (pre_blocks + own_blocks > 0x7fffffffLL) return WH_EINVAL;
     cudaLaunchConfig_t lc = {};

@@ -26,6 +26,8 @@ struct PaArgs {
     int tile;                 // prefix: rows of a row tile
     int slots;                // prefix: row-tile slots of a key head over all groups
     int own_tiles;            // row tiles of a sequence
+    int own_wpi;              // own keys: warps of a work item
+    long long own_items;      // own keys: (sequence, range, key head, row tile)
     long long pre_blocks;     // blocks [0, pre_blocks) take prefix work, the rest own keys
     float *part_o;            // [row][pre.splits + own.splits][64], row = (b nq + i) n_head + h
     float2 *part_ml;          // [row][pre.splits + own.splits]: running maximum and sum
