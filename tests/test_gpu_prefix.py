@@ -129,6 +129,11 @@ CASES = {
     "65 rows, short prefixes": dict(n_head=3, n_kv=3, nq=1, groups=[65, 65, 65, 65], n_pre=[0, 1, 2, 300], n_own=[i % 3 for i in range(260)]),
     "128 rows, ranges": dict(n_head=4, n_kv=2, nq=2, groups=[32], n_pre=[5003], n_own=[2] * 32, weigh=True),
     "300 and 3 rows": dict(n_head=2, n_kv=2, nq=1, groups=[300, 3], n_pre=[1000, 515], weigh=True),
+    "own keys in ranges": dict(n_head=3, n_kv=3, nq=1, n_own=[0, 700, 1, 64, 65, 3000, 129], cap_own=3001, weigh=True),
+    "own keys in many ranges": dict(n_head=1, n_kv=1, nq=2, n_own=[40000, 2], weigh=True),
+    "prefix and long own keys": dict(n_head=1, n_kv=1, nq=1, groups=[1, 1], n_pre=[700, 0], n_own=[900, 4000], weigh=True),
+    "long prefix and own keys": dict(n_head=1, n_kv=1, nq=1, groups=[3], n_pre=[30000], n_own=[900, 0, 4000], weigh=True),
+    "long prefix of many rows and own keys": dict(n_head=1, n_kv=1, nq=1, groups=[20], n_pre=[40000], n_own=[9 * i for i in range(20)], weigh=True),
     "many queries": dict(n_head=2, n_kv=1, nq=41, groups=[1, 2], n_pre=[50, 77], n_own=[41, 43, 100], weigh=True),
     "wide group": dict(n_head=2, n_kv=1, nq=1, groups=[201], n_pre=[333], n_own=[i % 7 for i in range(201)], weigh=True),
 }
@@ -148,12 +153,15 @@ def test_equal_groups_need_no_table():
     b.check(b.run())
 
 
-def test_sequences_outside_every_group_have_no_prefix():
-    c = Case(4, n_head=2, n_kv=2, nq=1, start=np.array([2, 5], np.int32), n_pre=[50], n_own=[4, 0, 3, 0, 1, 6, 0],
-             weigh=True)
+@pytest.mark.parametrize("keys", [50, 700, 20000])
+@pytest.mark.parametrize("wide", [1, 20])
+@pytest.mark.parametrize("own", [True, False])
+def test_sequences_outside_every_group_have_no_prefix(keys, wide, own):
+    kw = dict(n_own=[4, 0, 3, 0, 1, 6, 0] + [2] * (3 * wide)) if own else dict(batch=7 + 3 * wide)
+    c = Case(4, n_head=2, n_kv=2, nq=1, start=np.array([2, 2, 5 + 3 * wide], np.int32), n_pre=[3, keys], weigh=True, **kw)
     out = c.run()
     c.check(out)
-    assert torch.all(out[[1, 6]] == 0)                # no prefix, no keys
+    assert torch.all(out[1] == 0) and (own or torch.all(out[[0, -1]] == 0))    # no prefix, no keys
 
 
 @pytest.mark.parametrize("beams", [4, 20, 40])

@@ -21,7 +21,8 @@ constexpr int PA_SMEM = PA_WARPS * PA_RING;
 constexpr int SO_ROW = 68;         // floats a row of the warps' staged results
 constexpr int PM_ROWS = 8;         // rows of one merge block (16 threads a row)
 constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
-constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp
+constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp at a time
+constexpr int PW_TURNS = 4;        // weight kernel: times
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -87,51 +88,53 @@ __device__ __forceinline__ void score8(const uint32_t (&a)[4][4], const uint4 &k
     mma_bf16(s, a[3][0], a[3][1], a[3][2], a[3][3], k1.z, k1.w);
 }
 
+// OWN = false: the prefixes; true: the sequences' own keys.
+template <bool OWN>
 __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    // What runs after this kernel's trigger may count on its inputs.  Beside k_prefix_tc, which waited for
-    // them, it only makes sure that that kernel has ended before it does itself.
-    if (!p.beside_tc) pdl_wait();
+    // What runs after this kernel's trigger may count on its inputs (the prefix blocks waited for them).
+    if (!OWN || !p.after_pre) pdl_wait();
     pdl_launch_dependents();
     // ---- which rows, which keys ----
     // A work item is done by `wpi` neighbouring warps: all four for a prefix, p.own_wpi for own keys.
-    const bool is_pre = blockIdx.x < p.pre_blocks;
-    const int wpi = is_pre ? PA_WARPS : p.own_wpi, iw = warp & (wpi - 1);
-    const bool first = iw == 0 && lane == 0;
+    const PaSet &ks = OWN ? p.own : p.pre;
+    const int cluster = OWN ? p.own_cluster : p.pre_cluster;
+    const int wpi = OWN ? p.own_wpi : PA_WARPS, iw = warp & (wpi - 1);
     Rows rw;
     int set, split, r0;
-    if (is_pre) {
-        unsigned x = blockIdx.x;
-        const int slot = x % p.slots;
-        x /= p.slots;
-        rw.hk = x % p.n_kv;
-        split = x / p.n_kv;
-        if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw)) return;
-    } else {
-        long long x = (blockIdx.x - p.pre_blocks) * (PA_WARPS / wpi) + warp / wpi;
+    if (OWN) {
+        long long x = (long long)blockIdx.x * (PA_WARPS / wpi) + warp / wpi;
         if (x >= p.own_items) {
-            if (p.beside_tc) pdl_wait();
+            pdl_wait();   // on every path: the kernel after this one counts on the one before it too
             return;
         }
+        split = x % ks.splits;
+        x /= ks.splits;
         const int tile = x % p.own_tiles;
         x /= p.own_tiles;
         rw.hk = x % p.n_kv;
-        x /= p.n_kv;
-        split = x % p.own.splits;
-        set = x / p.own.splits;
+        set = x / p.n_kv;
         rw.seq0 = set;
         rw.n = p.nq * p.rep;
         r0 = tile * PA_TILE;
+    } else {
+        unsigned x = blockIdx.x;
+        split = x % ks.splits;
+        x /= ks.splits;
+        const int slot = x % p.slots;
+        rw.hk = x / p.slots;
+        if (cluster && split == 0) finish_outside(p, slot, rw.hk);
+        if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw)) return;
     }
-    const PaSet &ks = is_pre ? p.pre : p.own;
     const int nk = clamp_count(ks, set);
-    if (ks.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && first && __ldg(ks.n_keys + set) != nk)
+    if (ks.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && iw == 0 && lane == 0 && __ldg(ks.n_keys + set) != nk)
         set_status(p.ctl, WH_EBOUNDS);
     const int k0 = split * ks.chunk, k1 = min(nk, k0 + ks.chunk);
-    if (k0 >= k1 && !p.direct) {   // nothing here: the merge knows
-        if (p.beside_tc) pdl_wait();
+    if (k0 >= k1 && !cluster) {   // nothing here: the merge knows
+        if (OWN) pdl_wait();
         return;
     }
+    const int before = OWN && cluster && p.after_pre ? pre_parts_of(p, group_of(p, set)) : 0;
 
     uint32_t qa[4][4];
     int lim[2];   // own keys: the first key that a row does not see
@@ -139,13 +142,13 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         lim[half] = nk;
-        if (!is_pre) {
+        if (OWN) {
             int qrow, head, qi;
             rw.locate(p, min(r0 + g + 8 * half, rw.n - 1), qrow, head, qi);
             lim[half] = nk - (p.nq - 1 - qi);
         }
     }
-    const int full = is_pre ? nk : nk - (p.nq - 1);   // every row sees the keys before this one
+    const int full = OWN ? nk - (p.nq - 1) : nk;   // every row sees the keys before this one
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, o[8][4] = {};
     // Each warp copies its steps of 16 keys and values into a ring of its own, PA_STAGES - 1 ahead: four rows
@@ -180,6 +183,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         }
         cp_async_commit();
     };
+    float *scores = reinterpret_cast<float *>(ring_all + PA_SMEM) + (warp / wpi) * p.score_floats;
     const int stride = wpi * PA_KEYS;
     int t0 = k0 + iw * PA_KEYS, slot = 0;
 #pragma unroll
@@ -218,6 +222,15 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
                     const int key = t0 + 8 * j + 2 * c + (i & 1);
                     if (key >= min(k1, lim[i >> 1])) s[j][i] = -INFINITY;
                 }
+        }
+        if (OWN && p.score_floats) {   // for the weights, once the row's sum is known
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    if (g + 8 * half < rw.n)
+                        *reinterpret_cast<float2 *>(scores + (g + 8 * half) * ks.chunk + t0 - k0 + 8 * j + 2 * c) =
+                            make_float2(s[j][2 * half], s[j][2 * half + 1]);
         }
         float mx[2], mn[2];
 #pragma unroll
@@ -284,10 +297,12 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
                 make_float4(o[4][2 * half + i], o[5][2 * half + i], o[6][2 * half + i], o[7][2 * half + i]);
         }
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpi), "r"(32 * wpi) : "memory");
-    const int part = is_pre ? split : p.pre.splits + split, w0 = warp - iw;
-    const int todo = 8 * min(PA_TILE, rw.n - r0);
-    for (int i = 32 * iw + lane; i < todo; i += 32 * wpi) {
+    auto item_bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpi), "r"(32 * wpi) : "memory"); };
+    item_bar();
+    if (OWN && p.after_pre) pdl_wait();   // the prefix's partial results are complete
+    __shared__ float2 fin[PA_WARPS][PA_TILE];   // the block's maximum and sum; own weights: the row's maximum, 1 / sum
+    const int w0 = warp - iw, rows = min(PA_TILE, rw.n - r0);
+    for (int i = 32 * iw + lane; i < 8 * rows; i += 32 * wpi) {
         const int r = i >> 3, d0 = 8 * (i & 7);
         float mt = -INFINITY;
         for (int w = 0; w < wpi; ++w) mt = fmaxf(mt, sml[w0 + w][r].x);
@@ -301,9 +316,45 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
             v[0] = fmaf(x.x, f, v[0]), v[1] = fmaf(x.y, f, v[1]), v[2] = fmaf(x.z, f, v[2]), v[3] = fmaf(x.w, f, v[3]);
             v[4] = fmaf(y.x, f, v[4]), v[5] = fmaf(y.y, f, v[5]), v[6] = fmaf(y.z, f, v[6]), v[7] = fmaf(y.w, f, v[7]);
         }
-        finish_row(p, rw, r0 + r, part, d0, mt, lt, v);
+        if (cluster == 0) {
+            leave_part(p, rw, r0 + r, OWN ? p.pre.splits + split : split, d0, mt, lt, v);
+        } else if (cluster == 1) {
+            const float2 st = finish_row(p, rw, r0 + r, d0, mt, lt, v, before);
+            if (d0 == 0) fin[w0][r] = st;
+        } else {
+            float *d = so(w0, r) + d0;   // (only this thread reads or writes these dims)
+            *reinterpret_cast<float4 *>(d) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            if (d0 == 0) fin[w0][r] = make_float2(mt, lt);
+        }
     }
-    if (p.beside_tc) pdl_wait();
+    if (cluster > 1) {   // whole blocks: wpi = 4
+        __syncwarp();
+        cluster_sync();
+        finish_cluster<PA_THREADS>(p, rw, r0, rows, so(0, 0), SO_ROW, fin[0], cluster, threadIdx.x);
+        __syncwarp();
+        cluster_sync();   // no block leaves while another may still read its rows
+    }
+    if (OWN && p.score_floats) {
+        item_bar();
+        float *w = ks.weight + ((long long)set * p.n_kv + rw.hk) * ks.max_keys;
+        constexpr int U = 4;   // keys of a thread at a time: their accumulators are read together
+        for (int t = 32 * iw + lane; t < k1; t += U * 32 * wpi) {
+            float add[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) add[u] = t + u * 32 * wpi < k1 ? __ldcg(w + t + u * 32 * wpi) : 0.0f;
+            for (int r = 0; r < rows; ++r) {
+                const float2 st = fin[w0][r];
+                const float *sr = scores + r * ks.chunk + t;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (t + u * 32 * wpi < k1) add[u] = fmaf(ex2_approx(sr[u * 32 * wpi] - st.x), st.y, add[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (t + u * 32 * wpi < k1) w[t + u * 32 * wpi] = add[u];
+        }
+    }
 }
 
 // o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the ranges of a row that hold keys, in order.
@@ -314,25 +365,13 @@ __global__ void __launch_bounds__(16 * PM_ROWS) k_prefix_merge(const PaArgs p) {
     const long long row = (long long)blockIdx.x * PM_ROWS + (threadIdx.x >> 4);
     const int lane = threadIdx.x & 15;
     const int b = (int)(min(row, rows - 1) / ((long long)p.nq * p.n_head));
-    int np = 0, no = 0;
-    if (p.pre.n_set > 0) {
-        int g = -1;
-        if (p.group_start) {
-            // (the two rows of a warp may belong to different sequences: search one after the other)
-            const int b0 = __shfl_sync(0xffffffffu, b, 0), b1 = __shfl_sync(0xffffffffu, b, 16);
-            const int g0 = warp_search(p.group_start, p.pre.n_set, 1, 1, 0, b0);
-            const int g1 = b1 == b0 ? g0 : warp_search(p.group_start, p.pre.n_set, 1, 1, 0, b1);
-            const int gg = (threadIdx.x & 16) ? g1 : g0;
-            int s, e;
-            group_range(p, gg, s, e);
-            if (b >= s && b < e) g = gg;
-        } else if (b / p.gsize < p.pre.n_set) {
-            g = b / p.gsize;
-        }
-        if (g >= 0) np = (clamp_count(p.pre, g) + p.pre.chunk - 1) / p.pre.chunk;
-    }
+    int no = 0;
+    // (the two rows of a warp may belong to different sequences: one after the other)
+    const int b0 = __shfl_sync(0xffffffffu, b, 0), b1 = __shfl_sync(0xffffffffu, b, 16);
+    const int np0 = pre_parts_of(p, group_of(p, b0)), np1 = b1 == b0 ? np0 : pre_parts_of(p, group_of(p, b1));
+    const int np = (threadIdx.x & 16) ? np1 : np0;
     if (p.own.n_set > 0) no = (clamp_count(p.own, b) + p.own.chunk - 1) / p.own.chunk;
-    const int ns = p.pre.splits + p.own.splits;
+    const int ns = p.n_part;
     const float2 *ml = p.part_ml + min(row, rows - 1) * ns;
     const uint32_t half = 0xffffu << (threadIdx.x & 16);
     // ranges that hold keys: 0 .. np-1 of the prefix, then 0 .. no-1 of the sequence's own
@@ -360,18 +399,18 @@ __global__ void __launch_bounds__(16 * PM_ROWS) k_prefix_merge(const PaArgs p) {
 }
 
 // weight[t] += sum over the set's queries of 2^(s_t - m) / l: the scores again, with every row's final
-// maximum and sum.  One warp holds 32 keys and goes through the rows 16 at a time, so each sum has one
-// fixed order.
+// maximum and sum.  A warp holds 32 keys at a time, PW_TURNS times, and goes through the rows 16 at a time, so
+// each sum has one fixed order.
 __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p, int own) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const PaSet &ks = own ? p.own : p.pre;
     Rows rw;
     rw.hk = blockIdx.y;
     const int set = blockIdx.z;
-    const int t0 = (blockIdx.x * PW_WARPS + (threadIdx.x >> 5)) * PW_KEYS;
     const int nk = clamp_count(ks, set);
+    int t0 = (blockIdx.x * PW_WARPS * PW_TURNS + (threadIdx.x >> 5)) * PW_KEYS;
     if (t0 >= nk) {
-        pdl_wait();   // on every path: a kernel after this one counts on the merge's end too
+        pdl_wait();   // on every path: a kernel after this one counts on what came before too
         return;
     }
     int s0 = set, e0 = set + 1;
@@ -380,23 +419,25 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
     rw.n = (e0 - s0) * p.nq * p.rep;
     const __nv_bfloat16 *kb = ks.k + (long long)set * ks.set_stride + rw.hk * 64 + 8 * c;
     uint4 kr[4][2];
+    auto load_k = [&](int t) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int tk = t0 + 8 * j + g;
-        kr[j][0] = kr[j][1] = make_uint4(0, 0, 0, 0);
-        if (tk < nk) {
-            const uint4 *s = reinterpret_cast<const uint4 *>(kb + (long long)tk * ks.row_stride);
-            kr[j][0] = __ldg(s);
-            kr[j][1] = __ldg(s + 4);
+        for (int j = 0; j < 4; ++j) {
+            const int tk = t + 8 * j + g;
+            kr[j][0] = kr[j][1] = make_uint4(0, 0, 0, 0);
+            if (tk < nk) {
+                const uint4 *s = reinterpret_cast<const uint4 *>(kb + (long long)tk * ks.row_stride);
+                kr[j][0] = __ldg(s);
+                kr[j][1] = __ldg(s + 4);
+            }
         }
-    }
+    };
+    load_k(t0);
     pdl_wait();
-    float acc[4][2] = {};
-    for (int r0 = 0; r0 < rw.n; r0 += 16) {
-        uint32_t qa[4][4];
+    uint32_t qa[4][4];
+    float2 st[2];
+    int lim[2];
+    auto load_rows = [&](int r0) {
         load_q(p, rw, r0, qa);
-        float2 st[2];
-        int lim[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             st[half] = make_float2(0.0f, 0.0f);
@@ -408,49 +449,66 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
                 lim[half] = own ? nk - (p.nq - 1 - qi) : nk;
             }
         }
+    };
+    load_rows(0);
+    for (int turn = 0; turn < PW_TURNS && t0 < nk; ++turn) {
+        float acc[4][2] = {};
+        for (int r0 = 0; r0 < rw.n; r0 += 16) {
+            if (rw.n > 16) load_rows(r0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float s[4];
-            score8(qa, kr[j][0], kr[j][1], s);
+            for (int j = 0; j < 4; ++j) {
+                float s[4];
+                score8(qa, kr[j][0], kr[j][1], s);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = t0 + 8 * j + 2 * c + (i & 1);
-                const float e = ex2_approx(s[i] * PA_SCALE - st[i >> 1].x);
-                if (key < lim[i >> 1]) acc[j][i & 1] = fmaf(e, st[i >> 1].y, acc[j][i & 1]);
+                for (int i = 0; i < 4; ++i) {
+                    const int key = t0 + 8 * j + 2 * c + (i & 1);
+                    const float e = ex2_approx(s[i] * PA_SCALE - st[i >> 1].x);
+                    if (key < lim[i >> 1]) acc[j][i & 1] = fmaf(e, st[i >> 1].y, acc[j][i & 1]);
+                }
             }
         }
+        const int done = t0;
+        t0 += PW_WARPS * PW_KEYS;
+        load_k(t0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float a = acc[j][i];
+                a += __shfl_xor_sync(0xffffffffu, a, 4);
+                a += __shfl_xor_sync(0xffffffffu, a, 8);
+                a += __shfl_xor_sync(0xffffffffu, a, 16);
+                const int key = done + 8 * j + 2 * c + i;
+                if (g == 0 && key < nk) ks.weight[((long long)set * p.n_kv + rw.hk) * ks.max_keys + key] += a;
+            }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float a = acc[j][i];
-            a += __shfl_xor_sync(0xffffffffu, a, 4);
-            a += __shfl_xor_sync(0xffffffffu, a, 8);
-            a += __shfl_xor_sync(0xffffffffu, a, 16);
-            const int key = t0 + 8 * j + 2 * c + i;
-            if (g == 0 && key < nk) ks.weight[((long long)set * p.n_kv + rw.hk) * ks.max_keys + key] += a;
-        }
 }
 
 size_t up256p(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Key ranges of a set: as many as are resident at once, in whole steps of a block.
+// Key ranges of a set: as many as are resident at once, in whole steps of a block, of at least `least` keys.  No more than one cluster's
+// blocks if those then take at most `cluster_keys` keys each: joining ranges in a cluster saves a kernel.
 constexpr long long PA_BLOCKS = 3 * 152;   // k_prefix_attention: 3 blocks on each of GB300's 152 SMs
 constexpr long long PT_BLOCKS = 2 * 152;   // k_prefix_tc: 2 on each
 constexpr int PT_MIN_ROWS = 16;
-void split_keys(PaSet &s, long long items, long long blocks, int step) {
+constexpr int PA_CLUSTER = 16, PT_CLUSTER = 2;
+constexpr int PA_CLUSTER_KEYS = 512, PT_CLUSTER_KEYS = 0;
+constexpr int PA_SCORE_BYTES = 8192;
+constexpr int PA_OWN_LEAST = 512;   // beside a prefix, shorter own keys are not cut into ranges: that saves the merge
+void split_keys(PaSet &s, long long items, long long blocks, int step, int least, int cluster, int cluster_keys) {
     s.splits = s.chunk = 0;
     if (s.n_set <= 0) return;
     long long n = blocks / items;
-    const long long most = (s.max_keys + step - 1) / step;
+    const long long most = (s.max_keys + least - 1) / least;
     n = n < 1 ? 1 : (n > most ? most : n);
+    if (n > cluster && (long long)cluster * cluster_keys >= s.max_keys) n = cluster;
     s.chunk = (int)(((s.max_keys + n - 1) / n + step - 1) / step * step);
     s.splits = (s.max_keys + s.chunk - 1) / s.chunk;
 }
 
 struct PaPlan {
-    bool tc;   // the prefix part runs on the tcgen05 kernel
+    bool tc;      // the prefix part runs on the tcgen05 kernel
+    bool merge;   // partial results are joined by k_prefix_merge
     size_t part_o, part_ml, stats, total;
 };
 
@@ -459,29 +517,41 @@ PaPlan plan(PaArgs &a, bool may_tc) {
     PaPlan pl;
     const long long per = (long long)a.nq * a.rep, all = a.batch * per;
     const long long rows_a_set = a.pre.n_set > 0 ? (all + a.pre.n_set - 1) / a.pre.n_set : 0;
+    const bool has_pre = a.pre.n_set > 0, has_own = a.own.n_set > 0;
     pl.tc = may_tc && rows_a_set > PT_MIN_ROWS;
     a.tile = !pl.tc ? PA_TILE : rows_a_set > 64 ? 128 : rows_a_set > 32 ? 64 : 32;
     a.slots = 0;
-    if (a.pre.n_set > 0)
+    if (has_pre)
         a.slots = (int)(a.gsize == 0 ? a.pre.n_set + all / a.tile
                                      : a.pre.n_set * ((a.gsize * per + a.tile - 1) / a.tile));
     a.own_tiles = (int)((per + PA_TILE - 1) / PA_TILE);
     if (pl.tc)
-        split_keys(a.pre, (long long)a.slots * a.n_kv, PT_BLOCKS, PT_KEYS);
+        split_keys(a.pre, (long long)a.slots * a.n_kv, PT_BLOCKS, PT_KEYS, PT_KEYS, PT_CLUSTER, PT_CLUSTER_KEYS);
     else
-        split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, PA_WARPS * PA_KEYS);
+        split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, PA_WARPS * PA_KEYS, PA_WARPS * PA_KEYS, PA_CLUSTER,
+                   PA_CLUSTER_KEYS);
     // own keys: one warp an item when that fills the device, more warps, then key ranges, when it does not
     const long long items = (long long)a.own.n_set * a.n_kv * a.own_tiles;
     a.own_wpi = PA_WARPS;
     while (a.own_wpi > 1 && (items * a.own_wpi > PA_BLOCKS * PA_WARPS || (a.own_wpi - 1) * PA_KEYS >= a.own.max_keys))
         a.own_wpi /= 2;
-    split_keys(a.own, items, PA_BLOCKS * (PA_WARPS / a.own_wpi), a.own_wpi * PA_KEYS);
+    split_keys(a.own, items, PA_BLOCKS * (PA_WARPS / a.own_wpi), a.own_wpi * PA_KEYS,
+               has_pre ? PA_OWN_LEAST : PA_WARPS * PA_KEYS, PA_CLUSTER, PA_CLUSTER_KEYS);
     a.own_items = items * a.own.splits;
-    const size_t rows = (size_t)a.batch * a.nq * a.n_head, ns = (size_t)a.pre.splits + a.own.splits;
-    a.direct = ns == 1 && (a.pre.n_set == 0 || a.gsize > 0);
+    const bool one_launch = a.own_wpi == PA_WARPS && a.own.splits <= PA_CLUSTER && !has_pre;
+    a.own_cluster = has_own && (a.own.splits == 1 || one_launch) ? a.own.splits : 0;
+    a.pre_cluster = has_pre && !has_own && a.pre.splits <= (pl.tc ? PT_CLUSTER : PA_CLUSTER) ? a.pre.splits : 0;
+    pl.merge = has_own ? a.own_cluster == 0 : a.pre_cluster == 0;
+    a.after_pre = has_pre && has_own;
+    a.n_part = pl.merge || a.after_pre ? a.pre.splits + (a.own_cluster ? 0 : a.own.splits) : 0;
+    // the weights of own keys without a second pass, when an item sees all its keys and has room for the scores
+    const long long scores = (per < PA_TILE ? per : PA_TILE) * (long long)a.own.chunk;
+    const bool room = scores * (PA_WARPS / a.own_wpi) * 4 <= PA_SCORE_BYTES;
+    a.score_floats = a.own_cluster == 1 && a.own_tiles == 1 && room ? (int)scores : 0;
+    const size_t rows = (size_t)a.batch * a.nq * a.n_head;
     size_t off = 0;
-    pl.part_o = off;  off += a.direct ? 0 : up256p(rows * ns * 64 * 4);
-    pl.part_ml = off; off += a.direct ? 0 : up256p(rows * ns * 8);
+    pl.part_o = off;  off += up256p(rows * a.n_part * 64 * 4);
+    pl.part_ml = off; off += up256p(rows * a.n_part * 8);
     pl.stats = off;   off += up256p(rows * 8);
     pl.total = off < 256 ? 256 : off;
     return pl;
@@ -520,41 +590,31 @@ int launch(PaArgs &a, const PaPlan &pl, const PtMaps &maps, uint8_t *ws, cudaStr
     const long long pre_blocks = (long long)a.slots * a.n_kv * a.pre.splits;
     const long long own_blocks = (a.own_items * a.own_wpi + PA_WARPS - 1) / PA_WARPS;
     const long long rows = (long long)a.batch * a.nq * a.n_head;
-    if (pre_blocks + own_blocks > 0x7fffffffLL) return WH_EINVAL;
-    cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.stream = s;
-    if (pl.tc && pre_blocks > 0) {
-        if (int rc = prefix_tc_launch(a, maps, s)) return rc;
-        a.beside_tc = 1;
-        lc.numAttrs = 1;   // own keys beside the prefix blocks' last ones
+    if (pre_blocks > 0x7fffffffLL || own_blocks > 0x7fffffffLL) return WH_EINVAL;
+    if (!a.own.weight) a.score_floats = 0;
+    bool pdl = false;
+    if (pre_blocks > 0) {
+        if (int rc = pl.tc ? prefix_tc_launch(a, maps, s)
+                           : launch_ex(k_prefix_attention<false>, dim3((unsigned)pre_blocks), PA_THREADS, PA_SMEM,
+                                       a.pre_cluster, false, s, a))
+            return rc;
+        pdl = true;   // own keys beside the prefix's last blocks
     }
-    a.pre_blocks = pl.tc ? 0 : pre_blocks;
-    if (a.pre_blocks + own_blocks > 0) {
-        lc.gridDim = dim3((unsigned)(a.pre_blocks + own_blocks));
-        lc.blockDim = dim3(PA_THREADS);
-        lc.dynamicSmemBytes = PA_SMEM;
-        if (cudaLaunchKernelEx(&lc, k_prefix_attention, a) != cudaSuccess) return WH_ECUDA;
-        count_launch();
-        lc.dynamicSmemBytes = 0;
+    if (own_blocks > 0) {
+        const int smem = PA_SMEM + (a.score_floats ? PA_SCORE_BYTES : 0);
+        if (int rc = launch_ex(k_prefix_attention<true>, dim3((unsigned)own_blocks), PA_THREADS, smem, a.own_cluster, pdl, s, a))
+            return rc;
     }
-    lc.numAttrs = 1;
-    if (!a.direct) {
-        lc.gridDim = dim3((unsigned)((rows + PM_ROWS - 1) / PM_ROWS));
-        lc.blockDim = dim3(16 * PM_ROWS);
-        if (cudaLaunchKernelEx(&lc, k_prefix_merge, a) != cudaSuccess) return WH_ECUDA;
-        count_launch();
-    }
+    if (pl.merge)
+        if (int rc = launch_ex(k_prefix_merge, dim3((unsigned)((rows + PM_ROWS - 1) / PM_ROWS)), 16 * PM_ROWS, 0, 1, true, s, a))
+            return rc;
     for (int own = 0; own < 2; ++own) {
         const PaSet &ks = own ? a.own : a.pre;
-        if (!ks.weight) continue;
-        lc.gridDim = dim3((ks.max_keys + PW_WARPS * PW_KEYS - 1) / (PW_WARPS * PW_KEYS), a.n_kv, ks.n_set);
-        lc.blockDim = dim3(32 * PW_WARPS);
-        if (cudaLaunchKernelEx(&lc, k_prefix_weight, a, own) != cudaSuccess) return WH_ECUDA;
-        count_launch();
+        if (!ks.weight || (own && a.score_floats)) continue;
+        const int per_block = PW_WARPS * PW_KEYS * PW_TURNS;
+        if (int rc = launch_ex(k_prefix_weight, dim3((ks.max_keys + per_block - 1) / per_block, a.n_kv, ks.n_set),
+                               32 * PW_WARPS, 0, 1, true, s, a, own))
+            return rc;
     }
     return cudaGetLastError() == cudaSuccess ? WH_OK : WH_ECUDA;
 }
@@ -562,8 +622,12 @@ int launch(PaArgs &a, const PaPlan &pl, const PtMaps &maps, uint8_t *ws, cudaStr
 }  // namespace
 
 int prefix_attention_prepare() {
-    if (cudaFuncSetAttribute(k_prefix_attention, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM) != cudaSuccess)
-        return WH_ECUDA;
+    const void *const kernels[2] = {reinterpret_cast<const void *>(k_prefix_attention<false>),
+                                    reinterpret_cast<const void *>(k_prefix_attention<true>)};
+    for (const void *k : kernels)
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PA_SMEM + PA_SCORE_BYTES) != cudaSuccess ||
+            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return WH_ECUDA;
     return prefix_tc_prepare();
 }
 

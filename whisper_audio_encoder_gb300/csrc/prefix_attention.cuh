@@ -27,14 +27,19 @@ struct PaArgs {
     int slots;                // prefix: row-tile slots of a key head over all groups
     int own_tiles;            // row tiles of a sequence
     int own_wpi;              // own keys: warps of a work item
-    long long own_items;      // own keys: (sequence, range, key head, row tile)
-    long long pre_blocks;     // blocks [0, pre_blocks) take prefix work, the rest own keys
-    float *part_o;            // [row][pre.splits + own.splits][64], row = (b nq + i) n_head + h
-    float2 *part_ml;          // [row][pre.splits + own.splits]: running maximum and sum
+    long long own_items;      // own keys: (sequence, key head, row tile, range)
+    // How the key ranges of a row come together.  Without own keys, and for own keys alone, the blocks of one
+    // item's ranges form a thread-block cluster (its size; 1: a single range) and finish their rows themselves.
+    // With both, the prefix blocks leave partial results and the sequences' own blocks, one range each, finish
+    // the rows.  Otherwise (0) all leave partial results and k_prefix_merge joins them.
+    int pre_cluster, own_cluster;
+    int n_part;               // partial results of a row: of the prefix's ranges, then of the own keys'
+    int after_pre;            // own keys' blocks: the prefix's may still be running until pdl_wait
+    int score_floats;         // own keys: scores that an item keeps in shared memory for the weights, or 0
+    float *part_o;            // [row][n_part][64], row = (b nq + i) n_head + h
+    float2 *part_ml;          // [row][n_part]: running maximum and sum
     float2 *stats;            // [row]: maximum and 1 / sum (weights only)
     __nv_bfloat16 *out;       // [batch * nq][64 n_head]
-    int direct;               // one range covers everything a row sees: write out, no merge
-    int beside_tc;            // k_prefix_attention runs beside k_prefix_tc: it waits for it at its end
     DevCtl ctl;
 };
 
@@ -84,6 +89,20 @@ struct Rows {
     }
 };
 
+// The prefix set of sequence b, or -1.  Whole warp, one b.
+__device__ __forceinline__ int group_of(const PaArgs &p, int b) {
+    if (p.pre.n_set <= 0) return -1;
+    if (!p.group_start) return b / p.gsize;
+    const int g = warp_search(p.group_start, p.pre.n_set, 1, 1, 0, b);
+    int s, e;
+    group_range(p, g, s, e);
+    return b >= s && b < e ? g : -1;
+}
+// Partial results that the prefix blocks leave for a sequence of set g.
+__device__ __forceinline__ int pre_parts_of(const PaArgs &p, int g) {
+    return g < 0 ? 0 : (clamp_count(p.pre, g) + p.pre.chunk - 1) / p.pre.chunk;
+}
+
 // Prefix work of one block: its group, the rows r0 .. of that group's tile, false if the slot is empty.  With
 // group_start, group g's tiles take the slots from start[g] (nq rep) / tile + g on, which end before group
 // g + 1's, so no block needs to know the other groups' sizes.  One block per group reports a bad range.
@@ -109,25 +128,98 @@ __device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report
     return r0 >= 0 && r0 < rw.n;
 }
 
-// Dims d0 .. d0 + 7 of row r of a block's result (v relative to the maximum mt, with sum lt): the output
-// itself, or partial result number `part` for the merge.
-__device__ __forceinline__ void finish_row(const PaArgs &p, const Rows &rw, int r, int part, int d0, float mt, float lt,
+// Partial result `part` of row r of a block: dims d0 .. d0 + 7, relative to the maximum mt, with sum lt.
+__device__ __forceinline__ void leave_part(const PaArgs &p, const Rows &rw, int r, int part, int d0, float mt, float lt,
                                            const float (&v)[8]) {
     int qrow, head, qi;
     rw.locate(p, r, qrow, head, qi);
+    const long long at = ((long long)qrow * p.n_head + head) * p.n_part + part;
+    float4 *d = reinterpret_cast<float4 *>(p.part_o + at * 64 + d0);
+    d[0] = make_float4(v[0], v[1], v[2], v[3]);
+    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    if (d0 == 0) p.part_ml[at] = make_float2(mt, lt);
+}
+
+// The finished row, together with the first pre_parts partial results of the row.  Returns the row's maximum
+// and 1 / sum.
+__device__ __forceinline__ float2 finish_row(const PaArgs &p, const Rows &rw, int r, int d0, float mt, float lt,
+                                             float (&v)[8], int pre_parts) {
+    int qrow, head, qi;
+    rw.locate(p, r, qrow, head, qi);
     const long long row = (long long)qrow * p.n_head + head;
-    if (p.direct) {
-        const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;   // a query that sees no key: zeros
-        *reinterpret_cast<uint4 *>(p.out + row * 64 + d0) =
-            make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
-                       pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
-        if (p.stats && d0 == 0) p.stats[row] = make_float2(mt == -INFINITY ? 0.0f : mt, inv);
-    } else {
-        const long long at = row * (p.pre.splits + p.own.splits) + part;
-        float4 *d = reinterpret_cast<float4 *>(p.part_o + at * 64 + d0);
-        d[0] = make_float4(v[0], v[1], v[2], v[3]);
-        d[1] = make_float4(v[4], v[5], v[6], v[7]);
-        if (d0 == 0) p.part_ml[at] = make_float2(mt, lt);
+#pragma unroll 2
+    for (int i = 0; i < pre_parts; ++i) {
+        const long long at = row * p.n_part + i;
+        const float2 ml = __ldcg(p.part_ml + at);
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * 64 + d0));
+        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * 64 + d0 + 4));
+        const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const float mn = fmaxf(mt, ml.x);
+        const float f = mt == -INFINITY ? 0.0f : ex2_approx(mt - mn), e = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mn);
+        lt = lt * f + ml.y * e;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = v[k] * f + u[k] * e;
+        mt = mn;
+    }
+    const float2 st = make_float2(mt == -INFINITY ? 0.0f : mt, lt == 0.0f ? 0.0f : 1.0f / lt);   // no key: zeros
+    *reinterpret_cast<uint4 *>(p.out + row * 64 + d0) =
+        make_uint4(pack_bf16(v[0] * st.y, v[1] * st.y), pack_bf16(v[2] * st.y, v[3] * st.y),
+                   pack_bf16(v[4] * st.y, v[5] * st.y), pack_bf16(v[6] * st.y, v[7] * st.y));
+    if (p.stats && d0 == 0) p.stats[row] = st;
+    return st;
+}
+
+// Finishes the rows of a cluster whose blocks hold one key range each: row r's 64 values at `so` (so_row floats
+// a row) and its maximum and sum at `sml`, at the same places in every block's shared memory.  Between two
+// cluster barriers; the blocks share the rows, each thread takes 8 dims and adds the ranges in order.
+template <int THREADS>
+__device__ __forceinline__ void finish_cluster(const PaArgs &p, const Rows &rw, int r0, int rows, const void *so, int so_row,
+                                               const void *sml, int ranks, int tid) {
+    const int rank = (int)cluster_ctarank();
+    for (int i = rank * THREADS + tid; i < rows * 8; i += ranks * THREADS) {
+        const int r = i >> 3, d0 = 8 * (i & 7);
+        const uint32_t la = smem_u32(sml) + r * 8, oa = smem_u32(so) + (r * so_row + d0) * 4;
+        float mt = -INFINITY, lt = 0.0f, v[8] = {};
+        for (int c = 0; c < ranks; ++c) {
+            float m, l;
+            uint32_t ra, rb;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(la), "r"(c));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(oa), "r"(c));
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(m), "=f"(l) : "r"(ra) : "memory");
+            float u[8];
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3])
+                         : "r"(rb)
+                         : "memory");
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(u[4]), "=f"(u[5]), "=f"(u[6]), "=f"(u[7])
+                         : "r"(rb + 16)
+                         : "memory");
+            const float mn = fmaxf(mt, m);
+            const float f = mt == -INFINITY ? 0.0f : ex2_approx(mt - mn), e = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
+            lt = lt * f + l * e;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = v[k] * f + u[k] * e;
+            mt = mn;
+        }
+        finish_row(p, rw, r0 + r, d0, mt, lt, v, 0);
+    }
+}
+
+// Sequences outside every group have no prefix: the blocks of the first and the last slot finish their rows.
+// Whole block.
+__device__ __forceinline__ void finish_outside(const PaArgs &p, int slot, int hk) {
+    if (!p.group_start || (slot != 0 && slot != p.slots - 1)) return;
+    for (int end = 0; end < 2; ++end) {
+        if (slot != (end ? p.slots - 1 : 0)) continue;
+        Rows rw;
+        rw.hk = hk;
+        rw.seq0 = end ? min(max(__ldg(p.group_start + p.pre.n_set), 0), p.batch) : 0;
+        rw.n = ((end ? p.batch : min(max(__ldg(p.group_start), 0), p.batch)) - rw.seq0) * p.nq * p.rep;
+        for (long long i = threadIdx.x; i < 8LL * rw.n; i += blockDim.x) {
+            float none[8] = {};
+            finish_row(p, rw, (int)(i >> 3), 8 * (int)(i & 7), -INFINITY, 0.0f, none, 0);
+        }
     }
 }
 
@@ -139,6 +231,32 @@ struct PtMaps {
 };
 int prefix_tc_maps(const PaArgs &a, PtMaps *m);
 int prefix_tc_launch(const PaArgs &a, const PtMaps &m, cudaStream_t s);
+// One launch with optional programmatic serialization and cluster size along x.
+template <class... F, class... A>
+int launch_ex(void (*kernel)(F...), dim3 grid, int threads, int smem, int cluster, bool pdl, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    lc.attrs = attr;
+    lc.numAttrs = n;
+    if (cudaLaunchKernelEx(&lc, kernel, F(args)...) != cudaSuccess) return WH_ECUDA;
+    count_launch();
+    return WH_OK;
+}
 int prefix_tc_prepare();
 
 }  // namespace wh

@@ -70,26 +70,41 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
     pdl_launch_dependents();
     Rows rw;
     int set, r0;
-    const int slot = blockIdx.x % p.slots;
-    rw.hk = (blockIdx.x / p.slots) % p.n_kv;
-    const int split = blockIdx.x / p.slots / p.n_kv;
+    const int split = blockIdx.x % p.pre.splits, slot = blockIdx.x / p.pre.splits % p.slots;
+    rw.hk = blockIdx.x / p.pre.splits / p.slots;
+    const int cluster = p.pre_cluster;
+    if (cluster && split == 0) finish_outside(p, slot, rw.hk);
     if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw)) return;
     const int nk = clamp_count(p.pre, set);
     if (p.pre.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && threadIdx.x == 0 && __ldg(p.pre.n_keys + set) != nk)
         set_status(p.ctl, WH_EBOUNDS);
     const int k0 = split * p.pre.chunk, k1 = min(nk, k0 + p.pre.chunk);
     const int a = threadIdx.x - 128;   // the rows' threads: TMEM lane and matrix row
-    if (k0 >= k1) {                   // no keys: zeros if this is all there is, else the merge knows
-        if (p.direct) {
-            const float none[8] = {};
-            for (int i = threadIdx.x; i < TILE * 8; i += PT_THREADS)
-                if (r0 + (i >> 3) < rw.n) finish_row(p, rw, r0 + (i >> 3), split, 8 * (i & 7), -INFINITY, 0.0f, none);
+    float *so = reinterpret_cast<float *>(sKV);   // the epilogue's rows, then their maxima and sums
+    float2 *sml = reinterpret_cast<float2 *>(sKV + 128 * SO_ROW * 4);
+    const int rows = min(TILE, rw.n - r0);
+    if (k0 >= k1) {                   // no keys here
+        if (cluster) {
+            for (int i = threadIdx.x; i < rows * SO_ROW; i += PT_THREADS) so[i] = 0.0f;
+            for (int i = threadIdx.x; i < rows; i += PT_THREADS) sml[i] = make_float2(-INFINITY, 0.0f);
+            if (cluster > 1) {
+                __syncwarp();
+                cluster_sync();
+                if (warp >= 4) finish_cluster<128>(p, rw, r0, rows, so, SO_ROW, sml, cluster, a);
+                __syncwarp();
+                cluster_sync();
+            } else {
+                for (int i = threadIdx.x; i < rows * 8; i += PT_THREADS) {
+                    float none[8] = {};
+                    finish_row(p, rw, r0 + (i >> 3), 8 * (i & 7), -INFINITY, 0.0f, none, 0);
+                }
+            }
         }
         return;
     }
     if ((smem_u32(smem) & 1023u) != 0) {   // the swizzled tiles must lie on 1024-byte boundaries
         if (threadIdx.x == 0) set_status(p.ctl, WH_EBOUNDS);
-        return;
+        return;                            // (every block of a cluster alike)
     }
     const int nt = (k1 - k0 + PT_KEYS - 1) / PT_KEYS;
 
@@ -200,6 +215,11 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
             mbar_wait(drain, 0, p.ctl);
         }
       }
+      __syncwarp();
+      if (cluster > 1) {   // the row warps' two barriers
+          cluster_sync();
+          cluster_sync();
+      }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HIGH));
         const int col0 = (a / TILE) * COLS;   // the columns of this copy
@@ -305,11 +325,10 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full, (nt - 1) & 1u, p.ctl));
         if (!ok) *abort_flag = 1;
         tc_fence_after();
-        // every product is done, so the ring is free: stage O, merge the copies, write whole rows
-        float *so = reinterpret_cast<float *>(sKV);
-        float2 *sml = reinterpret_cast<float2 *>(sKV + 128 * SO_ROW * 4);
+        // every product is done, so the ring is free: stage O, merge the copies, then the ranges
+        float2 *sml_copy = sml + 128;
         if (ok) {
-            sml[a] = make_float2(m == -INFINITY ? m : m * PA_SCALE, l);
+            sml_copy[a] = make_float2(m == -INFINITY ? m : m * PA_SCALE, l);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t v[32];
@@ -323,15 +342,14 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
         }
         rows_bar();
         if (!*abort_flag) {
-            for (int i = a; i < TILE * 8; i += 128) {
+            for (int i = a; i < rows * 8; i += 128) {
                 const int r = i >> 3, d0 = 8 * (i & 7);
-                if (r0 + r >= rw.n) break;
                 float mt = -INFINITY, lt = 0.0f, v[8] = {};
 #pragma unroll
-                for (int c = 0; c < COPIES; ++c) mt = fmaxf(mt, sml[r + TILE * c].x);
+                for (int c = 0; c < COPIES; ++c) mt = fmaxf(mt, sml_copy[r + TILE * c].x);
 #pragma unroll
                 for (int c = 0; c < COPIES; ++c) {
-                    const float2 ml = sml[r + TILE * c];
+                    const float2 ml = sml_copy[r + TILE * c];
                     const float f = COPIES == 1 ? 1.0f : ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mt);
                     lt = fmaf(ml.y, f, lt);
 #pragma unroll
@@ -341,8 +359,24 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
                         v[k + 2] = fmaf(x.z, f, v[k + 2]), v[k + 3] = fmaf(x.w, f, v[k + 3]);
                     }
                 }
-                finish_row(p, rw, r0 + r, split, d0, mt, lt, v);
+                if (cluster == 0) {
+                    leave_part(p, rw, r0 + r, split, d0, mt, lt, v);
+                } else if (cluster == 1) {
+                    finish_row(p, rw, r0 + r, d0, mt, lt, v, 0);
+                } else {
+                    float *d = so + r * SO_ROW + d0;   // (only this thread reads or writes these dims)
+                    *reinterpret_cast<float4 *>(d) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4 *>(d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                    if (d0 == 0) sml[r] = make_float2(mt, lt);
+                }
             }
+        }
+        if (cluster > 1) {
+            __syncwarp();
+            cluster_sync();
+            if (!*abort_flag) finish_cluster<128>(p, rw, r0, rows, so, SO_ROW, sml, cluster, a);
+            __syncwarp();
+            cluster_sync();   // no block leaves while another may still read its rows
         }
     }
     tc_fence_before();
@@ -375,15 +409,9 @@ int prefix_tc_maps(const PaArgs &a, PtMaps *m) {
 }
 
 int prefix_tc_launch(const PaArgs &a, const PtMaps &m, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((long long)a.slots * a.n_kv * a.pre.splits);
-    if (a.tile == 128)
-        k_prefix_tc<1><<<blocks, PT_THREADS, PT_SMEM, s>>>(m, a);
-    else if (a.tile == 64)
-        k_prefix_tc<2><<<blocks, PT_THREADS, PT_SMEM, s>>>(m, a);
-    else
-        k_prefix_tc<4><<<blocks, PT_THREADS, PT_SMEM, s>>>(m, a);
-    count_launch();
-    return cudaGetLastError() == cudaSuccess ? WH_OK : WH_ECUDA;
+    const dim3 grid((unsigned)((long long)a.slots * a.n_kv * a.pre.splits));
+    auto *kernel = a.tile == 128 ? k_prefix_tc<1> : a.tile == 64 ? k_prefix_tc<2> : k_prefix_tc<4>;
+    return launch_ex(kernel, grid, PT_THREADS, PT_SMEM, a.pre_cluster, false, s, m, a);
 }
 
 }  // namespace wh

@@ -42,14 +42,14 @@ int ensure_device(DevState **out) {
         cudaGetLastError();
         return WH_ENODEV;
     }
-    int count = 0;
-    if (cudaGetDeviceCount(&count) != cudaSuccess || count == 0) {
-        cudaGetLastError();
-        return WH_ENODEV;
-    }
     std::lock_guard<std::mutex> lk(g_dev_mu);
     DevState &st = g_dev[dev];
     if (!st.ready) {
+        int count = 0;
+        if (cudaGetDeviceCount(&count) != cudaSuccess || count == 0) {
+            cudaGetLastError();
+            return WH_ENODEV;
+        }
         void *p = nullptr;
         if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return WH_ECUDA;
         const int zero = 0;

@@ -5,6 +5,7 @@ and streams.  There is no fallback: if libwh.so has not been built, or there is 
 calls raise.
 """
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -283,38 +284,50 @@ class Keys:
     [n_set] or None (max_keys for all); weight: float32 [n_set][n_kv_head][max_keys] or None, the
     accumulated attention weight of every key.  Holds the tensors it points to."""
 
+    __slots__ = ("k", "v", "n_keys", "weight", "device", "n_set", "max_keys", "width", "weight_heads", "c")
+
     def __init__(self, k, v, n_keys=None, weight=None):
         import torch
-        _need(k.dim() == 3 and k.shape == v.shape and k.stride() == v.stride() and k.stride(2) == 1 and
-              k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16, "Keys: k, v bf16 [n_set][max_keys][d], equal strides")
-        n_set, max_keys, d = k.shape
-        dev = k.device
+        shape, stride, dev = k.shape, k.stride(), k.device
+        _need(len(shape) == 3 and v.shape == shape and v.stride() == stride and stride[2] == 1 and
+              k.dtype == v.dtype == torch.bfloat16, "Keys: k, v bf16 [n_set][max_keys][d], equal strides")
+        n_set, max_keys, d = shape
         _need(dev.type == "cuda" and v.device == dev, "Keys: k and v must be on one CUDA device")
-        _need(n_keys is None or (n_keys.dtype == torch.int32 and n_keys.shape == (n_set,) and n_keys.is_contiguous() and
-                                 n_keys.device == dev), "Keys: n_keys int32 [n_set]")
-        _need(weight is None or (weight.dtype == torch.float32 and weight.dim() == 3 and weight.shape[0] == n_set and
-                                 weight.shape[2] == max_keys and weight.is_contiguous() and weight.device == dev),
-              "Keys: weight float32 [n_set][n_kv_head][max_keys]")
+        self.weight_heads = 0
+        if n_keys is not None:
+            _need(n_keys.dtype == torch.int32 and n_keys.shape == (n_set,) and n_keys.is_contiguous() and
+                  n_keys.device == dev, "Keys: n_keys int32 [n_set]")
+        if weight is not None:
+            ws = weight.shape
+            _need(weight.dtype == torch.float32 and len(ws) == 3 and ws[0] == n_set and ws[2] == max_keys and
+                  weight.is_contiguous() and weight.device == dev, "Keys: weight float32 [n_set][n_kv_head][max_keys]")
+            self.weight_heads = ws[1]
         self.k, self.v, self.n_keys, self.weight, self.device = k, v, n_keys, weight, dev
+        self.n_set, self.max_keys, self.width = n_set, max_keys, d
         # (the stride of a dimension of size one is never used)
-        self.c = wh_keys(k.data_ptr(), v.data_ptr(), k.stride(1) if max_keys > 1 else d, k.stride(0) if n_set > 1 else 0,
+        self.c = wh_keys(k.data_ptr(), v.data_ptr(), stride[1] if max_keys > 1 else d, stride[0] if n_set > 1 else 0,
                          None if n_keys is None else n_keys.data_ptr(), None if weight is None else weight.data_ptr(),
                          n_set, max_keys)
 
     def _check(self, n_kv_head, device, what):
-        _need(self.k.shape[2] >= 64 * n_kv_head, f"{what}: rows shorter than 64 n_kv_head")
-        _need(self.weight is None or self.weight.shape[1] == n_kv_head, f"{what}: weight [n_set][n_kv_head][max_keys]")
+        _need(self.width >= 64 * n_kv_head, f"{what}: rows shorter than 64 n_kv_head")
+        _need(self.weight is None or self.weight_heads == n_kv_head, f"{what}: weight [n_set][n_kv_head][max_keys]")
         _need(self.device == device, f"{what}: tensors on different devices")
 
 
-def _on_device(device, stream):
-    """(context, stream handle) for a launch on `device`, whatever the current device is."""
-    import contextlib
-
+def _launch(device, stream, call):
+    """call(stream handle) with `device` current; stream None is the device's current stream."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    here = torch.cuda.current_device() == device.index
-    return contextlib.nullcontext() if here else torch.cuda.device(device), ctypes.c_void_p(s.cuda_stream)
+    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        return call(handle)
+    with torch.cuda.device(device):
+        return call(handle)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(name, *args):
+    return max(256, getattr(lib(), name)(*args))
 
 
 def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_start=None, n_query=1, out=None,
@@ -326,33 +339,43 @@ def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_
     [batch * n_query][64 n_head]."""
     import torch
     what = "wh_prefix_attention"
-    _need(q.dim() == 2 and q.dtype == torch.bfloat16 and q.device.type == "cuda" and q.stride(1) == 1 and n_head >= 1 and
-          q.shape[1] >= 64 * n_head and n_query >= 1 and q.shape[0] % n_query == 0, f"{what}: q bf16 [batch * n_query][64 n_head]")
-    rows = q.shape[0]
-    batch, dev = rows // n_query, q.device
-    n_kv_head = n_head if n_kv_head is None else n_kv_head
-    for keys in (prefix, own):
-        if keys is not None:
-            keys._check(n_kv_head, dev, what)
-    _need(group_start is None or (prefix is not None and group_start.dtype == torch.int32 and group_start.device == dev and
-                                  group_start.is_contiguous() and group_start.shape == (prefix.c.n_set + 1,)),
-          f"{what}: group_start int32 [prefix sets + 1]")
+    shape, stride, dev = q.shape, q.stride(), q.device
+    _need(len(shape) == 2 and q.dtype == torch.bfloat16 and dev.type == "cuda" and stride[1] == 1 and n_head >= 1 and
+          shape[1] >= 64 * n_head and n_query >= 1 and shape[0] % n_query == 0,
+          "wh_prefix_attention: q bf16 [batch * n_query][64 n_head]")
+    rows = shape[0]
+    batch = rows // n_query
+    if n_kv_head is None:
+        n_kv_head = n_head
+    n_pre = max_pre = max_own = 0
+    if prefix is not None:
+        prefix._check(n_kv_head, dev, what)
+        n_pre, max_pre = prefix.n_set, prefix.max_keys
+    if own is not None:
+        own._check(n_kv_head, dev, what)
+        max_own = own.max_keys
+    if group_start is not None:
+        _need(group_start.dtype == torch.int32 and group_start.device == dev and group_start.is_contiguous() and
+              group_start.shape == (n_pre + 1,) and n_pre > 0, "wh_prefix_attention: group_start int32 [prefix sets + 1]")
     if out is None:
         out = torch.empty(rows, 64 * n_head, dtype=torch.bfloat16, device=dev)
     else:
         _need(out.dtype == torch.bfloat16 and out.shape == (rows, 64 * n_head) and out.is_contiguous() and
-              out.device == dev, f"{what}: out bf16 [batch * n_query][64 n_head]")
+              out.device == dev, "wh_prefix_attention: out bf16 [batch * n_query][64 n_head]")
     if workspace is None:
-        need = lib().wh_prefix_attention_workspace(batch, n_query, n_head, n_kv_head, prefix.c.n_set if prefix else 0,
-                                                   prefix.c.max_keys if prefix else 0, own.c.max_keys if own else 0)
-        workspace = torch.empty(max(256, need), dtype=torch.uint8, device=dev)
-    ctx, s = _on_device(dev, stream)
-    with ctx:
-        rc = lib().wh_prefix_attention(q.data_ptr(), q.stride(0) if rows > 1 else 64 * n_head, batch, n_query, n_head,
-                                       n_kv_head, ctypes.byref(prefix.c) if prefix else None, _ptr(group_start),
-                                       ctypes.byref(own.c) if own else None, out.data_ptr(), workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(), s)
-    _check(rc, what)
+        need = _workspace_bytes("wh_prefix_attention_workspace", batch, n_query, n_head, n_kv_head, n_pre, max_pre, max_own)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    else:
+        _need(workspace.device == dev, "wh_prefix_attention: workspace on another device")
+        need = workspace.numel() * workspace.element_size()
+    rc = _launch(dev, stream, lambda s: (_lib or lib()).wh_prefix_attention(
+        q.data_ptr(), stride[0] if rows > 1 else 64 * n_head, batch, n_query, n_head, n_kv_head,
+        prefix and prefix.c, group_start if group_start is None else group_start.data_ptr(), own and own.c,
+        out.data_ptr(), workspace.data_ptr(), need, s))
+    if rc != WH_OK:
+        raise WhError(rc, what)
     return out
 
 
@@ -365,23 +388,28 @@ def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, worksp
     import torch
     what = "wh_cache_evict"
     to = cache if out is None else out
-    dev, n_set = cache.device, cache.c.n_set
-    for keys in (cache, to):
-        keys._check(n_kv_head, dev, what)
-        _need(keys.weight is not None, f"{what}: Keys without weight")
-    _need(budget >= 1, f"{what}: budget >= 1")
-    _need(kept is None or (kept.dtype == torch.int32 and kept.shape == (n_set, n_kv_head, budget) and kept.is_contiguous()
-                           and kept.device == dev), f"{what}: kept int32 [n_set][n_kv_head][budget]")
+    dev, n_set = cache.device, cache.n_set
+    cache._check(n_kv_head, dev, what)
+    to._check(n_kv_head, dev, what)
+    _need(cache.weight is not None and to.weight is not None, "wh_cache_evict: Keys without weight")
+    _need(budget >= 1, "wh_cache_evict: budget >= 1")
+    if kept is not None:
+        _need(kept.dtype == torch.int32 and kept.shape == (n_set, n_kv_head, budget) and kept.is_contiguous() and
+              kept.device == dev, "wh_cache_evict: kept int32 [n_set][n_kv_head][budget]")
     n_out = to.n_keys if to.n_keys is not None else torch.empty(n_set, dtype=torch.int32, device=dev)
     if workspace is None:
-        workspace = torch.empty(max(256, lib().wh_cache_evict_workspace(n_set, n_kv_head, budget)), dtype=torch.uint8,
-                                device=dev)
-    ctx, s = _on_device(dev, stream)
-    with ctx:
-        rc = lib().wh_cache_evict(ctypes.byref(cache.c), n_kv_head, budget, recent,
-                                  None if out is None else ctypes.byref(out.c), n_out.data_ptr(), _ptr(kept),
-                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
-    _check(rc, what)
+        need = _workspace_bytes("wh_cache_evict_workspace", n_set, n_kv_head, budget)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    else:
+        _need(workspace.device == dev, "wh_cache_evict: workspace on another device")
+        need = workspace.numel() * workspace.element_size()
+    rc = _launch(dev, stream, lambda s: (_lib or lib()).wh_cache_evict(
+        cache.c, n_kv_head, budget, recent, out and out.c, n_out.data_ptr(), kept if kept is None else kept.data_ptr(),
+        workspace.data_ptr(), need, s))
+    if rc != WH_OK:
+        raise WhError(rc, what)
     return n_out
 
 
