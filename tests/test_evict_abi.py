@@ -45,6 +45,7 @@ def test_rejects_what_shares_memory(L):
     assert _call(L, _keys(set_stride=12800 - 128)) == wh.WH_EINVAL
     assert _call(L, _keys(v=P)) == wh.WH_EINVAL                       # keys and values the same memory
     assert _call(L, _keys(v=P + 2 * 64)) == wh.WH_EINVAL              # or a head apart
+    assert _call(L, _keys(n_keys=FAKE.value + 4)) == wh.WH_EINVAL     # new counts one off the old ones
     far = P + (1 << 24)
     assert _call(L, _keys(), out=_keys(at=far, n_set=2)) == wh.WH_EINVAL
     assert _call(L, _keys(), out=_keys(at=far, max_keys=39)) == wh.WH_EINVAL

@@ -107,6 +107,8 @@ CASES = {
     "budget past the cache": dict(heads=2, cap=20, counts=[20, 3], budget=50, recent=10),
     "kv rows": dict(heads=5, cap=150, counts=[150, 149, 60], budget=50, recent=9, layout="kv"),
     "sets beside each other": dict(heads=2, cap=90, counts=[90, 10, 64], budget=33, recent=1, layout="beside"),
+    "a few long heads": dict(heads=2, cap=1900, counts=[1900, 1025, 1024], budget=900, recent=50, kind="ties"),
+    "many long heads": dict(heads=8, cap=1030, counts=[1030 - 7 * i for i in range(40)], budget=700, recent=50, kind="odd"),
     "many sets": dict(heads=2, cap=64, counts=[(7 * i) % 65 for i in range(300)], budget=31, recent=4, kind="ties"),
 }
 

@@ -3,23 +3,30 @@
 // Each head of each set keeps, of its n keys, the last `recent` and of the others the budget - recent
 // with the largest weight (ties: the lowest index), in their order, moved together at the front.
 //
-// k_evict_select: one block per (head, set) finds the weight W below which no older key stays -- a
-// binary search over the bits of an order-preserving integer image of the weights, counting how many
-// are at least the candidate -- then numbers the keys that stay in order: those above W, the first few
-// equal to W, the recent ones.  It writes the source index of each and its weight.
-// k_evict_move / k_evict_shift: copy the rows, 16 bytes a thread, to other buffers or within the cache.
+// Choosing: the weight W below which no older key stays is found by a binary search over the 32 bits of an
+// order-preserving integer image of the weights, which the choosing threads hold in registers, counting how
+// many are at least the candidate.  Then the keys that stay are numbered in order: those above W, the first
+// few equal to W, the recent ones.
+// Moving is a copy of 128-byte rows, 16 bytes a thread, bound by HBM: within the cache every key moves towards
+// the front, so going up the rows with each step's reads before its writes is safe.
+//   k_evict_small   up to 2048 keys: a block chooses and moves one head of one set
+//   k_evict_select, then k_evict_move (other buffers: rows spread over the device) or k_evict_shift (within
+//   the cache: a block per head and keys or values), for long caches and where few heads move many rows
 #include "common.cuh"
 #include "internal.h"
 
 namespace wh {
 namespace {
 
-constexpr int EV_THREADS = 256;
-constexpr int EV_WARPS = EV_THREADS / 32;
+constexpr int SM_THREADS = 256;      // k_evict_small
+constexpr int SM_MOST = 2048;        // its longest cache
+constexpr int SM_ROWS = 512;         // rows that a block of it moves without a second thought
+constexpr int SM_HEADS = 3 * 152;    // blocks of it that are resident at once
+constexpr int SEL_THREADS = 1024;    // k_evict_select
+constexpr int SEL_HELD = 32;         // keys that a thread of it holds: longer caches are read again for every bit
 constexpr int MV_THREADS = 256;
-constexpr int MV_ROWS = 16;      // rows of one head that a block of k_evict_move copies at a time
-constexpr int SH_THREADS = 256;
-constexpr int SH_ROWS = SH_THREADS / 8;
+constexpr int MV_ROWS = 8;           // rows of a block of k_evict_move
+constexpr int SH_THREADS = 512;      // k_evict_shift
 
 struct EvArgs {
     const __nv_bfloat16 *k, *v;
@@ -42,99 +49,271 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Sum over the block, the same in every thread (two barriers).
-__device__ __forceinline__ int block_sum(int x, int *buf) {
-    x = __reduce_add_sync(0xffffffffu, x);
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
-    __syncthreads();
-    int s = 0;
-#pragma unroll
-    for (int w = 0; w < EV_WARPS; ++w) s += buf[w];
-    __syncthreads();
-    return s;
+// Threads that choose together: one warp, or a block of N warps.
+template <int THREADS>
+struct Team {
+    static constexpr int WARPS = THREADS / 32;
+    int *buf;   // [2 * WARPS]
+    __device__ __forceinline__ static void sync() {
+        if (WARPS == 1)
+            __syncwarp();
+        else
+            __syncthreads();
+    }
+    // Sum over the team, the same in every thread.
+    __device__ __forceinline__ int sum(int x) const {
+        x = __reduce_add_sync(0xffffffffu, x);
+        if (WARPS == 1) return x;
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+        __syncthreads();
+        const int s = __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < WARPS ? buf[threadIdx.x & 31] : 0);
+        __syncthreads();
+        return s;
+    }
+    __device__ __forceinline__ uint32_t largest(uint32_t x) const {
+        x = __reduce_max_sync(0xffffffffu, x);
+        if (WARPS == 1) return x;
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = (int)x;
+        __syncthreads();
+        const uint32_t m = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < WARPS ? (uint32_t)buf[threadIdx.x & 31] : 0u);
+        __syncthreads();
+        return m;
+    }
+    // Exclusive sums over the team's warps of two per-warp numbers.
+    __device__ __forceinline__ void before(int x, int y, int &bx, int &by) const {
+        bx = by = 0;
+        if (WARPS == 1) return;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) buf[warp] = x, buf[WARPS + warp] = y;
+        __syncthreads();
+        bx = __reduce_add_sync(0xffffffffu, lane < warp ? buf[lane] : 0);
+        by = __reduce_add_sync(0xffffffffu, lane < warp ? buf[WARPS + lane] : 0);
+        __syncthreads();
+    }
+};
+
+// The weights' image W and how many keys equal to it stay: the keys above W, `above` many, all do.  `count`
+// gives the number of the older keys whose image is at least a candidate; `most` is the largest image and
+// `differ` has a bit set wherever any two images differ, so that their common leading bits cost no counting.
+// Stops early when exactly `need` keys are at least the candidate: then none equal to W has to be told apart.
+template <class Count>
+__device__ __forceinline__ void find_threshold(int need, uint32_t most, uint32_t differ, Count count, uint32_t &W, int &ties) {
+    int bit = 31 - __clz(differ | 1u);
+    W = bit == 31 ? 0u : most >> (bit + 1) << (bit + 1);
+    for (; bit >= 0; --bit) {
+        const uint32_t cand = W | (1u << bit);
+        const int c = count(cand);
+        if (c >= need) W = cand;
+        if (c == need) {
+            W = cand - 1;   // the need-th largest is at least cand, the next one less
+            ties = 0;
+            return;
+        }
+    }
+    ties = need - (W == 0xffffffffu ? 0 : count(W + 1));
 }
 
-__global__ void __launch_bounds__(EV_THREADS) k_evict_select(const EvArgs p) {
-    __shared__ int buf[EV_WARPS], wgt[EV_WARPS], weq[EV_WARPS];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int h = blockIdx.x, set = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// The weights of the keys that stay, to wo (which may be w): a step's reads are before its writes, and a
+// key's place is never behind it.
+template <int THREADS>
+__device__ __forceinline__ void move_weights(const Team<THREADS> team, const float *w, const int *src, int rows, float *wo) {
+    const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
+    constexpr int U = 4;
+    for (int base = 0; base < rows; base += U * THREADS) {
+        float x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = base + u * THREADS + tid < rows ? w[src[base + u * THREADS + tid]] : 0.0f;
+        team.sync();
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (base + u * THREADS + tid < rows) wo[base + u * THREADS + tid] = x[u];
+    }
+}
+
+// Chooses among n > budget weights w, at most THREADS * E: writes the source index of every key that stays to
+// src (and kept, if not null) and its weight to wo (which may be w).  Warp k of the team holds the 32 E weights
+// from 32 E k on, lane by lane.
+template <int THREADS, int E>
+__device__ __forceinline__ void choose(const Team<THREADS> team, const float *w, int n, int budget, int recent, int *src,
+                                       int *kept, float *wo) {
+    const int lane = threadIdx.x & 31, first = (THREADS == 32 ? 0 : threadIdx.x >> 5) * 32 * E + lane;
+    const int old = n - recent, need = budget - recent;   // 0 <= need < old
+    uint32_t key[E];   // past the older keys: 0, which no candidate reaches
+    float raw[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) raw[j] = first + 32 * j < old ? w[first + 32 * j] : 0.0f;
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        const bool in = first + 32 * j < old;
+        key[j] = in ? weight_key(raw[j]) : 0u;
+        hi = max(hi, key[j]);
+        lo = max(lo, in ? ~key[j] : 0u);
+    }
+    uint32_t W = 0xffffffffu;
+    int ties = 0;
+    if (need > 0) {
+        hi = team.largest(hi);
+        lo = ~team.largest(lo);
+        find_threshold(need, hi, hi ^ lo, [&](uint32_t cand) {
+            int c[4] = {};
+#pragma unroll
+            for (int j = 0; j < E; ++j) c[j & 3] += key[j] >= cand;
+            return team.sum((c[0] + c[1]) + (c[2] + c[3]));
+        }, W, ties);
+    }
+    int ng = 0, ne = 0;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        const bool in = need > 0 && first + 32 * j < old;
+        ng += __popc(__ballot_sync(0xffffffffu, in && key[j] > W));
+        ne += __popc(__ballot_sync(0xffffffffu, in && key[j] == W));
+    }
+    int g, e;
+    team.before(ng, ne, g, e);
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        const int i = first + 32 * j;
+        const bool in = need > 0 && i < old, gt = in && key[j] > W, eq = in && key[j] == W;
+        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+        const int rank = e + __popc(me & below);   // among the keys with image W
+        int at = -1;
+        if (gt || (eq && rank < ties)) at = g + __popc(mg & below) + min(rank, ties);
+        if (i >= old && i < n) at = need + i - old;
+        if (at >= 0) {
+            src[at] = i;
+            if (kept) kept[at] = i;
+        }
+        g += __popc(mg);
+        e += __popc(me);
+    }
+    team.sync();
+    move_weights<THREADS>(team, w, src, budget, wo);
+}
+
+// The same for any n, reading the weights again for every bit.
+__device__ void choose_long(const Team<SEL_THREADS> team, const float *w, int n, int budget, int recent, int *src, float *wo) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int old = n - recent, need = budget - recent;
+    uint32_t W = 0xffffffffu;
+    int ties = 0;
+    if (need > 0)
+        find_threshold(need, 0u, 0xffffffffu, [&](uint32_t cand) {
+            int c = 0;
+            for (int i = tid; i < old; i += SEL_THREADS) c += weight_key(w[i]) >= cand;
+            return team.sum(c);
+        }, W, ties);
+    int g0 = 0, e0 = 0;
+    const uint32_t below = (1u << lane) - 1u;
+    for (int base = 0; base < n; base += SEL_THREADS) {
+        const int i = base + tid;
+        const uint32_t key = i < old ? weight_key(w[i]) : 0u;
+        const bool in = need > 0 && i < old, gt = in && key > W, eq = in && key == W;
+        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+        int g, e;
+        team.before(__popc(mg), __popc(me), g, e);
+        g += g0 + __popc(mg & below);
+        e += e0 + __popc(me & below);
+        int at = -1;
+        if (gt || (eq && e < ties)) at = g + min(e, ties);
+        if (i >= old && i < n) at = need + i - old;
+        if (at >= 0) src[at] = i;
+        g0 += team.sum(lane == 0 ? __popc(mg) : 0);
+        e0 += team.sum(lane == 0 ? __popc(me) : 0);
+    }
+    move_weights<SEL_THREADS>(team, w, src, budget, wo);
+}
+
+__device__ __forceinline__ int count_of(const EvArgs &p, int set, bool report) {
     int n = p.max_keys;
     if (p.n_keys) {
-        const int want = __ldg(p.n_keys + set);
+        const int want = __ldcg(p.n_keys + set);
         n = min(max(want, 0), p.max_keys);
-        if (want != n && h == 0 && tid == 0) atomicCAS(p.status, 0, WH_EBOUNDS);
+        if (want != n && report) atomicCAS(p.status, 0, WH_EBOUNDS);
     }
-    if (h == 0 && tid == 0) p.count[set] = n;
+    return n;
+}
+
+// One head of one set: choose (warp 0, or the whole block for more than 32 E keys), then move.
+template <int CHOOSERS, int E>
+__global__ void __launch_bounds__(SM_THREADS) k_evict_small(const EvArgs p) {
+    extern __shared__ int src[];   // [budget]
+    __shared__ int buf[2 * SM_THREADS / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int h = blockIdx.x, set = blockIdx.y, tid = threadIdx.x;
+    const int n = count_of(p, set, h == 0 && tid == 0), rows = min(n, p.budget);
+    if (p.n_out && h == 0 && tid == 0) p.n_out[set] = rows;
     const long long sh = (long long)set * p.n_head + h;
     const float *w = p.weight + sh * p.max_keys;
     float *wo = p.weight_out + sh * p.out_keys;
-    int *src = p.kept + sh * p.budget;
-    if (n <= p.budget) {   // everything stays
-        for (int i = tid; i < n; i += EV_THREADS) {
+    int *kept = p.kept ? p.kept + sh * p.budget : nullptr;
+    const bool all = n <= p.budget;   // everything stays
+    if (all) {
+        for (int i = tid; i < n; i += SM_THREADS) {
             src[i] = i;
-            if (!p.in_place) wo[i] = __ldg(w + i);
+            if (kept) kept[i] = i;
+            if (!p.in_place) wo[i] = w[i];
         }
-        return;
+    } else if (CHOOSERS != 32 || tid < 32) {
+        choose<CHOOSERS, E>(Team<CHOOSERS>{buf}, w, n, p.budget, p.recent, src, kept, wo);
     }
-    const int old = n - p.recent, need = p.budget - p.recent;   // 0 <= need < old
-    // the need-th largest image of the older keys: the largest W with at least need images >= W
-    uint32_t W = 0;
-    if (need > 0) {
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t cand = W | (1u << bit);
-            int c = 0;
-            for (int i = tid; i < old; i += EV_THREADS) c += weight_key(w[i]) >= cand;
-            if (block_sum(c, buf) >= need) W = cand;
-        }
-    } else {
-        W = 0xffffffffu;
-    }
-    int above = 0;
-    for (int i = tid; i < old; i += EV_THREADS) above += weight_key(w[i]) > W;
-    above = need > 0 ? block_sum(above, buf) : 0;
-    const int ties = need - above;   // how many of the keys with image W stay
-    // number what stays, EV_THREADS keys at a time; within the cache every key moves towards the front, so
-    // writing behind the reads is safe
-    int gt0 = 0, eq0 = 0;
-    for (int base = 0; base < old; base += EV_THREADS) {
-        const int i = base + tid;
-        const float x = i < old ? w[i] : 0.0f;
-        const uint32_t key = weight_key(x);
-        const bool gt = i < old && need > 0 && key > W, eq = i < old && need > 0 && key == W;
-        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) {
-            wgt[warp] = __popc(mg);
-            weq[warp] = __popc(me);
-        }
-        __syncthreads();
-        int g = gt0, e = eq0;
-        for (int j = 0; j < EV_WARPS; ++j) {
-            if (j < warp) {
-                g += wgt[j];
-                e += weq[j];
+    if (all && p.in_place) return;
+    __syncthreads();
+    // rows in steps of U * SM_THREADS / 8; thread x takes piece x % 8 of keys and values
+    constexpr int U = 4, STEP = SM_THREADS / 8;
+    const long long in0 = (long long)set * p.set_stride + h * 64 + 8 * (tid & 7);
+    const long long to0 = (long long)set * p.out_set_stride + h * 64 + 8 * (tid & 7);
+    for (int base = tid >> 3; base < (rows + U * STEP - 1) / (U * STEP) * (U * STEP); base += U * STEP) {
+        uint4 a[U], b[U];
+        int t[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = base + u * STEP;
+            t[u] = j < rows ? src[j] : -1;
+            if (p.in_place && t[u] == j) t[u] = -1;   // where it was
+            if (t[u] >= 0) {
+                a[u] = __ldcg(reinterpret_cast<const uint4 *>(p.k + in0 + t[u] * p.row_stride));
+                b[u] = __ldcg(reinterpret_cast<const uint4 *>(p.v + in0 + t[u] * p.row_stride));
             }
-            gt0 += wgt[j];
-            eq0 += weq[j];
         }
-        const uint32_t below = (1u << lane) - 1u;
-        g += __popc(mg & below);
-        e += __popc(me & below);
-        if (gt || (eq && e < ties)) {
-            const int at = g + min(e, ties);
-            src[at] = i;
-            wo[at] = x;
-        }
-        __syncthreads();
+        if (p.in_place) __syncthreads();   // (the trip count is the block's)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t[u] >= 0) {
+                const long long to = to0 + (long long)(base + u * STEP) * p.out_row_stride;
+                *reinterpret_cast<uint4 *>(p.k_out + to) = a[u];
+                *reinterpret_cast<uint4 *>(p.v_out + to) = b[u];
+            }
     }
-    for (int base = 0; base < p.recent; base += EV_THREADS) {
-        const int i = base + tid;
-        const float x = i < p.recent ? w[old + i] : 0.0f;
-        __syncthreads();
-        if (i < p.recent) {
-            src[need + i] = old + i;
-            wo[need + i] = x;
+}
+
+// Chooses only: a warp (of four) or a block per head and set.
+template <int CHOOSERS, int E>
+__global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS) k_evict_select(const EvArgs p) {
+    __shared__ int buf[2 * SEL_THREADS / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = CHOOSERS == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const long long sh = CHOOSERS == 32 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x;
+    if (sh >= (long long)p.n_set * p.n_head) return;
+    const int set = (int)(sh / p.n_head), h = (int)(sh % p.n_head);
+    const int n = count_of(p, set, h == 0 && tid == 0);
+    if (h == 0 && tid == 0) p.count[set] = n;
+    const float *w = p.weight + sh * p.max_keys;
+    float *wo = p.weight_out + sh * p.out_keys;
+    int *src = p.kept + sh * p.budget;
+    const Team<CHOOSERS> team{buf};
+    if (n <= p.budget) {   // everything stays
+        for (int i = tid; i < n; i += CHOOSERS) {
+            src[i] = i;
+            if (!p.in_place) wo[i] = w[i];
         }
+    } else if constexpr (E > 0) {
+        choose<CHOOSERS, E>(team, w, n, p.budget, p.recent, src, nullptr, wo);
+    } else {
+        choose_long(team, w, n, p.budget, p.recent, src, wo);
     }
 }
 
@@ -145,22 +324,36 @@ __global__ void __launch_bounds__(MV_THREADS) k_evict_move(const EvArgs p) {
     if (blockIdx.x == 0 && threadIdx.x == 0) p.n_out[set] = n;
     const int j0 = blockIdx.x * MV_ROWS, rows = min(MV_ROWS, n - j0);
     if (rows <= 0) return;
-    const int per_row = p.n_head * 8;   // 16-byte pieces of a row
-    for (int i = threadIdx.x; i < rows * per_row; i += MV_THREADS) {
-        const int j = j0 + i / per_row, x = i % per_row, h = x >> 3;
-        const int t = __ldcg(p.kept + ((long long)set * p.n_head + h) * p.budget + j);
-        const long long from = (long long)set * p.set_stride + (long long)t * p.row_stride + 8 * x;
-        const long long to = (long long)set * p.out_set_stride + (long long)j * p.out_row_stride + 8 * x;
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p.k + from));
-        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(p.v + from));
-        *reinterpret_cast<uint4 *>(p.k_out + to) = a;
-        *reinterpret_cast<uint4 *>(p.v_out + to) = b;
+    const int per_row = p.n_head * 8, todo = rows * per_row;   // 16-byte pieces
+    constexpr int U = 4;
+    for (int base = threadIdx.x; base < todo; base += U * MV_THREADS) {
+        int x[U], j[U], t[U];
+        uint4 a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = base + u * MV_THREADS;
+            j[u] = j0 + i / per_row;
+            x[u] = i % per_row;
+            t[u] = i < todo ? __ldcg(p.kept + ((long long)set * p.n_head + (x[u] >> 3)) * p.budget + j[u]) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t[u] >= 0) {
+                const long long from = (long long)set * p.set_stride + (long long)t[u] * p.row_stride + 8 * x[u];
+                a[u] = __ldcg(reinterpret_cast<const uint4 *>(p.k + from));
+                b[u] = __ldcg(reinterpret_cast<const uint4 *>(p.v + from));
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t[u] >= 0) {
+                const long long to = (long long)set * p.out_set_stride + (long long)j[u] * p.out_row_stride + 8 * x[u];
+                *reinterpret_cast<uint4 *>(p.k_out + to) = a[u];
+                *reinterpret_cast<uint4 *>(p.v_out + to) = b[u];
+            }
     }
 }
 
-// The same within the cache: one block per (head, set, keys or values) goes up the rows.  A row's source
-// lies at or behind it, so what later rows read is never overwritten; the barrier holds back the writes of
-// a step until its reads are done.
+// The same within the cache, one block per (head, set, keys or values).
 __global__ void __launch_bounds__(SH_THREADS) k_evict_shift(const EvArgs p) {
     pdl_wait();
     const int h = blockIdx.x, set = blockIdx.y, n0 = __ldcg(p.count + set), n = min(n0, p.budget);
@@ -168,17 +361,29 @@ __global__ void __launch_bounds__(SH_THREADS) k_evict_shift(const EvArgs p) {
     if (n0 <= p.budget) return;
     __nv_bfloat16 *x = (blockIdx.z ? p.v_out : p.k_out) + (long long)set * p.set_stride + h * 64 + 8 * (threadIdx.x & 7);
     const int *src = p.kept + ((long long)set * p.n_head + h) * p.budget;
-    for (int base = 0; base < n; base += SH_ROWS) {
-        const int j = base + (threadIdx.x >> 3);
-        int t = j;
-        uint4 a = make_uint4(0, 0, 0, 0);
-        if (j < n) {
-            t = __ldcg(src + j);
-            if (t != j) a = *reinterpret_cast<const uint4 *>(x + (long long)t * p.row_stride);
+    constexpr int U = 4, STEP = SH_THREADS / 8;
+    for (int base = threadIdx.x >> 3; base < (n + U * STEP - 1) / (U * STEP) * (U * STEP); base += U * STEP) {
+        int t[U];
+        uint4 a[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) t[u] = base + u * STEP < n ? __ldcg(src + base + u * STEP) : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t[u] == base + u * STEP) t[u] = -1;   // where it was
+            if (t[u] >= 0) a[u] = __ldcg(reinterpret_cast<const uint4 *>(x + (long long)t[u] * p.row_stride));
         }
         __syncthreads();
-        if (t != j) *reinterpret_cast<uint4 *>(x + (long long)j * p.row_stride) = a;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t[u] >= 0) *reinterpret_cast<uint4 *>(x + (long long)(base + u * STEP) * p.row_stride) = a[u];
     }
+}
+
+// The new counts, where they overwrite the old ones that k_evict_small's blocks read.
+__global__ void k_evict_counts(const EvArgs p, int *n_out) {
+    pdl_wait();
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.n_set; i += gridDim.x * blockDim.x)
+        n_out[i] = min(count_of(p, i, false), p.budget);
 }
 
 size_t up256e(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -241,6 +446,8 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
             for (const Span &y : to)
                 if (meet(x, y)) return WH_EINVAL;
     }
+    if (cache->n_keys && n_out != cache->n_keys && meet(span_of(n_out, cache->n_set, 4), span_of(cache->n_keys, cache->n_set, 4)))
+        return WH_EINVAL;
     if (ws_bytes < wh_cache_evict_workspace(cache->n_set, n_kv_head, budget)) return WH_ENOSPC;
     DevCtl ctl;
     int num_sms = 0;
@@ -260,7 +467,6 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
     a.n_keys = cache->n_keys;
     a.n_out = n_out;
     a.count = static_cast<int *>(workspace);
-    a.kept = kept ? kept : reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + up256e((size_t)cache->n_set * 4));
     a.max_keys = cache->max_keys;
     a.out_keys = o->max_keys;
     a.n_set = cache->n_set;
@@ -270,29 +476,40 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
     a.in_place = out == nullptr;
     a.status = ctl.status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int most = budget < a.max_keys ? budget : a.max_keys;
+    const dim3 heads(n_kv_head, a.n_set);
+    int rc;
     trace_begin(TR_DEC_OTHER, s);
-    k_evict_select<<<dim3(n_kv_head, a.n_set), EV_THREADS, 0, s>>>(a);
-    count_launch();
-    cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    lc.stream = s;
-    cudaError_t e;
-    if (a.in_place) {
-        lc.gridDim = dim3(n_kv_head, a.n_set, 2);
-        lc.blockDim = dim3(SH_THREADS);
-        e = cudaLaunchKernelEx(&lc, k_evict_shift, a);
+    const long long items = (long long)n_kv_head * a.n_set;
+    // one kernel for short caches of as many heads as are resident at once, unless few of them move many rows
+    if (a.max_keys <= SM_MOST && items <= SM_HEADS && (most <= SM_ROWS || 2 * items >= SM_HEADS)) {
+        const bool same = n_out == a.n_keys;
+        a.kept = kept;
+        a.n_out = same ? nullptr : n_out;
+        auto *kernel = a.max_keys <= 512 ? k_evict_small<32, 16>
+                       : a.max_keys <= 1024 ? k_evict_small<32, 32> : k_evict_small<SM_THREADS, 8>;
+        rc = launch_ex(kernel, heads, SM_THREADS, most * (int)sizeof(int), 1, false, s, a);
+        if (!rc && same) rc = launch_ex(k_evict_counts, dim3((a.n_set + 255) / 256), 256, 0, 1, true, s, a, n_out);
     } else {
-        const int most = budget < a.max_keys ? budget : a.max_keys;
-        lc.gridDim = dim3((most + MV_ROWS - 1) / MV_ROWS, a.n_set);
-        lc.blockDim = dim3(MV_THREADS);
-        e = cudaLaunchKernelEx(&lc, k_evict_move, a);
+        a.kept = kept ? kept : reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + up256e((size_t)cache->n_set * 4));
+        const dim3 warps((unsigned)((items + 3) / 4)), blocks((unsigned)items);
+        if (a.max_keys <= 512)
+            rc = launch_ex(k_evict_select<32, 16>, warps, 128, 0, 1, false, s, a);
+        else if (a.max_keys <= 1024)
+            rc = launch_ex(k_evict_select<32, 32>, warps, 128, 0, 1, false, s, a);
+        else if (a.max_keys <= 2048)
+            rc = launch_ex(k_evict_select<256, 8>, blocks, 256, 0, 1, false, s, a);
+        else if (a.max_keys <= 8192)
+            rc = launch_ex(k_evict_select<SEL_THREADS, 8>, blocks, SEL_THREADS, 0, 1, false, s, a);
+        else if (a.max_keys <= SEL_HELD * SEL_THREADS)
+            rc = launch_ex(k_evict_select<SEL_THREADS, SEL_HELD>, blocks, SEL_THREADS, 0, 1, false, s, a);
+        else
+            rc = launch_ex(k_evict_select<SEL_THREADS, 0>, blocks, SEL_THREADS, 0, 1, false, s, a);
+        if (!rc)
+            rc = a.in_place ? launch_ex(k_evict_shift, dim3(n_kv_head, a.n_set, 2), SH_THREADS, 0, 1, true, s, a)
+                            : launch_ex(k_evict_move, dim3((most + MV_ROWS - 1) / MV_ROWS, a.n_set), MV_THREADS, 0, 1, true, s, a);
     }
-    count_launch();
     const double held = (double)a.n_set * n_kv_head;
-    trace_end(TR_DEC_OTHER, s, 0.0, held * (4.0 * a.max_keys + 520.0 * (budget < a.max_keys ? budget : a.max_keys)));
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? WH_OK : WH_ECUDA;
+    trace_end(TR_DEC_OTHER, s, 0.0, held * (4.0 * a.max_keys + 520.0 * most));
+    return rc ? rc : cudaGetLastError() == cudaSuccess ? WH_OK : WH_ECUDA;
 }

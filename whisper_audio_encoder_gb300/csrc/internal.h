@@ -122,4 +122,31 @@ void trace_begin(int cls, cudaStream_t s);
 void trace_end(int cls, cudaStream_t s, double flops, double bytes);
 void count_launch(int n = 1);
 
+// One launch with optional programmatic serialization and cluster size along x.
+template <class... F, class... A>
+int launch_ex(void (*kernel)(F...), dim3 grid, int threads, int smem, int cluster, bool pdl, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    lc.attrs = attr;
+    lc.numAttrs = n;
+    if (cudaLaunchKernelEx(&lc, kernel, F(args)...) != cudaSuccess) return WH_ECUDA;
+    count_launch();
+    return WH_OK;
+}
+
 }  // namespace wh

@@ -231,32 +231,6 @@ struct PtMaps {
 };
 int prefix_tc_maps(const PaArgs &a, PtMaps *m);
 int prefix_tc_launch(const PaArgs &a, const PtMaps &m, cudaStream_t s);
-// One launch with optional programmatic serialization and cluster size along x.
-template <class... F, class... A>
-int launch_ex(void (*kernel)(F...), dim3 grid, int threads, int smem, int cluster, bool pdl, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr[2];
-    int n = 0;
-    if (pdl) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    if (cluster > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = cluster;
-        attr[n].val.clusterDim.y = 1;
-        attr[n++].val.clusterDim.z = 1;
-    }
-    lc.gridDim = grid;
-    lc.blockDim = dim3(threads);
-    lc.dynamicSmemBytes = smem;
-    lc.stream = s;
-    lc.attrs = attr;
-    lc.numAttrs = n;
-    if (cudaLaunchKernelEx(&lc, kernel, F(args)...) != cudaSuccess) return WH_ECUDA;
-    count_launch();
-    return WH_OK;
-}
 int prefix_tc_prepare();
 
 }  // namespace wh
