@@ -25,7 +25,7 @@ constexpr int SM_HEADS = 3 * 152;    // blocks of it that are resident at once
 constexpr int SEL_THREADS = 1024;    // k_evict_select
 constexpr int SEL_HELD = 32;         // keys that a thread of it holds: longer caches are read again for every bit
 constexpr int MV_THREADS = 256;
-constexpr int MV_ROWS = 8;           // rows of a block of k_evict_move
+constexpr int MV_PIECES = 1024;      // 16-byte pieces (of keys, and of values) of a block of k_evict_move
 constexpr int SH_THREADS = 512;      // k_evict_shift
 
 struct EvArgs {
@@ -162,31 +162,46 @@ __device__ __forceinline__ void choose(const Team<THREADS> team, const float *w,
             return team.sum((c[0] + c[1]) + (c[2] + c[3]));
         }, W, ties);
     }
-    int ng = 0, ne = 0;
+    // number what stays: those above W, the first `ties` equal to W, the recent ones
+    int g = 0, e = 0;
+    if (THREADS > 32) {
+        int ng = 0, ne = 0;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-        const bool in = need > 0 && first + 32 * j < old;
-        ng += __popc(__ballot_sync(0xffffffffu, in && key[j] > W));
-        ne += __popc(__ballot_sync(0xffffffffu, in && key[j] == W));
+        for (int j = 0; j < E; ++j) {
+            const bool in = need > 0 && first + 32 * j < old;
+            ng += __popc(__ballot_sync(0xffffffffu, in && key[j] > W));
+            if (ties > 0) ne += __popc(__ballot_sync(0xffffffffu, in && key[j] == W));
+        }
+        team.before(ng, ne, g, e);
     }
-    int g, e;
-    team.before(ng, ne, g, e);
     const uint32_t below = (1u << lane) - 1u;
+    const int steps = (n - (first - lane) + 31) / 32;   // of this warp that hold keys at all
 #pragma unroll
     for (int j = 0; j < E; ++j) {
+        if (j >= steps) break;
         const int i = first + 32 * j;
-        const bool in = need > 0 && i < old, gt = in && key[j] > W, eq = in && key[j] == W;
-        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        const int rank = e + __popc(me & below);   // among the keys with image W
-        int at = -1;
-        if (gt || (eq && rank < ties)) at = g + __popc(mg & below) + min(rank, ties);
-        if (i >= old && i < n) at = need + i - old;
-        if (at >= 0) {
+        const bool in = need > 0 && i < old;
+        bool stays = in && key[j] > W;
+        int at = g;
+        const uint32_t mg = __ballot_sync(0xffffffffu, stays);
+        at += __popc(mg & below);
+        g += __popc(mg);
+        if (ties > 0) {
+            const bool eq = in && key[j] == W;
+            const uint32_t me = __ballot_sync(0xffffffffu, eq);
+            const int rank = e + __popc(me & below);   // among the keys equal to W
+            stays = stays || (eq && rank < ties);
+            at += min(rank, ties);
+            e += __popc(me);
+        }
+        if (i >= old) {
+            stays = i < n;
+            at = need + i - old;
+        }
+        if (stays) {
             src[at] = i;
             if (kept) kept[at] = i;
         }
-        g += __popc(mg);
-        e += __popc(me);
     }
     team.sync();
     move_weights<THREADS>(team, w, src, budget, wo);
@@ -322,35 +337,35 @@ __global__ void __launch_bounds__(MV_THREADS) k_evict_move(const EvArgs p) {
     pdl_wait();
     const int set = blockIdx.y, n = min(__ldcg(p.count + set), p.budget);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.n_out[set] = n;
-    const int j0 = blockIdx.x * MV_ROWS, rows = min(MV_ROWS, n - j0);
-    if (rows <= 0) return;
-    const int per_row = p.n_head * 8, todo = rows * per_row;   // 16-byte pieces
-    constexpr int U = 4;
-    for (int base = threadIdx.x; base < todo; base += U * MV_THREADS) {
-        int x[U], j[U], t[U];
-        uint4 a[U], b[U];
+    const int per_row = p.n_head * 8;   // 16-byte pieces of a row
+    const long long todo = (long long)n * per_row, base = (long long)blockIdx.x * MV_PIECES + threadIdx.x;
+    constexpr int U = MV_PIECES / MV_THREADS;
+    int x[U], j[U], t[U];
+    uint4 a[U], b[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = base + u * MV_THREADS;
-            j[u] = j0 + i / per_row;
-            x[u] = i % per_row;
-            t[u] = i < todo ? __ldcg(p.kept + ((long long)set * p.n_head + (x[u] >> 3)) * p.budget + j[u]) : -1;
+    for (int u = 0; u < U; ++u) {
+        const long long i = base + u * MV_THREADS;
+        t[u] = -1;
+        if (i < todo) {
+            j[u] = (int)(i / per_row);
+            x[u] = (int)(i - (long long)j[u] * per_row);
+            t[u] = __ldcg(p.kept + ((long long)set * p.n_head + (x[u] >> 3)) * p.budget + j[u]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (t[u] >= 0) {
+            const long long from = (long long)set * p.set_stride + (long long)t[u] * p.row_stride + 8 * x[u];
+            a[u] = __ldcg(reinterpret_cast<const uint4 *>(p.k + from));
+            b[u] = __ldcg(reinterpret_cast<const uint4 *>(p.v + from));
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t[u] >= 0) {
-                const long long from = (long long)set * p.set_stride + (long long)t[u] * p.row_stride + 8 * x[u];
-                a[u] = __ldcg(reinterpret_cast<const uint4 *>(p.k + from));
-                b[u] = __ldcg(reinterpret_cast<const uint4 *>(p.v + from));
-            }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t[u] >= 0) {
-                const long long to = (long long)set * p.out_set_stride + (long long)j[u] * p.out_row_stride + 8 * x[u];
-                *reinterpret_cast<uint4 *>(p.k_out + to) = a[u];
-                *reinterpret_cast<uint4 *>(p.v_out + to) = b[u];
-            }
-    }
+    for (int u = 0; u < U; ++u)
+        if (t[u] >= 0) {
+            const long long to = (long long)set * p.out_set_stride + (long long)j[u] * p.out_row_stride + 8 * x[u];
+            *reinterpret_cast<uint4 *>(p.k_out + to) = a[u];
+            *reinterpret_cast<uint4 *>(p.v_out + to) = b[u];
+        }
 }
 
 // The same within the cache, one block per (head, set, keys or values).
@@ -507,7 +522,8 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
             rc = launch_ex(k_evict_select<SEL_THREADS, 0>, blocks, SEL_THREADS, 0, 1, false, s, a);
         if (!rc)
             rc = a.in_place ? launch_ex(k_evict_shift, dim3(n_kv_head, a.n_set, 2), SH_THREADS, 0, 1, true, s, a)
-                            : launch_ex(k_evict_move, dim3((most + MV_ROWS - 1) / MV_ROWS, a.n_set), MV_THREADS, 0, 1, true, s, a);
+                            : launch_ex(k_evict_move, dim3((unsigned)(((long long)most * n_kv_head * 8 + MV_PIECES - 1) / MV_PIECES), a.n_set),
+                                        MV_THREADS, 0, 1, true, s, a);
     }
     const double held = (double)a.n_set * n_kv_head;
     trace_end(TR_DEC_OTHER, s, 0.0, held * (4.0 * a.max_keys + 520.0 * most));
