@@ -13,10 +13,10 @@ namespace {
 constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = 32 * PA_WARPS;
 constexpr int PA_TILE = 16;        // rows of a block
-constexpr int PA_KEYS = 16;        // keys of one warp step
-constexpr int PA_STAGES = 4;       // warp steps in flight
-constexpr int PA_STEP_BYTES = 2 * PA_KEYS * 128;                     // keys and values of one warp step
-constexpr int PA_RING = PA_STAGES * PA_STEP_BYTES;                   // of one warp
+constexpr int PA_KEYS = 32;        // keys of one warp step
+constexpr int PA_SLOT_KEYS = 16;   // of one slot of a warp's ring
+constexpr int PA_SLOT = 2 * PA_SLOT_KEYS * 128;   // bytes: keys, then values
+constexpr int PA_RING = 4 * PA_SLOT;
 constexpr int PA_SMEM = PA_WARPS * PA_RING;
 constexpr int SO_ROW = 68;         // floats a row of the warps' staged results
 constexpr int PM_ROWS = 8;         // rows of one merge block (16 threads a row)
@@ -30,17 +30,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t to_tf32(float x) {
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-    return r;
+// Four 8 x 8 matrices of bf16 from shared memory, transposed: lane l gives the address of row l % 8 of matrix
+// l / 8 and gets elements (2c, g) and (2c + 1, g) of each.
+__device__ __forceinline__ void ldmatrix_trans(uint32_t a, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(a)
+                 : "memory");
 }
 
 // 16 bytes global -> shared, the last 16 - bytes of them zeros.
@@ -151,99 +147,94 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     const int full = OWN ? nk - (p.nq - 1) : nk;   // every row sees the keys before this one
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, o[8][4] = {};
-    // Each warp copies its steps of 16 keys and values into a ring of its own, PA_STAGES - 1 ahead: four rows
-    // of 128 bytes an instruction, zeros past the range.  The 16-byte pieces of a row are permuted (keys: by
-    // the row's lowest bit, values: by the next two) so that the fragment reads below meet no bank twice.
+    // Each warp copies its keys and values into a ring of its own, 16 at a time: four rows of 128 bytes an
+    // instruction, zeros past the range.  The 16-byte pieces of a row are permuted (keys: by the row's lowest
+    // bit, values: by the lowest three) so that the fragment reads below meet no bank twice.  A step takes two
+    // slots of the four while the next two are on their way.
     extern __shared__ __align__(128) uint8_t ring_all[];
     const uint32_t ring = smem_u32(ring_all) + warp * PA_RING;
     const int crow = lane >> 3, piece = lane & 7;
     const __nv_bfloat16 *kb = ks.k + (long long)set * ks.set_stride + rw.hk * 64 + 8 * piece;
     const __nv_bfloat16 *vb = ks.v + (long long)set * ks.set_stride + rw.hk * 64 + 8 * piece;
     const long long step4 = 4 * ks.row_stride;   // four rows on
-    auto fetch = [&](int t, int slot) {
-        if (t < k1) {
-            const uint32_t dk = ring + slot * PA_STEP_BYTES + crow * 128 + ((piece ^ ((crow & 1) << 2)) << 4);
-            const uint32_t dv = ring + slot * PA_STEP_BYTES + PA_KEYS * 128 + crow * 128;
-            const long long at = (long long)(t + crow) * ks.row_stride;
-            const __nv_bfloat16 *k = kb + at, *v = vb + at;
-            if (t + PA_KEYS <= k1) {
+    const uint32_t ck = ring + crow * 128 + ((piece ^ ((crow & 1) << 2)) << 4);
+    const uint32_t cv = ring + PA_SLOT_KEYS * 128 + crow * 128 + ((piece ^ crow) << 4);
+    auto fetch = [&](int t, int slot) {   // keys t .. t + 15
+        if (t >= k1) return;
+        const uint32_t dk = ck + slot * PA_SLOT, dv = cv + slot * PA_SLOT;
+        const long long at = (long long)(t + crow) * ks.row_stride;
+        const __nv_bfloat16 *k = kb + at, *v = vb + at;
+        if (t + PA_SLOT_KEYS <= k1) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i, k += step4, v += step4) {
-                    cp_async16(dk + i * 512, k, 16u);
-                    cp_async16(dv + i * 512 + ((piece ^ ((4 * i + crow) & 6)) << 4), v, 16u);
-                }
-            } else {
+            for (int i = 0; i < 4; ++i, k += step4, v += step4) {
+                cp_async16(dk + i * 512, k, 16u);
+                cp_async16((dv + i * 512) ^ ((i & 1) << 6), v, 16u);   // rows 4i + crow: the third bit is i's lowest
+            }
+        } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i, k += step4, v += step4) {
-                    const bool in = t + 4 * i + crow < k1;
-                    cp_async16(dk + i * 512, in ? k : kb, in ? 16u : 0u);
-                    cp_async16(dv + i * 512 + ((piece ^ ((4 * i + crow) & 6)) << 4), in ? v : vb, in ? 16u : 0u);
-                }
+            for (int i = 0; i < 4; ++i, k += step4, v += step4) {
+                const bool in = t + 4 * i + crow < k1;
+                cp_async16(dk + i * 512, in ? k : kb, in ? 16u : 0u);
+                cp_async16((dv + i * 512) ^ ((i & 1) << 6), in ? v : vb, in ? 16u : 0u);
             }
         }
-        cp_async_commit();
     };
     float *scores = reinterpret_cast<float *>(ring_all + PA_SMEM) + (warp / wpi) * p.score_floats;
     const int stride = wpi * PA_KEYS;
-    int t0 = k0 + iw * PA_KEYS, slot = 0;
-#pragma unroll
-    for (int i = 0; i < PA_STAGES - 1; ++i) fetch(t0 + i * stride, i);
+    int t0 = k0 + iw * PA_KEYS, half_ring = 0;
+    fetch(t0, 0);
+    fetch(t0 + PA_SLOT_KEYS, 1);
+    cp_async_commit();
     for (; t0 < k1; t0 += stride) {
-        cp_async_wait<PA_STAGES - 2>();
-        __syncwarp();   // every lane's copies of this step have landed, and every lane is done with the last one
-        fetch(t0 + (PA_STAGES - 1) * stride, slot == 0 ? PA_STAGES - 1 : slot - 1);
-        // keys g, 8 + g for the scores; values 2c, 2c + 1, 8 + 2c, 9 + 2c
-        const uint32_t sk = ring + slot * PA_STEP_BYTES, sv = sk + PA_KEYS * 128;
-        uint4 kr[2][2], vr[2][2];
+        fetch(t0 + stride, 2 - half_ring);
+        fetch(t0 + stride + PA_SLOT_KEYS, 3 - half_ring);
+        cp_async_commit();
+        cp_async_wait<1>();
+        __syncwarp();   // every lane's copies of this step have landed
+        const uint32_t base = ring + half_ring * PA_SLOT;
+        const int slots = t0 + PA_SLOT_KEYS < k1 ? 2 : 1;   // the second may hold nothing at all
+        // scores of keys 8j + 2c, 8j + 2c + 1 for rows g (0, 1) and g + 8 (2, 3)
+        float s[4][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t kk = sk + (8 * j + g) * 128;
-            kr[j][0] = lds128(kk + ((c ^ ((g & 1) << 2)) << 4));
-            kr[j][1] = lds128(kk + (((c + 4) ^ ((g & 1) << 2)) << 4));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 8 * j + 2 * c + i;
-                vr[j][i] = lds128(sv + r * 128 + ((g ^ (r & 6)) << 4));
+        for (int j = 0; j < 4; ++j) {
+            if (j < 2 * slots) {
+                const uint32_t kk = base + (j >> 1) * PA_SLOT + (8 * (j & 1) + g) * 128;
+                const uint4 x = lds128(kk + ((c ^ ((g & 1) << 2)) << 4)), y = lds128(kk + (((c + 4) ^ ((g & 1) << 2)) << 4));
+                score8(qa, x, y, s[j]);
+            } else {
+                s[j][0] = s[j][1] = s[j][2] = s[j][3] = -INFINITY;
             }
         }
-        slot = slot == PA_STAGES - 1 ? 0 : slot + 1;
-        float s[2][4];
-        score8(qa, kr[0][0], kr[0][1], s[0]);
-        score8(qa, kr[1][0], kr[1][1], s[1]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][i] *= PA_SCALE;
         if (t0 + PA_KEYS > min(k1, full)) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = t0 + 8 * j + 2 * c + (i & 1);
-                    if (key >= min(k1, lim[i >> 1])) s[j][i] = -INFINITY;
-                }
+                for (int i = 0; i < 4; ++i)
+                    if (t0 + 8 * j + 2 * c + (i & 1) >= min(k1, lim[i >> 1])) s[j][i] = -INFINITY;
         }
         if (OWN && p.score_floats) {   // for the weights, once the row's sum is known
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
                     if (g + 8 * half < rw.n)
                         *reinterpret_cast<float2 *>(scores + (g + 8 * half) * ks.chunk + t0 - k0 + 8 * j + 2 * c) =
                             make_float2(s[j][2 * half], s[j][2 * half + 1]);
         }
-        float mx[2], mn[2];
+        float mn[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            mx[half] = fmaxf(fmaxf(s[0][2 * half], s[0][2 * half + 1]), fmaxf(s[1][2 * half], s[1][2 * half + 1]));
-            mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 1));
-            mx[half] = fmaxf(mx[half], __shfl_xor_sync(0xffffffffu, mx[half], 2));
-            mn[half] = fmaxf(m[half], mx[half]);
+            const int i = 2 * half;
+            float mx = fmaxf(fmaxf(fmaxf(s[0][i], s[0][i + 1]), fmaxf(s[1][i], s[1][i + 1])),
+                             fmaxf(fmaxf(s[2][i], s[2][i + 1]), fmaxf(s[3][i], s[3][i + 1])));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            mn[half] = fmaxf(m[half], mx);
         }
         if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {   // some row's maximum moved
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const float f = m[half] == -INFINITY ? 0.0f : ex2_approx(m[half] - mn[half]);
+                const float f = m[half] == -INFINITY ? 0.0f : ex2_approx((m[half] - mn[half]) * PA_SCALE);
                 l[half] *= f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -253,24 +244,34 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
                 m[half] = mn[half];
             }
         }
-        const float ms[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+        const float mc[2] = {m[0] == -INFINITY ? 0.0f : -m[0] * PA_SCALE, m[1] == -INFINITY ? 0.0f : -m[1] * PA_SCALE};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t pt[4];
+        for (int h = 0; h < 2; ++h) {
+            if (h == 1 && slots == 1) break;
+            // the weights as a sum of two bf16 each: 16 bits of mantissa in two products of 8
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = ex2_approx(s[j][i] - ms[i >> 1]);
-                l[i >> 1] += e;
-                pt[i] = to_tf32(e);   // 11 bits of mantissa: an eighth of the output's rounding
+            for (int x = 0; x < 4; ++x) {   // rows g, g + 8 of keys 2c, 2c + 1, then of keys 8 + 2c, 9 + 2c
+                const float *sx = s[2 * h + (x >> 1)] + 2 * (x & 1);
+                const float e0 = ex2_approx(fmaf(sx[0], PA_SCALE, mc[x & 1]));
+                const float e1 = ex2_approx(fmaf(sx[1], PA_SCALE, mc[x & 1]));
+                l[x & 1] += e0 + e1;
+                hi[x] = pack_bf16(e0, e1);
+                lo[x] = pack_bf16(e0 - __uint_as_float(hi[x] << 16), e1 - __uint_as_float(hi[x] & 0xffff0000u));
             }
-            const uint32_t a0[4] = {vr[j][0].x, vr[j][0].y, vr[j][0].z, vr[j][0].w};
-            const uint32_t a1[4] = {vr[j][1].x, vr[j][1].y, vr[j][1].z, vr[j][1].w};
+            const uint32_t vrow = base + h * PA_SLOT + PA_SLOT_KEYS * 128 + (lane & 15) * 128;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                mma_tf32(o[2 * w], pt[0], pt[2], pt[1], pt[3], a0[w] << 16, a1[w] << 16);
-                mma_tf32(o[2 * w + 1], pt[0], pt[2], pt[1], pt[3], a0[w] & 0xffff0000u, a1[w] & 0xffff0000u);
+            for (int w = 0; w < 4; ++w) {   // dims 16w .. 16w + 15
+                uint32_t b0, b1, b2, b3;
+                ldmatrix_trans(vrow + (((2 * w + (lane >> 4)) ^ (lane & 7)) << 4), b0, b1, b2, b3);
+                mma_bf16(o[2 * w], hi[0], hi[1], hi[2], hi[3], b0, b1);
+                mma_bf16(o[2 * w + 1], hi[0], hi[1], hi[2], hi[3], b2, b3);
+                mma_bf16(o[2 * w], lo[0], lo[1], lo[2], lo[3], b0, b1);
+                mma_bf16(o[2 * w + 1], lo[0], lo[1], lo[2], lo[3], b2, b3);
             }
         }
+        half_ring = 2 - half_ring;
+        __syncwarp();   // every lane is done with the slots before they are filled again
     }
 
     // ---- merge the item's warps ----
@@ -286,16 +287,10 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         ls += __shfl_xor_sync(0xffffffffu, ls, 2);
         const int r = g + 8 * half;
         if (r0 + r >= rw.n) continue;
-        if (c == 0) sml[warp][r] = make_float2(m[half], ls);
-        // dims 16c + j (first column of n-tile j) and 16c + 8 + j (second)
+        if (c == 0) sml[warp][r] = make_float2(m[half] * PA_SCALE, ls);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float *d = so(warp, r) + 16 * c + 8 * i;
-            *reinterpret_cast<float4 *>(d) =
-                make_float4(o[0][2 * half + i], o[1][2 * half + i], o[2][2 * half + i], o[3][2 * half + i]);
-            *reinterpret_cast<float4 *>(d + 4) =
-                make_float4(o[4][2 * half + i], o[5][2 * half + i], o[6][2 * half + i], o[7][2 * half + i]);
-        }
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float2 *>(so(warp, r) + 8 * j + 2 * c) = make_float2(o[j][2 * half], o[j][2 * half + 1]);
     }
     auto item_bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpi), "r"(32 * wpi) : "memory"); };
     item_bar();
@@ -348,7 +343,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
                 const float *sr = scores + r * ks.chunk + t;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (t + u * 32 * wpi < k1) add[u] = fmaf(ex2_approx(sr[u * 32 * wpi] - st.x), st.y, add[u]);
+                    if (t + u * 32 * wpi < k1) add[u] = fmaf(ex2_approx(fmaf(sr[u * 32 * wpi], PA_SCALE, -st.x)), st.y, add[u]);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -528,7 +523,7 @@ PaPlan plan(PaArgs &a, bool may_tc) {
     if (pl.tc)
         split_keys(a.pre, (long long)a.slots * a.n_kv, PT_BLOCKS, PT_KEYS, PT_KEYS, PT_CLUSTER, PT_CLUSTER_KEYS);
     else
-        split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, PA_WARPS * PA_KEYS, PA_WARPS * PA_KEYS, PA_CLUSTER,
+        split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, PA_WARPS * PA_SLOT_KEYS, PA_WARPS * PA_SLOT_KEYS, PA_CLUSTER,
                    PA_CLUSTER_KEYS);
     // own keys: one warp an item when that fills the device, more warps, then key ranges, when it does not
     const long long items = (long long)a.own.n_set * a.n_kv * a.own_tiles;
@@ -536,7 +531,7 @@ PaPlan plan(PaArgs &a, bool may_tc) {
     while (a.own_wpi > 1 && (items * a.own_wpi > PA_BLOCKS * PA_WARPS || (a.own_wpi - 1) * PA_KEYS >= a.own.max_keys))
         a.own_wpi /= 2;
     split_keys(a.own, items, PA_BLOCKS * (PA_WARPS / a.own_wpi), a.own_wpi * PA_KEYS,
-               has_pre ? PA_OWN_LEAST : PA_WARPS * PA_KEYS, PA_CLUSTER, PA_CLUSTER_KEYS);
+               has_pre ? PA_OWN_LEAST : PA_WARPS * PA_SLOT_KEYS, PA_CLUSTER, PA_CLUSTER_KEYS);
     a.own_items = items * a.own.splits;
     const bool one_launch = a.own_wpi == PA_WARPS && a.own.splits <= PA_CLUSTER && !has_pre;
     a.own_cluster = has_own && (a.own.splits == 1 || one_launch) ? a.own.splits : 0;
