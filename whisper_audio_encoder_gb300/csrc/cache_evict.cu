@@ -503,23 +503,23 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
         a.n_out = same ? nullptr : n_out;
         auto *kernel = a.max_keys <= 512 ? k_evict_small<32, 16>
                        : a.max_keys <= 1024 ? k_evict_small<32, 32> : k_evict_small<SM_THREADS, 8>;
-        rc = launch_ex(kernel, heads, SM_THREADS, most * (int)sizeof(int), 1, false, s, a);
+        rc = launch_ex(kernel, heads, SM_THREADS, most * (int)sizeof(int), 1, true, s, a);
         if (!rc && same) rc = launch_ex(k_evict_counts, dim3((a.n_set + 255) / 256), 256, 0, 1, true, s, a, n_out);
     } else {
         a.kept = kept ? kept : reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + up256e((size_t)cache->n_set * 4));
         const dim3 warps((unsigned)((items + 3) / 4)), blocks((unsigned)items);
         if (a.max_keys <= 512)
-            rc = launch_ex(k_evict_select<32, 16>, warps, 128, 0, 1, false, s, a);
+            rc = launch_ex(k_evict_select<32, 16>, warps, 128, 0, 1, true, s, a);
         else if (a.max_keys <= 1024)
-            rc = launch_ex(k_evict_select<32, 32>, warps, 128, 0, 1, false, s, a);
+            rc = launch_ex(k_evict_select<32, 32>, warps, 128, 0, 1, true, s, a);
         else if (a.max_keys <= 2048)
-            rc = launch_ex(k_evict_select<256, 8>, blocks, 256, 0, 1, false, s, a);
+            rc = launch_ex(k_evict_select<256, 8>, blocks, 256, 0, 1, true, s, a);
         else if (a.max_keys <= 8192)
-            rc = launch_ex(k_evict_select<SEL_THREADS, 8>, blocks, SEL_THREADS, 0, 1, false, s, a);
+            rc = launch_ex(k_evict_select<SEL_THREADS, 8>, blocks, SEL_THREADS, 0, 1, true, s, a);
         else if (a.max_keys <= SEL_HELD * SEL_THREADS)
-            rc = launch_ex(k_evict_select<SEL_THREADS, SEL_HELD>, blocks, SEL_THREADS, 0, 1, false, s, a);
+            rc = launch_ex(k_evict_select<SEL_THREADS, SEL_HELD>, blocks, SEL_THREADS, 0, 1, true, s, a);
         else
-            rc = launch_ex(k_evict_select<SEL_THREADS, 0>, blocks, SEL_THREADS, 0, 1, false, s, a);
+            rc = launch_ex(k_evict_select<SEL_THREADS, 0>, blocks, SEL_THREADS, 0, 1, true, s, a);
         if (!rc)
             rc = a.in_place ? launch_ex(k_evict_shift, dim3(n_kv_head, a.n_set, 2), SH_THREADS, 0, 1, true, s, a)
                             : launch_ex(k_evict_move, dim3((unsigned)(((long long)most * n_kv_head * 8 + MV_PIECES - 1) / MV_PIECES), a.n_set),

@@ -19,10 +19,10 @@ constexpr int PA_SLOT = 2 * PA_SLOT_KEYS * 128;   // bytes: keys, then values
 constexpr int PA_RING = 4 * PA_SLOT;
 constexpr int PA_SMEM = PA_WARPS * PA_RING;
 constexpr int SO_ROW = 68;         // floats a row of the warps' staged results
-constexpr int PM_ROWS = 8;         // rows of one merge block (16 threads a row)
+constexpr int PM_ROWS = 4;         // rows of one merge block (16 threads a row)
 constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
-constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp at a time
-constexpr int PW_TURNS = 4;        // weight kernel: times
+constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp step
+constexpr int PW_BLOCKS = 5 * 152; // weight kernel: blocks that are resident at once
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(16 * PM_ROWS) k_prefix_merge(const PaArgs p) {
     float l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float4 *po = reinterpret_cast<const float4 *>(p.part_o + min(row, rows - 1) * ns * 64) + lane;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < np + no; ++i) {
         const int s = i < np ? i : p.pre.splits + i - np;
         const float2 x = __ldcg(ml + s);
@@ -394,16 +394,17 @@ __global__ void __launch_bounds__(16 * PM_ROWS) k_prefix_merge(const PaArgs p) {
 }
 
 // weight[t] += sum over the set's queries of 2^(s_t - m) / l: the scores again, with every row's final
-// maximum and sum.  A warp holds 32 keys at a time, PW_TURNS times, and goes through the rows 16 at a time, so
-// each sum has one fixed order.
+// maximum and sum.  A warp takes 32 keys at a time from a ring of two such steps and goes through the rows
+// 16 at a time; each sum has one fixed order.  Bound by the keys' bytes for few rows.
 __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p, int own) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    __shared__ __align__(128) uint8_t rings[PW_WARPS][2 * PW_KEYS * 128];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const PaSet &ks = own ? p.own : p.pre;
     Rows rw;
     rw.hk = blockIdx.y;
     const int set = blockIdx.z;
-    const int nk = clamp_count(ks, set);
-    int t0 = (blockIdx.x * PW_WARPS * PW_TURNS + (threadIdx.x >> 5)) * PW_KEYS;
+    const int nk = clamp_count(ks, set), stride = gridDim.x * PW_WARPS * PW_KEYS;
+    int t0 = (blockIdx.x * PW_WARPS + warp) * PW_KEYS;
     if (t0 >= nk) {
         pdl_wait();   // on every path: a kernel after this one counts on what came before too
         return;
@@ -412,21 +413,21 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
     if (!own) group_range(p, set, s0, e0);
     rw.seq0 = s0;
     rw.n = (e0 - s0) * p.nq * p.rep;
-    const __nv_bfloat16 *kb = ks.k + (long long)set * ks.set_stride + rw.hk * 64 + 8 * c;
-    uint4 kr[4][2];
-    auto load_k = [&](int t) {
+    const int crow = lane >> 3, piece = lane & 7;
+    const uint32_t ring = smem_u32(rings[warp]);
+    const __nv_bfloat16 *kb = ks.k + (long long)set * ks.set_stride + rw.hk * 64 + 8 * piece;
+    auto fetch = [&](int t, int slot) {   // keys t .. t + 31, permuted as in k_prefix_attention
+        if (t < nk) {
+            const uint32_t dst = ring + slot * PW_KEYS * 128 + crow * 128 + ((piece ^ ((crow & 1) << 2)) << 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int tk = t + 8 * j + g;
-            kr[j][0] = kr[j][1] = make_uint4(0, 0, 0, 0);
-            if (tk < nk) {
-                const uint4 *s = reinterpret_cast<const uint4 *>(kb + (long long)tk * ks.row_stride);
-                kr[j][0] = __ldg(s);
-                kr[j][1] = __ldg(s + 4);
+            for (int i = 0; i < PW_KEYS / 4; ++i) {
+                const bool in = t + 4 * i + crow < nk;
+                cp_async16(dst + i * 512, in ? kb + (long long)(t + 4 * i + crow) * ks.row_stride : kb, in ? 16u : 0u);
             }
         }
+        cp_async_commit();
     };
-    load_k(t0);
+    fetch(t0, 0);
     pdl_wait();
     uint32_t qa[4][4];
     float2 st[2];
@@ -446,7 +447,22 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
         }
     };
     load_rows(0);
-    for (int turn = 0; turn < PW_TURNS && t0 < nk; ++turn) {
+    // the key whose sum this lane ends up with
+    const int mine = ((lane & 16) ? 16 : 0) + ((lane & 8) ? 8 : 0) + 2 * c + ((lane & 4) ? 1 : 0);
+    float *w = ks.weight + ((long long)set * p.n_kv + rw.hk) * ks.max_keys + mine;
+    for (int slot = 0; t0 < nk; t0 += stride, slot ^= 1) {
+        fetch(t0 + stride, slot ^ 1);
+        const float before = t0 + mine < nk ? __ldcg(w + t0) : 0.0f;
+        cp_async_wait<1>();
+        __syncwarp();
+        uint4 kr[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t kk = ring + slot * PW_KEYS * 128 + (8 * j + g) * 128;
+            kr[j][0] = lds128(kk + ((c ^ ((g & 1) << 2)) << 4));
+            kr[j][1] = lds128(kk + (((c + 4) ^ ((g & 1) << 2)) << 4));
+        }
+        __syncwarp();
         float acc[4][2] = {};
         for (int r0 = 0; r0 < rw.n; r0 += 16) {
             if (rw.n > 16) load_rows(r0);
@@ -457,25 +473,28 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int key = t0 + 8 * j + 2 * c + (i & 1);
-                    const float e = ex2_approx(s[i] * PA_SCALE - st[i >> 1].x);
+                    const float e = ex2_approx(fmaf(s[i], PA_SCALE, -st[i >> 1].x));
                     if (key < lim[i >> 1]) acc[j][i & 1] = fmaf(e, st[i >> 1].y, acc[j][i & 1]);
                 }
             }
         }
-        const int done = t0;
-        t0 += PW_WARPS * PW_KEYS;
-        load_k(t0);
+        // the eight row lanes' sums, each lane keeping half of its keys at every exchange
+        float x[2][2], y[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float a = acc[j][i];
-                a += __shfl_xor_sync(0xffffffffu, a, 4);
-                a += __shfl_xor_sync(0xffffffffu, a, 8);
-                a += __shfl_xor_sync(0xffffffffu, a, 16);
-                const int key = done + 8 * j + 2 * c + i;
-                if (g == 0 && key < nk) ks.weight[((long long)set * p.n_kv + rw.hk) * ks.max_keys + key] += a;
+                const bool up = lane & 16;
+                x[j][i] = (up ? acc[2 + j][i] : acc[j][i]) + __shfl_xor_sync(0xffffffffu, up ? acc[j][i] : acc[2 + j][i], 16);
             }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool up = lane & 8;
+            y[i] = (up ? x[1][i] : x[0][i]) + __shfl_xor_sync(0xffffffffu, up ? x[0][i] : x[1][i], 8);
+        }
+        const bool up = lane & 4;
+        const float sum = (up ? y[1] : y[0]) + __shfl_xor_sync(0xffffffffu, up ? y[0] : y[1], 4);
+        if (t0 + mine < nk) w[t0] = before + sum;
     }
 }
 
@@ -587,17 +606,15 @@ int launch(PaArgs &a, const PaPlan &pl, const PtMaps &maps, uint8_t *ws, cudaStr
     const long long rows = (long long)a.batch * a.nq * a.n_head;
     if (pre_blocks > 0x7fffffffLL || own_blocks > 0x7fffffffLL) return WH_EINVAL;
     if (!a.own.weight) a.score_floats = 0;
-    bool pdl = false;
     if (pre_blocks > 0) {
         if (int rc = pl.tc ? prefix_tc_launch(a, maps, s)
                            : launch_ex(k_prefix_attention<false>, dim3((unsigned)pre_blocks), PA_THREADS, PA_SMEM,
-                                       a.pre_cluster, false, s, a))
+                                       a.pre_cluster, true, s, a))
             return rc;
-        pdl = true;   // own keys beside the prefix's last blocks
     }
     if (own_blocks > 0) {
         const int smem = PA_SMEM + (a.score_floats ? PA_SCORE_BYTES : 0);
-        if (int rc = launch_ex(k_prefix_attention<true>, dim3((unsigned)own_blocks), PA_THREADS, smem, a.own_cluster, pdl, s, a))
+        if (int rc = launch_ex(k_prefix_attention<true>, dim3((unsigned)own_blocks), PA_THREADS, smem, a.own_cluster, true, s, a))
             return rc;
     }
     if (pl.merge)
@@ -606,8 +623,9 @@ int launch(PaArgs &a, const PaPlan &pl, const PtMaps &maps, uint8_t *ws, cudaStr
     for (int own = 0; own < 2; ++own) {
         const PaSet &ks = own ? a.own : a.pre;
         if (!ks.weight || (own && a.score_floats)) continue;
-        const int per_block = PW_WARPS * PW_KEYS * PW_TURNS;
-        if (int rc = launch_ex(k_prefix_weight, dim3((ks.max_keys + per_block - 1) / per_block, a.n_kv, ks.n_set),
+        const int most = (ks.max_keys + PW_WARPS * PW_KEYS - 1) / (PW_WARPS * PW_KEYS);
+        const long long fill = (PW_BLOCKS + (long long)a.n_kv * ks.n_set - 1) / ((long long)a.n_kv * ks.n_set);
+        if (int rc = launch_ex(k_prefix_weight, dim3(fill < most ? (unsigned)fill : most, a.n_kv, ks.n_set),
                                32 * PW_WARPS, 0, 1, true, s, a, own))
             return rc;
     }

@@ -411,7 +411,7 @@ int prefix_tc_maps(const PaArgs &a, PtMaps *m) {
 int prefix_tc_launch(const PaArgs &a, const PtMaps &m, cudaStream_t s) {
     const dim3 grid((unsigned)((long long)a.slots * a.n_kv * a.pre.splits));
     auto *kernel = a.tile == 128 ? k_prefix_tc<1> : a.tile == 64 ? k_prefix_tc<2> : k_prefix_tc<4>;
-    return launch_ex(kernel, grid, PT_THREADS, PT_SMEM, a.pre_cluster, false, s, m, a);
+    return launch_ex(kernel, grid, PT_THREADS, PT_SMEM, a.pre_cluster, true, s, m, a);
 }
 
 }  // namespace wh
