@@ -319,8 +319,10 @@ int wh_decode_attention(const wh_bf16 *q, const wh_bf16 *k, const wh_bf16 *v, in
  *   out     device bf16 [batch * n_query][64 n_head]; may not alias the inputs
  *   prefix or own may be NULL (not both).
  *   workspace >= wh_prefix_attention_workspace(batch, n_query, n_head, n_kv_head, prefix sets or 0,
- *           prefix->max_keys or 0, own->max_keys or 0) bytes, 256-byte aligned, contents need not
- *           be initialised; not shared by concurrent calls.
+ *           prefix->max_keys or 0, own->max_keys or 0, what the call needs: a sum of WH_GROUP_TABLE
+ *           (group_start is given), WH_PREFIX_WEIGHT, WH_OWN_WEIGHT (that weight is given)) bytes,
+ *           256-byte aligned, contents need not be initialised; not shared by concurrent calls.
+ *           May be NULL where that is 0.
  *   row_stride >= 64 n_kv_head, q_stride >= 64 n_head, set_stride >= 0, all multiples of 8; q, k, v,
  *   out 16-byte aligned; batch, n_set <= 65535, n_query, n_head <= 1024, 1 <= max_keys <= 2^30.
  * group_start is checked on the device: a group that does not lie in 0 .. batch is cut to it and
@@ -336,8 +338,9 @@ typedef struct {
     float *weight;
     int n_set, max_keys;
 } wh_keys;
+enum { WH_GROUP_TABLE = 1, WH_PREFIX_WEIGHT = 2, WH_OWN_WEIGHT = 4 };
 size_t wh_prefix_attention_workspace(int batch, int n_query, int n_head, int n_kv_head, int n_prefix,
-                                     int max_prefix, int max_own);
+                                     int max_prefix, int max_own, int needs);
 int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch, int n_query, int n_head, int n_kv_head,
                         const wh_keys *prefix, const int *group_start, const wh_keys *own, wh_bf16 *out,
                         void *workspace, size_t ws_bytes, void *stream);
@@ -359,13 +362,14 @@ int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch, int n_que
  *           stays; entries past the new count are left as they were
  *   0 <= recent <= budget, 1 <= budget <= 2^30; within a wh_keys no two sets and no keys and values
  *   may overlap (sets one after the other or side by side in a row; [K | V] rows are fine).
- *   workspace >= wh_cache_evict_workspace(n_set, n_kv_head, budget) bytes, 256-byte aligned, contents
- *           need not be initialised; not shared by concurrent calls.
+ *   workspace >= wh_cache_evict_workspace(n_set, n_kv_head, cache->max_keys, budget) bytes, 256-byte
+ *           aligned, contents need not be initialised; not shared by concurrent calls.  May be NULL
+ *           where that is 0.
  * A count outside 0 .. max_keys is clamped and recorded as WH_EBOUNDS.  All layers' caches
  * [n_layer][batch][...] are n_layer * batch sets of one call.
  * Errors: WH_EINVAL, WH_ENOSPC, WH_ECUDA.
  * ------------------------------------------------------------------------------------ */
-size_t wh_cache_evict_workspace(int n_set, int n_kv_head, int budget);
+size_t wh_cache_evict_workspace(int n_set, int n_kv_head, int max_keys, int budget);
 int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, int recent, const wh_keys *out, int *n_out,
                    int *kept, void *workspace, size_t ws_bytes, void *stream);
 

@@ -30,7 +30,7 @@ def _call(L, cache=None, n_kv=2, budget=40, recent=8, out=None, n_out=FAKE, kept
 
 def test_rejects_bad_arguments(L):
     bad = [dict(budget=0), dict(budget=-1), dict(recent=-1), dict(recent=41), dict(n_kv=0), dict(n_kv=3), dict(n_out=None),
-           dict(n_out=ctypes.c_void_p(P + 1)), dict(kept=ctypes.c_void_p(P + 2)), dict(ws=None), dict(ws=ctypes.c_void_p(P + 16))]
+           dict(n_out=ctypes.c_void_p(P + 1)), dict(kept=ctypes.c_void_p(P + 2)), dict(ws=ctypes.c_void_p(P + 16))]
     for kw in bad:
         assert _call(L, _keys(), **kw) == wh.WH_EINVAL, kw
     assert _call(L) == wh.WH_EINVAL
@@ -56,11 +56,15 @@ def test_rejects_what_shares_memory(L):
 
 
 def test_workspace(L):
-    need = L.wh_cache_evict_workspace(3, 2, 40)
-    assert need >= 3 * 4 + 3 * 2 * 40 * 4
-    assert _call(L, _keys(), ws_bytes=need - 1) == wh.WH_ENOSPC
-    for args in ((0, 2, 40), (3, 0, 40), (3, 2, 0)):
-        assert L.wh_cache_evict_workspace(*args) == 0
+    size = L.wh_cache_evict_workspace
+    assert size(3, 2, 100, 40) == 0                       # one kernel
+    need = size(3, 200, 100, 40)
+    assert need >= 3 * 4 + 3 * 200 * 40 * 4
+    wide = dict(row_stride=12800, set_stride=1280000, v=P + (1 << 26), weight=P + (1 << 27))
+    assert _call(L, _keys(**wide), n_kv=200, ws_bytes=need - 1) == wh.WH_ENOSPC
+    assert _call(L, _keys(**wide), n_kv=200, ws=None) == wh.WH_ENOSPC
+    for args in ((0, 200, 100, 40), (3, 0, 100, 40), (3, 200, 0, 40), (3, 200, 100, 0)):
+        assert size(*args) == 0
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device path")

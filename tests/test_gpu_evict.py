@@ -150,7 +150,7 @@ def test_recorded_and_replayed():
     w, n = torch.zeros(3, 4, 120, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
     cache, out = wh.Keys(c.k, c.v, c.n, c.w), wh.Keys(k, v, n, w)
     kept = torch.zeros(3, 4, 120, dtype=torch.int32, device="cuda")
-    ws = torch.empty(wh.lib().wh_cache_evict_workspace(3, 4, 120), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(256, wh.lib().wh_cache_evict_workspace(3, 4, 300, 120)), dtype=torch.uint8, device="cuda")
     wh.wh_cache_evict(cache, 4, 120, 20, out=out, kept=kept, workspace=ws)
     ref = [x.clone() for x in (k, v, w, n, kept)]
     graph = torch.cuda.CUDAGraph()
@@ -209,7 +209,7 @@ def test_refusals_of_the_binding():
     small = torch.zeros(2, 1, 4, 128, dtype=torch.bfloat16, device="cuda")
     bad = [dict(cache=wh.Keys(c.k, c.v, c.n)), dict(n_kv_head=3), dict(n_kv_head=1), dict(budget=0), dict(recent=5),
            dict(out=wh.Keys(small[0], small[1])), dict(out=wh.Keys(c.k[:, :4], c.v[:, :4], None, torch.zeros(1, 2, 4, device="cuda"))),
-           dict(kept=torch.zeros(1, 2, 5, dtype=torch.int32, device="cuda")), dict(workspace=torch.zeros(3, device="cuda"))]
+           dict(kept=torch.zeros(1, 2, 5, dtype=torch.int32, device="cuda")), dict(workspace=torch.zeros(64, device="cuda")[1:])]
     before = c.store.clone()
     for kw in bad:
         args = dict(cache=cache, n_kv_head=2, budget=4, recent=1)

@@ -219,7 +219,7 @@ def test_same_bits_again_with_a_dirty_workspace_on_another_stream(nq):
     x = a.run()
     wp, wo = a.pk.weight.clone(), a.ok.weight.clone()
     b = Case(7, **kw)
-    need = wh.lib().wh_prefix_attention_workspace(16, nq, 4, 2, 3, 700, 18)
+    need = wh.lib().wh_prefix_attention_workspace(16, nq, 4, 2, 3, 700, 18, 7)
     ws = torch.full((need // 4,), float("nan"), device="cuda")
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -235,7 +235,7 @@ def test_recorded_and_replayed():
     pk, ok, q = c.keys("pre"), c.keys("own"), _dev(c.q)
     start = torch.from_numpy(c.start).cuda()
     out = torch.zeros_like(ref)
-    ws = torch.empty(wh.lib().wh_prefix_attention_workspace(5, 1, 4, 4, 2, 300, 9), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(wh.lib().wh_prefix_attention_workspace(5, 1, 4, 4, 2, 300, 9, 7), dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
@@ -291,7 +291,7 @@ def test_agrees_with_the_one_query_attention():
 
 
 def test_refusals_of_the_binding():
-    c = Case(11, n_head=2, n_kv=2, nq=1, groups=[2, 2], n_pre=[8, 8])
+    c = Case(11, n_head=2, n_kv=2, nq=1, groups=[2, 2], n_pre=[8, 8], weigh=True)
     c.run()
     q, start = _dev(c.q), torch.from_numpy(c.start).cuda()
     bad = [dict(q=q.float()), dict(q=q[:3]), dict(n_kv_head=4), dict(n_query=3), dict(group_start=start.long()),

@@ -33,7 +33,7 @@ def test_rejects_bad_shapes_and_pointers(L):
     ok = _keys()
     bad = [dict(n_query=0), dict(n_query=2000), dict(n_head=0), dict(n_kv=4), dict(n_kv=0), dict(batch=-1),
            dict(batch=65536), dict(q_stride=376), dict(q_stride=388), dict(batch=3), dict(q=None), dict(q=ODD),
-           dict(out=None), dict(out=ODD), dict(ws=None), dict(ws=ctypes.c_void_p(P + 16)),
+           dict(out=None), dict(out=ODD), dict(ws=ctypes.c_void_p(P + 16)),
            dict(start=ctypes.c_void_p(P + 2)), dict(batch=65535, n_query=1024, n_head=1020, n_kv=6, q_stride=65536)]
     for kw in bad:
         assert _call(L, prefix=ok, **kw) == wh.WH_EINVAL, kw
@@ -47,14 +47,19 @@ def test_rejects_bad_shapes_and_pointers(L):
 
 
 def test_workspace(L):
-    need = L.wh_prefix_attention_workspace(4, 1, 6, 6, 2, 100, 0)
-    assert need >= 256
-    assert _call(L, prefix=_keys(), start=FAKE, ws_bytes=255) == wh.WH_ENOSPC
-    assert L.wh_prefix_attention_workspace(0, 1, 6, 6, 2, 100, 0) == 0
-    assert L.wh_prefix_attention_workspace(4, 1, 6, 5, 2, 100, 0) == 0
-    assert L.wh_prefix_attention_workspace(4, 1, 6, 6, -1, 100, 0) == 0
-    # long keys for few rows are split: partial results of every range
-    assert L.wh_prefix_attention_workspace(1, 1, 6, 6, 1, 30000, 448) > 6 * 2 * 64 * 4
+    size = L.wh_prefix_attention_workspace
+    assert size(4, 1, 6, 6, 2, 100, 0, 0) == 0                             # nothing to keep between kernels
+    need = size(4, 1, 6, 6, 2, 100, 0, wh.WH_PREFIX_WEIGHT)
+    assert need >= 4 * 6 * 8                                               # every row's maximum and sum
+    weighed = _keys(weight=P)
+    assert _call(L, prefix=weighed, ws_bytes=need - 1) == wh.WH_ENOSPC
+    assert _call(L, prefix=weighed, ws=None) == wh.WH_ENOSPC
+    for args in ((0, 1, 6, 6, 2, 100, 0, 0), (4, 1, 6, 5, 2, 100, 0, 0), (4, 1, 6, 6, -1, 100, 0, 0), (4, 1, 6, 6, 3, 100, 0, 2),
+                 (4, 1, 6, 6, 2, 100, 0, 8)):
+        assert size(*args) == 0
+    # partial results: of long keys for few rows, and of a prefix before own keys
+    assert size(1, 1, 6, 6, 1, 300000, 0, 0) > 6 * 17 * 64 * 4
+    assert size(4, 1, 6, 6, 2, 100, 50, wh.WH_GROUP_TABLE) >= 4 * 6 * (64 * 4 + 8)
 
 
 def test_empty_batch_is_a_no_op(L):

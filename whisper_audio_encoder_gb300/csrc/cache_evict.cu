@@ -401,6 +401,13 @@ __global__ void k_evict_counts(const EvArgs p, int *n_out) {
         n_out[i] = min(count_of(p, i, false), p.budget);
 }
 
+// One kernel for short caches of as many heads as are resident at once, unless few of them move many rows.
+bool one_kernel(int n_set, int n_head, int max_keys, int budget) {
+    const long long items = (long long)n_set * n_head;
+    return max_keys <= SM_MOST && items <= SM_HEADS &&
+           (budget <= SM_ROWS || max_keys <= SM_ROWS || 2 * items >= SM_HEADS);
+}
+
 size_t up256e(size_t x) { return (x + 255) & ~(size_t)255; }
 
 bool fits(const void *p, size_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -433,8 +440,10 @@ bool meet(Span x, Span y) { return x.a < y.b && y.a < x.b; }
 
 using namespace wh;
 
-extern "C" size_t wh_cache_evict_workspace(int n_set, int n_kv_head, int budget) {
-    if (n_set < 1 || n_set > 65535 || n_kv_head < 1 || n_kv_head > 1024 || budget < 1 || budget > (1 << 30)) return 0;
+extern "C" size_t wh_cache_evict_workspace(int n_set, int n_kv_head, int max_keys, int budget) {
+    if (n_set < 1 || n_set > 65535 || n_kv_head < 1 || n_kv_head > 1024 || max_keys < 1 || max_keys > (1 << 30) ||
+        budget < 1 || budget > (1 << 30) || one_kernel(n_set, n_kv_head, max_keys, budget))
+        return 0;
     return up256e((size_t)n_set * 4) + up256e((size_t)n_set * n_kv_head * budget * 4);
 }
 
@@ -442,7 +451,9 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
                               int *kept, void *workspace, size_t ws_bytes, void *stream) {
     if (n_kv_head < 1 || n_kv_head > 1024 || budget < 1 || budget > (1 << 30) || recent < 0 || recent > budget)
         return WH_EINVAL;
-    if (!keys_ok(cache, n_kv_head) || !fits(n_out, 4) || (kept && !fits(kept, 4)) || !fits(workspace, 256)) return WH_EINVAL;
+    if (!keys_ok(cache, n_kv_head) || !fits(n_out, 4) || (kept && !fits(kept, 4)) ||
+        (workspace && !fits(workspace, 256)))
+        return WH_EINVAL;
     if (out) {
         if (!keys_ok(out, n_kv_head) || out->n_set != cache->n_set) return WH_EINVAL;
         if (out->max_keys < (budget < cache->max_keys ? budget : cache->max_keys)) return WH_EINVAL;
@@ -463,7 +474,8 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
     }
     if (cache->n_keys && n_out != cache->n_keys && meet(span_of(n_out, cache->n_set, 4), span_of(cache->n_keys, cache->n_set, 4)))
         return WH_EINVAL;
-    if (ws_bytes < wh_cache_evict_workspace(cache->n_set, n_kv_head, budget)) return WH_ENOSPC;
+    if ((workspace ? ws_bytes : 0) < wh_cache_evict_workspace(cache->n_set, n_kv_head, cache->max_keys, budget))
+        return WH_ENOSPC;
     DevCtl ctl;
     int num_sms = 0;
     if (int rc = device_ctl(&ctl, &num_sms)) return rc;
@@ -496,8 +508,7 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
     int rc;
     trace_begin(TR_DEC_OTHER, s);
     const long long items = (long long)n_kv_head * a.n_set;
-    // one kernel for short caches of as many heads as are resident at once, unless few of them move many rows
-    if (a.max_keys <= SM_MOST && items <= SM_HEADS && (most <= SM_ROWS || 2 * items >= SM_HEADS)) {
+    if (one_kernel(a.n_set, n_kv_head, a.max_keys, budget)) {
         const bool same = n_out == a.n_keys;
         a.kept = kept;
         a.n_out = same ? nullptr : n_out;

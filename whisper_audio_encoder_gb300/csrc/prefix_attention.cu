@@ -22,7 +22,7 @@ constexpr int SO_ROW = 68;         // floats a row of the warps' staged results
 constexpr int PM_ROWS = 4;         // rows of one merge block (16 threads a row)
 constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
 constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp step
-constexpr int PW_BLOCKS = 5 * 152; // weight kernel: blocks that are resident at once
+constexpr int PW_BLOCKS = 4 * 152; // weight kernel: blocks that are resident at once
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -527,7 +527,7 @@ struct PaPlan {
 };
 
 // Row tiles, key ranges and the workspace's layout, from host-known sizes only.
-PaPlan plan(PaArgs &a, bool may_tc) {
+PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     PaPlan pl;
     const long long per = (long long)a.nq * a.rep, all = a.batch * per;
     const long long rows_a_set = a.pre.n_set > 0 ? (all + a.pre.n_set - 1) / a.pre.n_set : 0;
@@ -561,13 +561,13 @@ PaPlan plan(PaArgs &a, bool may_tc) {
     // the weights of own keys without a second pass, when an item sees all its keys and has room for the scores
     const long long scores = (per < PA_TILE ? per : PA_TILE) * (long long)a.own.chunk;
     const bool room = scores * (PA_WARPS / a.own_wpi) * 4 <= PA_SCORE_BYTES;
-    a.score_floats = a.own_cluster == 1 && a.own_tiles == 1 && room ? (int)scores : 0;
+    a.score_floats = own_weight && a.own_cluster == 1 && a.own_tiles == 1 && room ? (int)scores : 0;
     const size_t rows = (size_t)a.batch * a.nq * a.n_head;
     size_t off = 0;
     pl.part_o = off;  off += up256p(rows * a.n_part * 64 * 4);
     pl.part_ml = off; off += up256p(rows * a.n_part * 8);
-    pl.stats = off;   off += up256p(rows * 8);
-    pl.total = off < 256 ? 256 : off;
+    pl.stats = off;   off += pre_weight || (own_weight && !a.score_floats) ? up256p(rows * 8) : 0;
+    pl.total = off;
     return pl;
 }
 
@@ -600,12 +600,11 @@ bool shape_ok(int batch, int n_query, int n_head, int n_kv) {
 int launch(PaArgs &a, const PaPlan &pl, const PtMaps &maps, uint8_t *ws, cudaStream_t s) {
     a.part_o = reinterpret_cast<float *>(ws + pl.part_o);
     a.part_ml = reinterpret_cast<float2 *>(ws + pl.part_ml);
-    a.stats = a.pre.weight || a.own.weight ? reinterpret_cast<float2 *>(ws + pl.stats) : nullptr;
+    a.stats = pl.total > pl.stats ? reinterpret_cast<float2 *>(ws + pl.stats) : nullptr;
     const long long pre_blocks = (long long)a.slots * a.n_kv * a.pre.splits;
     const long long own_blocks = (a.own_items * a.own_wpi + PA_WARPS - 1) / PA_WARPS;
     const long long rows = (long long)a.batch * a.nq * a.n_head;
     if (pre_blocks > 0x7fffffffLL || own_blocks > 0x7fffffffLL) return WH_EINVAL;
-    if (!a.own.weight) a.score_floats = 0;
     if (pre_blocks > 0) {
         if (int rc = pl.tc ? prefix_tc_launch(a, maps, s)
                            : launch_ex(k_prefix_attention<false>, dim3((unsigned)pre_blocks), PA_THREADS, PA_SMEM,
@@ -649,9 +648,9 @@ int prefix_attention_prepare() {
 using namespace wh;
 
 extern "C" size_t wh_prefix_attention_workspace(int batch, int n_query, int n_head, int n_kv_head, int n_prefix,
-                                                int max_prefix, int max_own) {
+                                                int max_prefix, int max_own, int needs) {
     if (!shape_ok(batch, n_query, n_head, n_kv_head) || batch == 0 || n_prefix < 0 || n_prefix > 65535 ||
-        max_prefix < 0 || max_prefix > (1 << 30) || max_own < 0 || max_own > (1 << 30))
+        max_prefix < 0 || max_prefix > (1 << 30) || max_own < 0 || max_own > (1 << 30) || (needs & ~7))
         return 0;
     PaArgs a = {};
     a.batch = batch;
@@ -663,12 +662,13 @@ extern "C" size_t wh_prefix_attention_workspace(int batch, int n_query, int n_he
     a.pre.max_keys = max_prefix;
     a.own.n_set = max_own > 0 ? batch : 0;
     a.own.max_keys = max_own;
-    // the largest of: groups of any size or equal ones, the prefix part on either kernel
-    size_t most = 0;
-    const bool equal = a.pre.n_set > 0 && batch % a.pre.n_set == 0;
-    for (int i = 0; i < (equal ? 4 : 2); ++i) {
-        a.gsize = i < 2 ? 0 : batch / a.pre.n_set;
-        const size_t t = plan(a, i & 1).total;
+    if (a.pre.n_set > 0 && !(needs & WH_GROUP_TABLE)) {
+        if (batch % a.pre.n_set != 0) return 0;
+        a.gsize = batch / a.pre.n_set;
+    }
+    size_t most = 0;   // the prefix part may run on either kernel
+    for (int tc = 0; tc < 2; ++tc) {
+        const size_t t = plan(a, tc, needs & WH_PREFIX_WEIGHT, needs & WH_OWN_WEIGHT).total;
         most = t > most ? t : most;
     }
     return most;
@@ -686,7 +686,7 @@ extern "C" int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch
     if (group_start && (!prefix || !fits(group_start, 4))) return WH_EINVAL;
     if (prefix && !group_start && batch % prefix->n_set != 0) return WH_EINVAL;
     if (batch == 0) return WH_OK;
-    if (!fits(q, 16) || !fits(out, 16) || !fits(workspace, 256)) return WH_EINVAL;
+    if (!fits(q, 16) || !fits(out, 16) || (workspace && !fits(workspace, 256))) return WH_EINVAL;
     a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
     a.q_stride = q_stride;
     a.group_start = group_start;
@@ -697,16 +697,17 @@ extern "C" int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch
     a.n_kv = n_kv_head;
     a.rep = n_head / n_kv_head;
     a.out = reinterpret_cast<__nv_bfloat16 *>(out);
-    PaPlan pl = plan(a, true);
-    if (ws_bytes < pl.total) return WH_ENOSPC;
+    PaPlan pl = plan(a, true, a.pre.weight, a.own.weight);
+    const size_t have = workspace ? ws_bytes : 0;
+    if (have < pl.total) return WH_ENOSPC;
     DevCtl ctl;
     int num_sms = 0;
     if (int rc = device_ctl(&ctl, &num_sms)) return rc;
     a.ctl = ctl;
     PtMaps maps;
     if (pl.tc && prefix_tc_maps(a, &maps) != WH_OK) {   // strides that a tensor map cannot hold
-        pl = plan(a, false);
-        if (ws_bytes < pl.total) return WH_ENOSPC;
+        pl = plan(a, false, a.pre.weight, a.own.weight);
+        if (have < pl.total) return WH_ENOSPC;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     trace_begin(TR_DEC_ATTN, s);

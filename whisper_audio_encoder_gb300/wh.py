@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_PKG, "libwh.so")
 
 WH_OK, WH_EINVAL, WH_ENOSPC, WH_ECUDA, WH_ETIMEOUT, WH_EBOUNDS, WH_ENODEV = range(7)
 WH_EPI_BF16, WH_EPI_GELU_BF16, WH_EPI_RESID_F32 = range(3)
+WH_GROUP_TABLE, WH_PREFIX_WEIGHT, WH_OWN_WEIGHT = 1, 2, 4
 N_CTX, N_FRAMES, N_SAMPLES = 1500, 3000, 480_000
 
 _p = ctypes.c_void_p
@@ -102,11 +103,11 @@ def lib():
         "wh_decode_attention_workspace": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int]),
         "wh_decode_attention": (ctypes.c_int, [_p, _p, _p, ctypes.c_int64, ctypes.c_int64, _p, ctypes.c_int,
                                                ctypes.c_int, ctypes.c_int, _p, _p, ctypes.c_size_t, _p]),
-        "wh_prefix_attention_workspace": (ctypes.c_size_t, [ctypes.c_int] * 7),
+        "wh_prefix_attention_workspace": (ctypes.c_size_t, [ctypes.c_int] * 8),
         "wh_prefix_attention": (ctypes.c_int, [_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                ctypes.c_int, ctypes.POINTER(wh_keys), _p, ctypes.POINTER(wh_keys), _p,
                                                _p, ctypes.c_size_t, _p]),
-        "wh_cache_evict_workspace": (ctypes.c_size_t, [ctypes.c_int] * 3),
+        "wh_cache_evict_workspace": (ctypes.c_size_t, [ctypes.c_int] * 4),
         "wh_cache_evict": (ctypes.c_int, [ctypes.POINTER(wh_keys), ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                           ctypes.POINTER(wh_keys), _p, _p, _p, ctypes.c_size_t, _p]),
         "wh_decode_step_workspace": (ctypes.c_size_t, [ctypes.POINTER(wh_dec_config), ctypes.c_int]),
@@ -288,26 +289,28 @@ class Keys:
 
     def __init__(self, k, v, n_keys=None, weight=None):
         import torch
-        shape, stride, dev = k.shape, k.stride(), k.device
+        shape, stride, dev = k.shape, k.stride(), k.get_device()
         _need(len(shape) == 3 and v.shape == shape and v.stride() == stride and stride[2] == 1 and
-              k.dtype == v.dtype == torch.bfloat16, "Keys: k, v bf16 [n_set][max_keys][d], equal strides")
+              k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16, "Keys: k, v bf16 [n_set][max_keys][d], equal strides")
         n_set, max_keys, d = shape
-        _need(dev.type == "cuda" and v.device == dev, "Keys: k and v must be on one CUDA device")
+        _need(dev >= 0 and v.get_device() == dev, "Keys: k and v must be on one CUDA device")
+        counts = accumulators = None
         self.weight_heads = 0
         if n_keys is not None:
             _need(n_keys.dtype == torch.int32 and n_keys.shape == (n_set,) and n_keys.is_contiguous() and
-                  n_keys.device == dev, "Keys: n_keys int32 [n_set]")
+                  n_keys.get_device() == dev, "Keys: n_keys int32 [n_set]")
+            counts = n_keys.data_ptr()
         if weight is not None:
             ws = weight.shape
             _need(weight.dtype == torch.float32 and len(ws) == 3 and ws[0] == n_set and ws[2] == max_keys and
-                  weight.is_contiguous() and weight.device == dev, "Keys: weight float32 [n_set][n_kv_head][max_keys]")
-            self.weight_heads = ws[1]
+                  weight.is_contiguous() and weight.get_device() == dev,
+                  "Keys: weight float32 [n_set][n_kv_head][max_keys]")
+            self.weight_heads, accumulators = ws[1], weight.data_ptr()
         self.k, self.v, self.n_keys, self.weight, self.device = k, v, n_keys, weight, dev
         self.n_set, self.max_keys, self.width = n_set, max_keys, d
         # (the stride of a dimension of size one is never used)
         self.c = wh_keys(k.data_ptr(), v.data_ptr(), stride[1] if max_keys > 1 else d, stride[0] if n_set > 1 else 0,
-                         None if n_keys is None else n_keys.data_ptr(), None if weight is None else weight.data_ptr(),
-                         n_set, max_keys)
+                         counts, accumulators, n_set, max_keys)
 
     def _check(self, n_kv_head, device, what):
         _need(self.width >= 64 * n_kv_head, f"{what}: rows shorter than 64 n_kv_head")
@@ -315,19 +318,28 @@ class Keys:
         _need(self.device == device, f"{what}: tensors on different devices")
 
 
-def _launch(device, stream, call):
-    """call(stream handle) with `device` current; stream None is the device's current stream."""
+def _stream_handle(dev, stream):
+    """The handle of `stream`, or of device dev's current stream.  dev must be the current device: the
+    library launches there."""
     import torch
-    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == device.index:
-        return call(handle)
-    with torch.cuda.device(device):
-        return call(handle)
+    _need(torch._C._cuda_getDevice() == dev, "the tensors' device is not the current one (torch.cuda.set_device)")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 @functools.lru_cache(maxsize=4096)
 def _workspace_bytes(name, *args):
-    return max(256, getattr(lib(), name)(*args))
+    return getattr(lib(), name)(*args)
+
+
+def _scratch(need, dev, stream):
+    """A workspace of `need` bytes from torch's allocator, in the order of the launching stream (None: 0 bytes)."""
+    import torch
+    if need == 0:
+        return None
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
 
 
 def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_start=None, n_query=1, out=None,
@@ -339,41 +351,46 @@ def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_
     [batch * n_query][64 n_head]."""
     import torch
     what = "wh_prefix_attention"
-    shape, stride, dev = q.shape, q.stride(), q.device
-    _need(len(shape) == 2 and q.dtype == torch.bfloat16 and dev.type == "cuda" and stride[1] == 1 and n_head >= 1 and
+    shape, stride, dev = q.shape, q.stride(), q.get_device()
+    _need(len(shape) == 2 and q.dtype == torch.bfloat16 and dev >= 0 and stride[1] == 1 and n_head >= 1 and
           shape[1] >= 64 * n_head and n_query >= 1 and shape[0] % n_query == 0,
           "wh_prefix_attention: q bf16 [batch * n_query][64 n_head]")
     rows = shape[0]
     batch = rows // n_query
     if n_kv_head is None:
         n_kv_head = n_head
-    n_pre = max_pre = max_own = 0
+    n_pre = max_pre = max_own = needs = 0
     if prefix is not None:
         prefix._check(n_kv_head, dev, what)
-        n_pre, max_pre = prefix.n_set, prefix.max_keys
+        n_pre, max_pre, needs = prefix.n_set, prefix.max_keys, WH_PREFIX_WEIGHT if prefix.weight is not None else 0
     if own is not None:
         own._check(n_kv_head, dev, what)
         max_own = own.max_keys
+        if own.weight is not None:
+            needs |= WH_OWN_WEIGHT
+    table = None
     if group_start is not None:
-        _need(group_start.dtype == torch.int32 and group_start.device == dev and group_start.is_contiguous() and
+        _need(group_start.dtype == torch.int32 and group_start.get_device() == dev and group_start.is_contiguous() and
               group_start.shape == (n_pre + 1,) and n_pre > 0, "wh_prefix_attention: group_start int32 [prefix sets + 1]")
+        table = group_start.data_ptr()
+        needs |= WH_GROUP_TABLE
     if out is None:
-        out = torch.empty(rows, 64 * n_head, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(rows, 64 * n_head, dtype=torch.bfloat16, device=q.device)
     else:
         _need(out.dtype == torch.bfloat16 and out.shape == (rows, 64 * n_head) and out.is_contiguous() and
-              out.device == dev, "wh_prefix_attention: out bf16 [batch * n_query][64 n_head]")
+              out.get_device() == dev, "wh_prefix_attention: out bf16 [batch * n_query][64 n_head]")
+    s = _stream_handle(dev, stream)
     if workspace is None:
-        need = _workspace_bytes("wh_prefix_attention_workspace", batch, n_query, n_head, n_kv_head, n_pre, max_pre, max_own)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
+        need = _workspace_bytes("wh_prefix_attention_workspace", batch, n_query, n_head, n_kv_head, n_pre, max_pre, max_own,
+                                needs)
+        workspace = _scratch(need, dev, stream)
     else:
-        _need(workspace.device == dev, "wh_prefix_attention: workspace on another device")
+        _need(workspace.get_device() == dev and workspace.is_contiguous(), "wh_prefix_attention: workspace")
         need = workspace.numel() * workspace.element_size()
-    rc = _launch(dev, stream, lambda s: (_lib or lib()).wh_prefix_attention(
+    rc = (_lib or lib()).wh_prefix_attention(
         q.data_ptr(), stride[0] if rows > 1 else 64 * n_head, batch, n_query, n_head, n_kv_head,
-        prefix and prefix.c, group_start if group_start is None else group_start.data_ptr(), own and own.c,
-        out.data_ptr(), workspace.data_ptr(), need, s))
+        None if prefix is None else prefix.c, table, None if own is None else own.c, out.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), need, s)
     if rc != WH_OK:
         raise WhError(rc, what)
     return out
@@ -393,21 +410,22 @@ def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, worksp
     to._check(n_kv_head, dev, what)
     _need(cache.weight is not None and to.weight is not None, "wh_cache_evict: Keys without weight")
     _need(budget >= 1, "wh_cache_evict: budget >= 1")
+    indices = None
     if kept is not None:
         _need(kept.dtype == torch.int32 and kept.shape == (n_set, n_kv_head, budget) and kept.is_contiguous() and
-              kept.device == dev, "wh_cache_evict: kept int32 [n_set][n_kv_head][budget]")
-    n_out = to.n_keys if to.n_keys is not None else torch.empty(n_set, dtype=torch.int32, device=dev)
+              kept.get_device() == dev, "wh_cache_evict: kept int32 [n_set][n_kv_head][budget]")
+        indices = kept.data_ptr()
+    n_out = to.n_keys if to.n_keys is not None else torch.empty(n_set, dtype=torch.int32, device=cache.k.device)
+    s = _stream_handle(dev, stream)
     if workspace is None:
-        need = _workspace_bytes("wh_cache_evict_workspace", n_set, n_kv_head, budget)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
+        need = _workspace_bytes("wh_cache_evict_workspace", n_set, n_kv_head, cache.max_keys, budget)
+        workspace = _scratch(need, dev, stream)
     else:
-        _need(workspace.device == dev, "wh_cache_evict: workspace on another device")
+        _need(workspace.get_device() == dev and workspace.is_contiguous(), "wh_cache_evict: workspace")
         need = workspace.numel() * workspace.element_size()
-    rc = _launch(dev, stream, lambda s: (_lib or lib()).wh_cache_evict(
-        cache.c, n_kv_head, budget, recent, out and out.c, n_out.data_ptr(), kept if kept is None else kept.data_ptr(),
-        workspace.data_ptr(), need, s))
+    rc = (_lib or lib()).wh_cache_evict(cache.c, n_kv_head, budget, recent, None if out is None else out.c,
+                                        n_out.data_ptr(), indices, None if workspace is None else workspace.data_ptr(),
+                                        need, s)
     if rc != WH_OK:
         raise WhError(rc, what)
     return n_out
