@@ -19,10 +19,11 @@ constexpr int PA_SLOT = 2 * PA_SLOT_KEYS * 128;   // bytes: keys, then values
 constexpr int PA_RING = 4 * PA_SLOT;
 constexpr int PA_SMEM = PA_WARPS * PA_RING;
 constexpr int SO_ROW = 68;         // floats a row of the warps' staged results
+constexpr int PM_BATCH = 8;        // partial results that a merging thread loads at once
 constexpr int PM_ROWS = 4;         // rows of one merge block (16 threads a row)
 constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
 constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp step
-constexpr int PW_BLOCKS = 4 * 152; // weight kernel: blocks that are resident at once
+constexpr int PW_BLOCKS = 8 * 152; // weight kernel: blocks, some twice what is resident at once
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -130,23 +131,6 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         if (OWN) pdl_wait();
         return;
     }
-    const int before = OWN && cluster && p.after_pre ? pre_parts_of(p, group_of(p, set)) : 0;
-
-    uint32_t qa[4][4];
-    int lim[2];   // own keys: the first key that a row does not see
-    load_q(p, rw, r0, qa);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        lim[half] = nk;
-        if (OWN) {
-            int qrow, head, qi;
-            rw.locate(p, min(r0 + g + 8 * half, rw.n - 1), qrow, head, qi);
-            lim[half] = nk - (p.nq - 1 - qi);
-        }
-    }
-    const int full = OWN ? nk - (p.nq - 1) : nk;   // every row sees the keys before this one
-
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, o[8][4] = {};
     // Each warp copies its keys and values into a ring of its own, 16 at a time: four rows of 128 bytes an
     // instruction, zeros past the range.  The 16-byte pieces of a row are permuted (keys: by the row's lowest
     // bit, values: by the lowest three) so that the fragment reads below meet no bank twice.  A step takes two
@@ -185,6 +169,22 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     fetch(t0, 0);
     fetch(t0 + PA_SLOT_KEYS, 1);
     cp_async_commit();
+
+    uint32_t qa[4][4];
+    int lim[2];   // own keys: the first key that a row does not see
+    load_q(p, rw, r0, qa);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        lim[half] = nk;
+        if (OWN) {
+            int qrow, head, qi;
+            rw.locate(p, min(r0 + g + 8 * half, rw.n - 1), qrow, head, qi);
+            lim[half] = nk - (p.nq - 1 - qi);
+        }
+    }
+    const int full = OWN ? nk - (p.nq - 1) : nk;   // every row sees the keys before this one
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, o[8][4] = {};
     for (; t0 < k1; t0 += stride) {
         fetch(t0 + stride, 2 - half_ring);
         fetch(t0 + stride + PA_SLOT_KEYS, 3 - half_ring);
@@ -294,7 +294,11 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     }
     auto item_bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpi), "r"(32 * wpi) : "memory"); };
     item_bar();
-    if (OWN && p.after_pre) pdl_wait();   // the prefix's partial results are complete
+    int before = 0;
+    if (OWN && p.after_pre) {
+        if (cluster) before = pre_parts_of(p, group_of(p, set));
+        pdl_wait();   // the prefix's partial results are complete
+    }
     __shared__ float2 fin[PA_WARPS][PA_TILE];   // the block's maximum and sum; own weights: the row's maximum, 1 / sum
     const int w0 = warp - iw, rows = min(PA_TILE, rw.n - r0);
     for (int i = 32 * iw + lane; i < 8 * rows; i += 32 * wpi) {
@@ -352,41 +356,51 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     }
 }
 
-// o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the ranges of a row that hold keys, in order.
+// o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the ranges of a row that hold keys, in order.  16
+// threads a row, PM_BATCH ranges at a time, all of their loads before any arithmetic.
 __global__ void __launch_bounds__(16 * PM_ROWS) k_prefix_merge(const PaArgs p) {
     pdl_launch_dependents();
-    pdl_wait();
     const long long rows = (long long)p.batch * p.nq * p.n_head;
-    const long long row = (long long)blockIdx.x * PM_ROWS + (threadIdx.x >> 4);
+    const long long mine = (long long)blockIdx.x * PM_ROWS + (threadIdx.x >> 4), row = min(mine, rows - 1);
     const int lane = threadIdx.x & 15;
-    const int b = (int)(min(row, rows - 1) / ((long long)p.nq * p.n_head));
-    int no = 0;
+    const int b = (int)(row / ((long long)p.nq * p.n_head));
     // (the two rows of a warp may belong to different sequences: one after the other)
     const int b0 = __shfl_sync(0xffffffffu, b, 0), b1 = __shfl_sync(0xffffffffu, b, 16);
     const int np0 = pre_parts_of(p, group_of(p, b0)), np1 = b1 == b0 ? np0 : pre_parts_of(p, group_of(p, b1));
     const int np = (threadIdx.x & 16) ? np1 : np0;
-    if (p.own.n_set > 0) no = (clamp_count(p.own, b) + p.own.chunk - 1) / p.own.chunk;
-    const int ns = p.n_part;
-    const float2 *ml = p.part_ml + min(row, rows - 1) * ns;
-    const uint32_t half = 0xffffu << (threadIdx.x & 16);
-    // ranges that hold keys: 0 .. np-1 of the prefix, then 0 .. no-1 of the sequence's own
-    float m = -INFINITY;
-    for (int i = lane; i < np + no; i += 16) m = fmaxf(m, __ldcg(&ml[i < np ? i : p.pre.splits + i - np].x));
-#pragma unroll
-    for (int x = 8; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, x, 16));
-    float l = 0.0f;
+    const int n = np + (p.own.n_set > 0 ? (clamp_count(p.own, b) + p.own.chunk - 1) / p.own.chunk : 0);
+    const float2 *ml = p.part_ml + row * p.n_part;
+    const float4 *po = reinterpret_cast<const float4 *>(p.part_o + row * p.n_part * 64) + lane;
+    pdl_wait();   // the partial results; what came before only reads the call's inputs
+    float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float4 *po = reinterpret_cast<const float4 *>(p.part_o + min(row, rows - 1) * ns * 64) + lane;
-#pragma unroll 8
-    for (int i = 0; i < np + no; ++i) {
-        const int s = i < np ? i : p.pre.splits + i - np;
-        const float2 x = __ldcg(ml + s);
-        const float4 v = __ldcg(po + s * 16);
-        const float f = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - m);
-        l = fmaf(x.y, f, l);
-        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+    for (int i0 = 0; i0 < n; i0 += PM_BATCH) {
+        float2 x[PM_BATCH];
+        float4 v[PM_BATCH];
+#pragma unroll
+        for (int i = 0; i < PM_BATCH; ++i) {
+            x[i] = make_float2(-INFINITY, 0.0f);
+            v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i0 + i < n) {
+                const int s = i0 + i < np ? i0 + i : p.pre.splits + i0 + i - np;
+                x[i] = __ldcg(ml + s);
+                v[i] = __ldcg(po + s * 16);
+            }
+        }
+        float mn = m;
+#pragma unroll
+        for (int i = 0; i < PM_BATCH; ++i) mn = fmaxf(mn, x[i].x);
+        const float f = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
+        l *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+        m = mn;
+#pragma unroll
+        for (int i = 0; i < PM_BATCH; ++i) {
+            const float e = x[i].x == -INFINITY ? 0.0f : ex2_approx(x[i].x - m);
+            l = fmaf(x[i].y, e, l);
+            o.x = fmaf(v[i].x, e, o.x), o.y = fmaf(v[i].y, e, o.y), o.z = fmaf(v[i].z, e, o.z), o.w = fmaf(v[i].w, e, o.w);
+        }
     }
-    if (row >= rows) return;
+    if (mine >= rows) return;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint2 *>(p.out + row * 64 + 4 * lane) =
         make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));

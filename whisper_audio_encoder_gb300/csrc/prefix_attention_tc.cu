@@ -107,6 +107,14 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
         return;                            // (every block of a cluster alike)
     }
     const int nt = (k1 - k0 + PT_KEYS - 1) / PT_KEYS;
+    const int z = tm.one_set ? 0 : set;
+    auto load_step = [&](int j) {   // one thread
+        uint8_t *kb = sKV + (j % PT_STAGES) * 2 * TILE_BYTES;
+        uint64_t *bar = kv_full + j % PT_STAGES;
+        mbar_arrive_expect_tx(bar, 2 * TILE_BYTES);
+        tma_load_3d(kb, &tm.k, bar, rw.hk * 64, k0 + j * PT_KEYS, z);
+        tma_load_3d(kb + TILE_BYTES, &tm.v, bar, rw.hk * 64, k0 + j * PT_KEYS, z);
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < PT_STAGES; ++s) {
@@ -120,8 +128,8 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&tm.k);
-        tma_prefetch_desc(&tm.v);
+        // the first steps' keys and values are on their way while the block sets up
+        for (int j = 0; j < nt && j < PT_STAGES; ++j) load_step(j);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, PT_COLS);
@@ -153,25 +161,17 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
       if (warp == 0) {
         if (lane == 0) {
-            uint32_t issued = 0, last_parity = 0;
-            const int z = tm.one_set ? 0 : set;
-            for (int j = 0; j < nt; ++j) {
-                const int s = j % PT_STAGES;
-                const uint32_t ph = (j / PT_STAGES) & 1u;
-                if (*abort_flag || !mbar_wait(kv_empty + s, ph ^ 1u, p.ctl)) {
+            int j = nt < PT_STAGES ? nt : PT_STAGES;   // the steps so far
+            for (; j < nt; ++j) {
+                if (*abort_flag || !mbar_wait(kv_empty + j % PT_STAGES, (j / PT_STAGES - 1) & 1u, p.ctl)) {
                     *abort_flag = 1;
                     break;
                 }
-                uint8_t *kb = sKV + s * 2 * TILE_BYTES;
-                mbar_arrive_expect_tx(kv_full + s, 2 * TILE_BYTES);
-                tma_load_3d(kb, &tm.k, kv_full + s, rw.hk * 64, k0 + j * PT_KEYS, z);
-                tma_load_3d(kb + TILE_BYTES, &tm.v, kv_full + s, rw.hk * 64, k0 + j * PT_KEYS, z);
-                issued |= 1u << s;
-                last_parity = (last_parity & ~(1u << s)) | (ph << s);
+                load_step(j);
             }
             // no copy of this block may still be in flight when it exits
-            for (int s = 0; s < PT_STAGES; ++s)
-                if ((issued >> s) & 1u) mbar_wait(kv_full + s, (last_parity >> s) & 1u, p.ctl);
+            for (int i = j > PT_STAGES ? j - PT_STAGES : 0; i < j; ++i)
+                mbar_wait(kv_full + i % PT_STAGES, (i / PT_STAGES) & 1u, p.ctl);
         }
       } else if (warp == 1) {
         if (lane == 0) {
