@@ -331,15 +331,20 @@ def _workspace_bytes(name, *args):
     return getattr(lib(), name)(*args)
 
 
-def _scratch(need, dev, stream):
-    """A workspace of `need` bytes from torch's allocator, in the order of the launching stream (None: 0 bytes)."""
-    import torch
-    if need == 0:
-        return None
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+class _Scratch:
+    """A workspace of `need` bytes for one call (none if 0), from torch's caching allocator in the order of
+    the launching stream: handed back once the kernels are launched, as a freed tensor's memory is."""
+
+    __slots__ = ("ptr",)
+
+    def __init__(self, need, stream):
+        import torch
+        self.ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream) if need else None
+
+    def __del__(self):
+        if self.ptr:
+            import torch
+            torch._C._cuda_cudaCachingAllocator_raw_delete(self.ptr)
 
 
 def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_start=None, n_query=1, out=None,
@@ -383,14 +388,15 @@ def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_
     if workspace is None:
         need = _workspace_bytes("wh_prefix_attention_workspace", batch, n_query, n_head, n_kv_head, n_pre, max_pre, max_own,
                                 needs)
-        workspace = _scratch(need, dev, stream)
+        scratch = _Scratch(need, s)
+        at = scratch.ptr
     else:
         _need(workspace.get_device() == dev and workspace.is_contiguous(), "wh_prefix_attention: workspace")
-        need = workspace.numel() * workspace.element_size()
+        need, at = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     rc = (_lib or lib()).wh_prefix_attention(
         q.data_ptr(), stride[0] if rows > 1 else 64 * n_head, batch, n_query, n_head, n_kv_head,
         None if prefix is None else prefix.c, table, None if own is None else own.c, out.data_ptr(),
-        None if workspace is None else workspace.data_ptr(), need, s)
+        at, need, s)
     if rc != WH_OK:
         raise WhError(rc, what)
     return out
@@ -419,13 +425,13 @@ def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, worksp
     s = _stream_handle(dev, stream)
     if workspace is None:
         need = _workspace_bytes("wh_cache_evict_workspace", n_set, n_kv_head, cache.max_keys, budget)
-        workspace = _scratch(need, dev, stream)
+        scratch = _Scratch(need, s)
+        at = scratch.ptr
     else:
         _need(workspace.get_device() == dev and workspace.is_contiguous(), "wh_cache_evict: workspace")
-        need = workspace.numel() * workspace.element_size()
+        need, at = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     rc = (_lib or lib()).wh_cache_evict(cache.c, n_kv_head, budget, recent, None if out is None else out.c,
-                                        n_out.data_ptr(), indices, None if workspace is None else workspace.data_ptr(),
-                                        need, s)
+                                        n_out.data_ptr(), indices, at, need, s)
     if rc != WH_OK:
         raise WhError(rc, what)
     return n_out
