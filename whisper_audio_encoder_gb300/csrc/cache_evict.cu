@@ -24,6 +24,8 @@ constexpr int SM_ROWS = 512;         // rows that a block of it moves without a 
 constexpr int SM_HEADS = 3 * 152;    // blocks of it that are resident at once
 constexpr int SEL_THREADS = 1024;    // k_evict_select
 constexpr int SEL_HELD = 32;         // keys that a thread of it holds: longer caches are read again for every bit
+constexpr int SEL_CTAS = 8;          // blocks of a cluster that choose from one long cache
+constexpr int SEL_SPREAD = 76;       // while there are at most as many heads
 constexpr int MV_THREADS = 256;
 constexpr int MV_PIECES = 1024;      // 16-byte pieces (of keys, and of values) of a block of k_evict_move
 constexpr int SH_THREADS = 512;      // k_evict_shift
@@ -49,19 +51,39 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Threads that choose together: one warp, or a block of N warps.
-template <int THREADS>
+// Threads that choose together: one warp, a block, or the blocks of a cluster.
+template <int THREADS, int CTAS = 1>
 struct Team {
-    static constexpr int WARPS = THREADS / 32;
-    int *buf;   // [2 * WARPS]
+    static constexpr int WARPS = THREADS / 32, BLOCKS = CTAS, ALL = THREADS * CTAS;
+    int *buf;    // [2 * WARPS]
+    int *peers;  // CTAS > 1: [2][CTAS], one number of every block, in turns
+    int turn;
+    uint32_t *bins;   // CTAS > 1: [2][warp][8] and [2][block][8]
+    __device__ __forceinline__ static int rank() { return CTAS == 1 ? 0 : (int)cluster_ctarank(); }
+    __device__ __forceinline__ static int thread() {   // of the team
+        return THREADS == 32 ? threadIdx.x & 31 : rank() * THREADS + threadIdx.x;
+    }
+    // Everything written so far is visible to the whole team.
     __device__ __forceinline__ static void sync() {
-        if (WARPS == 1)
+        if (CTAS > 1)
+            cluster_sync();
+        else if (WARPS == 1)
             __syncwarp();
         else
             __syncthreads();
     }
-    // Sum over the team, the same in every thread.
-    __device__ __forceinline__ int sum(int x) const {
+    // Every block's x (the same in all of its threads), in every thread of the team: lane c holds block c's.
+    // The two turns' places alternate: a place is filled again only behind the barrier after its reads.
+    __device__ __forceinline__ int gather(int x) {
+        const int lane = threadIdx.x & 31;
+        int *mine = peers + turn * CTAS;
+        turn ^= 1;
+        if (threadIdx.x < CTAS)
+            asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_shared(mine + rank(), threadIdx.x)), "r"(x) : "memory");
+        cluster_sync();
+        return lane < CTAS ? mine[lane] : 0;
+    }
+    __device__ __forceinline__ int block_sum(int x) const {
         x = __reduce_add_sync(0xffffffffu, x);
         if (WARPS == 1) return x;
         if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
@@ -70,25 +92,38 @@ struct Team {
         __syncthreads();
         return s;
     }
-    __device__ __forceinline__ uint32_t largest(uint32_t x) const {
+    // Sum over the team, the same in every thread.
+    __device__ __forceinline__ int sum(int x) {
+        x = block_sum(x);
+        return CTAS == 1 ? x : __reduce_add_sync(0xffffffffu, gather(x));
+    }
+    __device__ __forceinline__ uint32_t largest(uint32_t x) {
         x = __reduce_max_sync(0xffffffffu, x);
-        if (WARPS == 1) return x;
-        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = (int)x;
-        __syncthreads();
-        const uint32_t m = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < WARPS ? (uint32_t)buf[threadIdx.x & 31] : 0u);
-        __syncthreads();
-        return m;
+        if (WARPS > 1) {
+            if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = (int)x;
+            __syncthreads();
+            x = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < WARPS ? (uint32_t)buf[threadIdx.x & 31] : 0u);
+            __syncthreads();
+        }
+        return CTAS == 1 ? x : __reduce_max_sync(0xffffffffu, (uint32_t)gather((int)x));
     }
     // Exclusive sums over the team's warps of two per-warp numbers.
-    __device__ __forceinline__ void before(int x, int y, int &bx, int &by) const {
+    __device__ __forceinline__ void before(int x, int y, int &bx, int &by) {
         bx = by = 0;
         if (WARPS == 1) return;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         if (lane == 0) buf[warp] = x, buf[WARPS + warp] = y;
         __syncthreads();
-        bx = __reduce_add_sync(0xffffffffu, lane < warp ? buf[lane] : 0);
-        by = __reduce_add_sync(0xffffffffu, lane < warp ? buf[WARPS + lane] : 0);
+        const int vx = lane < WARPS ? buf[lane] : 0, vy = lane < WARPS ? buf[WARPS + lane] : 0;
+        bx = __reduce_add_sync(0xffffffffu, lane < warp ? vx : 0);
+        by = __reduce_add_sync(0xffffffffu, lane < warp ? vy : 0);
+        const int tx = __reduce_add_sync(0xffffffffu, vx), ty = __reduce_add_sync(0xffffffffu, vy);
         __syncthreads();
+        if (CTAS > 1) {
+            const int gx = gather(tx), gy = gather(ty);
+            bx += __reduce_add_sync(0xffffffffu, lane < rank() ? gx : 0);
+            by += __reduce_add_sync(0xffffffffu, lane < rank() ? gy : 0);
+        }
     }
 };
 
@@ -113,30 +148,99 @@ __device__ __forceinline__ void find_threshold(int need, uint32_t most, uint32_t
     ties = need - (W == 0xffffffffu ? 0 : count(W + 1));
 }
 
+// The same for a cluster, four bits a round: every thread counts its images under the decided bits in 16 bins of
+// 8 bits, the warps, blocks and the cluster add them in bins of 16 (fewer than 65536 images in all).  A round
+// costs little more than one bit's count would, most of it the cluster barrier.
+template <int E, class T>
+__device__ __forceinline__ void find_threshold_radix(T &team, int need, const uint32_t (&key)[E], uint32_t &W, int &ties) {
+    static_assert(E < 256 && T::WARPS == 8 && T::BLOCKS == 8, "the bins' widths, the lanes' shares");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, word = lane & 7, part = lane >> 3;
+    uint32_t prefix = 0;
+    for (int shift = 28, turn = 0; shift >= 0; shift -= 4, turn ^= 1) {
+        unsigned long long c[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const uint32_t x = (key[j] ^ prefix) >> shift;   // below 16: the decided bits agree, these are the next
+            const unsigned long long one = x < 16u ? 1ull << (8 * (x & 7u)) : 0ull;
+            c[0] += x & 8u ? 0ull : one;
+            c[1] += x & 8u ? one : 0ull;
+        }
+        // bins 4i and 4i + 2 in word 2i, 4i + 1 and 4i + 3 in word 2i + 1
+        uint32_t *mine = team.bins + turn * 64;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = (uint32_t)(c[i >> 1] >> (32 * (i & 1)));
+            const uint32_t even = __reduce_add_sync(0xffffffffu, x & 0x00ff00ffu);
+            const uint32_t odd = __reduce_add_sync(0xffffffffu, (x >> 8) & 0x00ff00ffu);
+            if (lane == 0) {
+                mine[warp * 8 + 2 * i] = even;
+                mine[warp * 8 + 2 * i + 1] = odd;
+            }
+        }
+        __syncthreads();
+        uint32_t *all = team.bins + 128 + turn * 64;   // [block][word]
+        if (warp == 0) {   // lane (part, word): the block's word, to blocks part and part + 4
+            uint32_t v = mine[part * 8 + word] + mine[(part + 4) * 8 + word];
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(all + T::rank() * 8 + word, part + 4 * i)), "r"(v)
+                             : "memory");
+        }
+        cluster_sync();
+        uint32_t v = all[part * 8 + word] + all[(part + 4) * 8 + word];
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        // lane b: bin b's count, then how many images lie in bins b .. 15
+        const int b = lane & 15;
+        const int count = (int)((__shfl_sync(0xffffffffu, v, 2 * (b >> 2) + (b & 1)) >> (16 * ((b >> 1) & 1))) & 0xffffu);
+        int upward = count;
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+            const int up = __shfl_down_sync(0xffffffffu, upward, o, 16);
+            if (b + o < 16) upward += up;
+        }
+        const uint32_t reach = __ballot_sync(0xffffffffu, upward >= need) & 0xffffu;
+        const int digit = 31 - __clz(reach | 1u);
+        const int in_bin = __shfl_sync(0xffffffffu, count, digit);
+        const int above = __shfl_sync(0xffffffffu, upward, digit) - in_bin;
+        prefix |= (uint32_t)digit << shift;
+        need -= above;
+        if (in_bin == need && prefix != 0) {   // all of them stay: the next smaller image is below prefix
+            W = prefix - 1;
+            ties = 0;
+            return;
+        }
+    }
+    W = prefix;
+    ties = need;
+}
+
 // The weights of the keys that stay, to wo (which may be w): a step's reads are before its writes, and a
 // key's place is never behind it.
-template <int THREADS>
-__device__ __forceinline__ void move_weights(const Team<THREADS> team, const float *w, const int *src, int rows, float *wo) {
-    const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
+template <class T>
+__device__ __forceinline__ void move_weights(T &team, const float *w, const int *src, int rows, float *wo) {
+    const int tid = team.thread();
     constexpr int U = 4;
-    for (int base = 0; base < rows; base += U * THREADS) {
+    for (int base = 0; base < rows; base += U * T::ALL) {
         float x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = base + u * THREADS + tid < rows ? w[src[base + u * THREADS + tid]] : 0.0f;
+        for (int u = 0; u < U; ++u) x[u] = base + u * T::ALL + tid < rows ? w[src[base + u * T::ALL + tid]] : 0.0f;
         team.sync();
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (base + u * THREADS + tid < rows) wo[base + u * THREADS + tid] = x[u];
+            if (base + u * T::ALL + tid < rows) wo[base + u * T::ALL + tid] = x[u];
     }
 }
 
-// Chooses among n > budget weights w, at most THREADS * E: writes the source index of every key that stays to
+// Chooses among n > budget weights w, at most E a thread: writes the source index of every key that stays to
 // src (and kept, if not null) and its weight to wo (which may be w).  Warp k of the team holds the 32 E weights
 // from 32 E k on, lane by lane.
-template <int THREADS, int E>
-__device__ __forceinline__ void choose(const Team<THREADS> team, const float *w, int n, int budget, int recent, int *src,
-                                       int *kept, float *wo) {
-    const int lane = threadIdx.x & 31, first = (THREADS == 32 ? 0 : threadIdx.x >> 5) * 32 * E + lane;
+template <int E, class T>
+__device__ __forceinline__ void choose(T &team, const float *w, int n, int budget, int recent, int *src, int *kept,
+                                       float *wo) {
+    const int lane = threadIdx.x & 31, first = (team.thread() >> 5) * 32 * E + lane;
     const int old = n - recent, need = budget - recent;   // 0 <= need < old
     uint32_t key[E];   // past the older keys: 0, which no candidate reaches
     float raw[E];
@@ -152,7 +256,9 @@ __device__ __forceinline__ void choose(const Team<THREADS> team, const float *w,
     }
     uint32_t W = 0xffffffffu;
     int ties = 0;
-    if (need > 0) {
+    if constexpr (T::BLOCKS > 1) {
+        if (need > 0) find_threshold_radix<E>(team, need, key, W, ties);
+    } else if (need > 0) {
         hi = team.largest(hi);
         lo = ~team.largest(lo);
         find_threshold(need, hi, hi ^ lo, [&](uint32_t cand) {
@@ -164,7 +270,7 @@ __device__ __forceinline__ void choose(const Team<THREADS> team, const float *w,
     }
     // number what stays: those above W, the first `ties` equal to W, the recent ones
     int g = 0, e = 0;
-    if (THREADS > 32) {
+    if (T::ALL > 32) {
         int ng = 0, ne = 0;
 #pragma unroll
         for (int j = 0; j < E; ++j) {
@@ -204,11 +310,11 @@ __device__ __forceinline__ void choose(const Team<THREADS> team, const float *w,
         }
     }
     team.sync();
-    move_weights<THREADS>(team, w, src, budget, wo);
+    move_weights(team, w, src, budget, wo);
 }
 
 // The same for any n, reading the weights again for every bit.
-__device__ void choose_long(const Team<SEL_THREADS> team, const float *w, int n, int budget, int recent, int *src, float *wo) {
+__device__ void choose_long(Team<SEL_THREADS> &team, const float *w, int n, int budget, int recent, int *src, float *wo) {
     const int tid = threadIdx.x, lane = tid & 31;
     const int old = n - recent, need = budget - recent;
     uint32_t W = 0xffffffffu;
@@ -237,7 +343,8 @@ __device__ void choose_long(const Team<SEL_THREADS> team, const float *w, int n,
         g0 += team.sum(lane == 0 ? __popc(mg) : 0);
         e0 += team.sum(lane == 0 ? __popc(me) : 0);
     }
-    move_weights<SEL_THREADS>(team, w, src, budget, wo);
+    team.sync();
+    move_weights(team, w, src, budget, wo);
 }
 
 __device__ __forceinline__ int count_of(const EvArgs &p, int set, bool report) {
@@ -272,7 +379,8 @@ __global__ void __launch_bounds__(SM_THREADS) k_evict_small(const EvArgs p) {
             if (!p.in_place) wo[i] = w[i];
         }
     } else if (CHOOSERS != 32 || tid < 32) {
-        choose<CHOOSERS, E>(Team<CHOOSERS>{buf}, w, n, p.budget, p.recent, src, kept, wo);
+        Team<CHOOSERS> team{buf, nullptr, 0, nullptr};
+        choose<E>(team, w, n, p.budget, p.recent, src, kept, wo);
     }
     if (all && p.in_place) return;
     __syncthreads();
@@ -304,14 +412,16 @@ __global__ void __launch_bounds__(SM_THREADS) k_evict_small(const EvArgs p) {
     }
 }
 
-// Chooses only: a warp (of four) or a block per head and set.
-template <int CHOOSERS, int E>
+// Chooses only: a warp (of four), a block or a cluster of CTAS blocks per head and set.
+template <int CHOOSERS, int E, int CTAS = 1>
 __global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS) k_evict_select(const EvArgs p) {
-    __shared__ int buf[2 * SEL_THREADS / 32];
+    __shared__ int buf[2 * SEL_THREADS / 32], peers[2 * CTAS];
+    __shared__ uint32_t bins[CTAS > 1 ? 256 : 1];
     pdl_wait();
     pdl_launch_dependents();
-    const int tid = CHOOSERS == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const long long sh = CHOOSERS == 32 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x;
+    Team<CHOOSERS, CTAS> team{buf, peers, 0, bins};
+    const int tid = team.thread();
+    const long long sh = CHOOSERS == 32 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x / CTAS;
     if (sh >= (long long)p.n_set * p.n_head) return;
     const int set = (int)(sh / p.n_head), h = (int)(sh % p.n_head);
     const int n = count_of(p, set, h == 0 && tid == 0);
@@ -319,14 +429,15 @@ __global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS) k_evict_selec
     const float *w = p.weight + sh * p.max_keys;
     float *wo = p.weight_out + sh * p.out_keys;
     int *src = p.kept + sh * p.budget;
-    const Team<CHOOSERS> team{buf};
     if (n <= p.budget) {   // everything stays
-        for (int i = tid; i < n; i += CHOOSERS) {
+        for (int i = tid; i < n; i += team.ALL) {
             src[i] = i;
             if (!p.in_place) wo[i] = w[i];
         }
     } else if constexpr (E > 0) {
-        choose<CHOOSERS, E>(team, w, n, p.budget, p.recent, src, nullptr, wo);
+        if (CTAS > 1) team.sync();   // every block of the cluster is there before its memory is written
+        choose<E>(team, w, n, p.budget, p.recent, src, nullptr, wo);
+        if (CTAS > 1) team.sync();   // and none leaves before the last number was read
     } else {
         choose_long(team, w, n, p.budget, p.recent, src, wo);
     }
@@ -527,6 +638,10 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
             rc = launch_ex(k_evict_select<256, 8>, blocks, 256, 0, 1, true, s, a);
         else if (a.max_keys <= 8192)
             rc = launch_ex(k_evict_select<SEL_THREADS, 8>, blocks, SEL_THREADS, 0, 1, true, s, a);
+        else if (a.max_keys <= SEL_CTAS * 256 * 16 && items <= SEL_SPREAD)
+            rc = launch_ex(k_evict_select<256, 16, SEL_CTAS>, dim3((unsigned)(items * SEL_CTAS)), 256, 0, SEL_CTAS, true, s, a);
+        else if (a.max_keys < SEL_CTAS * 256 * 32 && items <= SEL_SPREAD)
+            rc = launch_ex(k_evict_select<256, 32, SEL_CTAS>, dim3((unsigned)(items * SEL_CTAS)), 256, 0, SEL_CTAS, true, s, a);
         else if (a.max_keys <= SEL_HELD * SEL_THREADS)
             rc = launch_ex(k_evict_select<SEL_THREADS, SEL_HELD>, blocks, SEL_THREADS, 0, 1, true, s, a);
         else
