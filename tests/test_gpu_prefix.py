@@ -290,6 +290,32 @@ def test_agrees_with_the_one_query_attention():
     assert torch.all((a - b).abs() <= 2.0 ** -7 * a.abs() + 2.0 ** -10 * kv.abs().max())
 
 
+@pytest.mark.parametrize("beams", [3, 20])
+def test_huge_scores(beams):
+    """Scores of 1e12: the softmax picks the largest.  Every query is a multiple of one key, whose score is the
+    largest by far more than fp32 rounding (64 2^-24 of the sum's magnitude)."""
+    rng = np.random.default_rng(16)
+    n = 300
+    k = _bf(rng, n, 128) * np.float32(2.0 ** 20)
+    v = _bf(rng, n, 128)
+    pick = rng.integers(0, n, size=(beams, 2))
+    q = np.concatenate([k[pick[:, h], 64 * h:64 * h + 64] for h in range(2)], axis=1)
+    own = [(k[:5], v[:5])] * beams
+    weight = torch.zeros(1, 2, n, device="cuda")
+    keys = wh.Keys(_dev(k[None]), _dev(v[None]), None, weight)
+    mine = wh.Keys(_dev(np.stack([a for a, _ in own])), _dev(np.stack([b for _, b in own])))
+    for extra in (None, mine):
+        out = wh.wh_prefix_attention(_dev(q), 2, prefix=keys, own=extra).float().cpu().numpy()
+        for b in range(beams):
+            for h in range(2):
+                cols = slice(64 * h, 64 * h + 64)
+                assert np.array_equal(out[b, cols], v[pick[b, h], cols])
+    assert abs(float(weight.sum()) - 2 * 2 * beams) < 2.01 * beams      # the picked key may also be an own one
+    for h in range(2):
+        seen = set(pick[:, h])
+        assert all(weight[0, h, t] == 0 for t in range(n) if t not in seen)
+
+
 def test_refusals_of_the_binding():
     c = Case(11, n_head=2, n_kv=2, nq=1, groups=[2, 2], n_pre=[8, 8], weigh=True)
     c.run()

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
                 m[half] = mn[half];
             }
         }
-        const float mc[2] = {m[0] == -INFINITY ? 0.0f : -m[0] * PA_SCALE, m[1] == -INFINITY ? 0.0f : -m[1] * PA_SCALE};
+        const float ms[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (h == 1 && slots == 1) break;
@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
 #pragma unroll
             for (int x = 0; x < 4; ++x) {   // rows g, g + 8 of keys 2c, 2c + 1, then of keys 8 + 2c, 9 + 2c
                 const float *sx = s[2 * h + (x >> 1)] + 2 * (x & 1);
-                const float e0 = ex2_approx(fmaf(sx[0], PA_SCALE, mc[x & 1]));
-                const float e1 = ex2_approx(fmaf(sx[1], PA_SCALE, mc[x & 1]));
+                const float e0 = ex2_approx((sx[0] - ms[x & 1]) * PA_SCALE);
+                const float e1 = ex2_approx((sx[1] - ms[x & 1]) * PA_SCALE);
                 l[x & 1] += e0 + e1;
                 hi[x] = pack_bf16(e0, e1);
                 lo[x] = pack_bf16(e0 - __uint_as_float(hi[x] << 16), e1 - __uint_as_float(hi[x] & 0xffff0000u));
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         ls += __shfl_xor_sync(0xffffffffu, ls, 2);
         const int r = g + 8 * half;
         if (r0 + r >= rw.n) continue;
-        if (c == 0) sml[warp][r] = make_float2(m[half] * PA_SCALE, ls);
+        if (c == 0) sml[warp][r] = make_float2(m[half], ls);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             *reinterpret_cast<float2 *>(so(warp, r) + 8 * j + 2 * c) = make_float2(o[j][2 * half], o[j][2 * half + 1]);
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         float lt = 0.0f, v[8] = {};
         for (int w = 0; w < wpi; ++w) {
             const float2 ml = sml[w0 + w][r];
-            const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mt);
+            const float f = ml.x == -INFINITY ? 0.0f : ex2_approx((ml.x - mt) * PA_SCALE);
             lt = fmaf(ml.y, f, lt);
             const float4 x = *reinterpret_cast<const float4 *>(so(w0 + w, r) + d0);
             const float4 y = *reinterpret_cast<const float4 *>(so(w0 + w, r) + d0 + 4);
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
                 const float *sr = scores + r * ks.chunk + t;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (t + u * 32 * wpi < k1) add[u] = fmaf(ex2_approx(fmaf(sr[u * 32 * wpi], PA_SCALE, -st.x)), st.y, add[u]);
+                    if (t + u * 32 * wpi < k1) add[u] = fmaf(ex2_approx((sr[u * 32 * wpi] - st.x) * PA_SCALE), st.y, add[u]);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -390,12 +390,12 @@ __global__ void __launch_bounds__(16 * PM_ROWS) k_prefix_merge(const PaArgs p) {
         float mn = m;
 #pragma unroll
         for (int i = 0; i < PM_BATCH; ++i) mn = fmaxf(mn, x[i].x);
-        const float f = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
+        const float f = m == -INFINITY ? 0.0f : ex2_approx((m - mn) * PA_SCALE);
         l *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
         m = mn;
 #pragma unroll
         for (int i = 0; i < PM_BATCH; ++i) {
-            const float e = x[i].x == -INFINITY ? 0.0f : ex2_approx(x[i].x - m);
+            const float e = x[i].x == -INFINITY ? 0.0f : ex2_approx((x[i].x - m) * PA_SCALE);
             l = fmaf(x[i].y, e, l);
             o.x = fmaf(v[i].x, e, o.x), o.y = fmaf(v[i].y, e, o.y), o.z = fmaf(v[i].z, e, o.z), o.w = fmaf(v[i].w, e, o.w);
         }
@@ -487,8 +487,10 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int key = t0 + 8 * j + 2 * c + (i & 1);
-                    const float e = ex2_approx(fmaf(s[i], PA_SCALE, -st[i >> 1].x));
-                    if (key < lim[i >> 1]) acc[j][i & 1] = fmaf(e, st[i >> 1].y, acc[j][i & 1]);
+                    // (no weight is above 1: where scores are so large that another kernel's rounding of the same
+                    // score is far off this one's, the difference must not run away)
+                    const float e = ex2_approx((s[i] - st[i >> 1].x) * PA_SCALE) * st[i >> 1].y;
+                    if (key < lim[i >> 1]) acc[j][i & 1] += e > 1.0f ? 1.0f : e;
                 }
             }
         }

@@ -6,7 +6,9 @@
 
 namespace wh {
 
-constexpr float PA_SCALE = 0.125f * 1.4426950408889634f;   // log2(e) / sqrt(64): scores in the exp2 domain
+// Weights are 2^((s - m) log2(e) / sqrt(64)) of the raw products s = q . k and their maximum m: the difference
+// comes first, so that it is exact near the maximum however large the scores are.
+constexpr float PA_SCALE = 0.125f * 1.4426950408889634f;
 
 struct PaSet {
     const __nv_bfloat16 *k, *v;
@@ -155,7 +157,7 @@ __device__ __forceinline__ float2 finish_row(const PaArgs &p, const Rows &rw, in
         const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * 64 + d0 + 4));
         const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         const float mn = fmaxf(mt, ml.x);
-        const float f = mt == -INFINITY ? 0.0f : ex2_approx(mt - mn), e = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mn);
+        const float f = mt == -INFINITY ? 0.0f : ex2_approx((mt - mn) * PA_SCALE), e = ml.x == -INFINITY ? 0.0f : ex2_approx((ml.x - mn) * PA_SCALE);
         lt = lt * f + ml.y * e;
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = v[k] * f + u[k] * e;
@@ -196,7 +198,7 @@ __device__ __forceinline__ void finish_cluster(const PaArgs &p, const Rows &rw, 
                          : "r"(rb + 16)
                          : "memory");
             const float mn = fmaxf(mt, m);
-            const float f = mt == -INFINITY ? 0.0f : ex2_approx(mt - mn), e = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
+            const float f = mt == -INFINITY ? 0.0f : ex2_approx((mt - mn) * PA_SCALE), e = m == -INFINITY ? 0.0f : ex2_approx((m - mn) * PA_SCALE);
             lt = lt * f + l * e;
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = v[k] * f + u[k] * e;

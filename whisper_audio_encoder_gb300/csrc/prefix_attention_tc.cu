@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
                     tmem_wait_st();
                 }
             }
-            const float mc = m == -INFINITY ? 0.0f : m * PA_SCALE;
-            const uint64_t scale2 = f2_pack(PA_SCALE, PA_SCALE), minus2 = f2_pack(-mc, -mc);
+            const float ms = m == -INFINITY ? 0.0f : m;
+            const uint64_t scale2 = f2_pack(PA_SCALE, PA_SCALE), minus2 = f2_pack(-ms, -ms);
             uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
             for (int i = 0; i < COLS / 32; ++i) {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     float x0, x1;
-                    f2_unpack(fma_f2(f2_pack(__uint_as_float(sv[i][2 * k]), __uint_as_float(sv[i][2 * k + 1])), scale2, minus2),
+                    f2_unpack(mul_f2(add_f2(f2_pack(__uint_as_float(sv[i][2 * k]), __uint_as_float(sv[i][2 * k + 1])), minus2), scale2),
                               x0, x1);
                     const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
                     sum2[k & 1] = add_f2(sum2[k & 1], f2_pack(e0, e1));
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
         // every product is done, so the ring is free: stage O, merge the copies, then the ranges
         float2 *sml_copy = sml + 128;
         if (ok) {
-            sml_copy[a] = make_float2(m == -INFINITY ? m : m * PA_SCALE, l);
+            sml_copy[a] = make_float2(m, l);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t v[32];
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
 #pragma unroll
                 for (int c = 0; c < COPIES; ++c) {
                     const float2 ml = sml_copy[r + TILE * c];
-                    const float f = COPIES == 1 ? 1.0f : ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mt);
+                    const float f = COPIES == 1 ? 1.0f : ml.x == -INFINITY ? 0.0f : ex2_approx((ml.x - mt) * PA_SCALE);
                     lt = fmaf(ml.y, f, lt);
 #pragma unroll
                     for (int k = 0; k < 8; k += 4) {
