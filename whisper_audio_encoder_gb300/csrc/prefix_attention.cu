@@ -523,6 +523,8 @@ constexpr long long PT_BLOCKS = 2 * 152;   // k_prefix_tc: 2 on each
 constexpr int PT_MIN_ROWS = 16;
 constexpr int PA_CLUSTER = 16, PT_CLUSTER = 2;
 constexpr int PA_CLUSTER_KEYS = 512, PT_CLUSTER_KEYS = 0;
+// Clusters of k_prefix_attention's blocks by size that GB300 holds at once (cudaOccupancyMaxActiveClusters)
+constexpr int PA_CLUSTERS[PA_CLUSTER + 1] = {0, 456, 228, 148, 110, 87, 74, 59, 51, 46, 43, 36, 36, 28, 26, 26, 21};
 constexpr int PA_SCORE_BYTES = 8192;
 constexpr int PA_OWN_LEAST = 512;   // beside a prefix, shorter own keys are not cut into ranges: that saves the merge
 void split_keys(PaSet &s, long long items, long long blocks, int step, int least, int cluster, int cluster_keys) {
@@ -532,6 +534,8 @@ void split_keys(PaSet &s, long long items, long long blocks, int step, int least
     const long long most = (s.max_keys + least - 1) / least;
     n = n < 1 ? 1 : (n > most ? most : n);
     if (n > cluster && (long long)cluster * cluster_keys >= s.max_keys) n = cluster;
+    if (cluster == PA_CLUSTER && n <= cluster)
+        while (n > 1 && items > PA_CLUSTERS[n]) --n;   // all clusters at once
     s.chunk = (int)(((s.max_keys + n - 1) / n + step - 1) / step * step);
     s.splits = (s.max_keys + s.chunk - 1) / s.chunk;
 }

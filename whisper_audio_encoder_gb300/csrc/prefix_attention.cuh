@@ -149,19 +149,37 @@ __device__ __forceinline__ float2 finish_row(const PaArgs &p, const Rows &rw, in
     int qrow, head, qi;
     rw.locate(p, r, qrow, head, qi);
     const long long row = (long long)qrow * p.n_head + head;
-#pragma unroll 2
-    for (int i = 0; i < pre_parts; ++i) {
-        const long long at = row * p.n_part + i;
-        const float2 ml = __ldcg(p.part_ml + at);
-        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * 64 + d0));
-        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * 64 + d0 + 4));
-        const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        const float mn = fmaxf(mt, ml.x);
-        const float f = mt == -INFINITY ? 0.0f : ex2_approx((mt - mn) * PA_SCALE), e = ml.x == -INFINITY ? 0.0f : ex2_approx((ml.x - mn) * PA_SCALE);
-        lt = lt * f + ml.y * e;
+    constexpr int BATCH = 4;   // partial results whose loads are under way together
+    for (int i0 = 0; i0 < pre_parts; i0 += BATCH) {
+        float2 ml[BATCH];
+        float4 x[BATCH], y[BATCH];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = v[k] * f + u[k] * e;
+        for (int i = 0; i < BATCH; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.0f);
+            x[i] = y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i0 + i < pre_parts) {
+                const long long at = row * p.n_part + i0 + i;
+                ml[i] = __ldcg(p.part_ml + at);
+                x[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * 64 + d0));
+                y[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * 64 + d0 + 4));
+            }
+        }
+        float mn = mt;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) mn = fmaxf(mn, ml[i].x);
+        const float f = mt == -INFINITY ? 0.0f : ex2_approx((mt - mn) * PA_SCALE);
+        lt *= f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= f;
         mt = mn;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const float e = ml[i].x == -INFINITY ? 0.0f : ex2_approx((ml[i].x - mt) * PA_SCALE);
+            const float u[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
+            lt = fmaf(ml[i].y, e, lt);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = fmaf(u[k], e, v[k]);
+        }
     }
     const float2 st = make_float2(mt == -INFINITY ? 0.0f : mt, lt == 0.0f ? 0.0f : 1.0f / lt);   // no key: zeros
     *reinterpret_cast<uint4 *>(p.out + row * 64 + d0) =

@@ -70,9 +70,14 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
     pdl_launch_dependents();
     Rows rw;
     int set, r0;
-    const int split = blockIdx.x % p.pre.splits, slot = blockIdx.x / p.pre.splits % p.slots;
-    rw.hk = blockIdx.x / p.pre.splits / p.slots;
+    // a cluster's blocks are the ranges of one item; else neighbours are tiles and heads, which read the same
+    // rows or the same DRAM pages at about the same time
     const int cluster = p.pre_cluster;
+    const unsigned tiles = p.slots * p.n_kv;
+    const int split = cluster > 1 ? blockIdx.x % cluster : blockIdx.x / tiles;
+    const unsigned item = cluster > 1 ? blockIdx.x / cluster : blockIdx.x % tiles;
+    const int slot = item % p.slots;
+    rw.hk = item / p.slots;
     if (cluster && split == 0) finish_outside(p, slot, rw.hk);
     if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw)) return;
     const int nk = clamp_count(p.pre, set);
@@ -390,7 +395,8 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
 
 template <int COPIES>
 int set_attr() {
-    return cudaFuncSetAttribute(k_prefix_tc<COPIES>, cudaFuncAttributeMaxDynamicSharedMemorySize, PT_SMEM) == cudaSuccess
+    return cudaFuncSetAttribute(k_prefix_tc<COPIES>, cudaFuncAttributeMaxDynamicSharedMemorySize, PT_SMEM) == cudaSuccess &&
+                   cudaFuncSetAttribute(k_prefix_tc<COPIES>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess
                ? WH_OK
                : WH_ECUDA;
 }
