@@ -206,6 +206,54 @@ def test_attend_evict_attend():
     assert wh.wh_status() == wh.WH_OK
 
 
+def test_beam_search_loop_with_a_bounded_cache():
+    """Three decoder layers as beam search uses them: the hypotheses of two windows share their window's
+    cross-attention keys (wh_prepare_cross rows) and their utterance's prompt, keep their own tokens' keys with
+    accumulated weight, and all layers' caches are cut in one call whenever they are full.  Every step's attention
+    is compared with the oracle on the very keys that the caches hold."""
+    from whisper_audio_encoder_gb300 import synth
+    rng = np.random.default_rng(8)
+    bf = lambda *s: synth.bf16_round(rng.standard_normal(s).astype(np.float32))  # noqa: E731
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(torch.bfloat16).cuda()  # noqa: E731
+    layers, windows, beams, H, cap, m, r, n_ctx, prompt = 3, 2, 5, 2, 12, 7, 2, 90, 20
+    B, d = windows * beams, 64 * H
+    cross, pre = bf(layers, windows, n_ctx, 2 * d), bf(layers, windows, prompt, 2 * d)
+    crossd, pred = dev(cross), dev(pre)
+    kc, vc = torch.zeros(2, layers * B, cap, d, dtype=torch.bfloat16, device="cuda")
+    weight = torch.zeros(layers * B, H, cap, device="cuda")
+    n = torch.zeros(layers * B, dtype=torch.int32, device="cuda")
+    whole = wh.Keys(kc, vc, n, weight)
+    own = [wh.Keys(*(x[l * B:(l + 1) * B] for x in (kc, vc, n, weight))) for l in range(layers)]
+    host = lambda x: x.float().cpu().numpy()  # noqa: E731
+    group = [b // beams for b in range(B)]
+    for step in range(19):
+        if step and int(n[0]) == cap:
+            before = host(weight).astype(np.float32), host(kc)
+            wh.wh_cache_evict(whole, H, m, r)
+            assert n.tolist() == [m] * (layers * B)
+            for i in (0, layers * B - 1):
+                for h in range(H):
+                    at = R.cache_evict(before[0][i, h], m, r)
+                    assert np.array_equal(host(kc)[i, :m, 64 * h:64 * h + 64], before[1][i, at, 64 * h:64 * h + 64])
+        at = int(n[0])
+        kc[:, at], vc[:, at] = dev(bf(layers * B, d)), dev(bf(layers * B, d))
+        n += 1
+        for l in range(layers):
+            q = bf(B, d)
+            w0 = host(own[l].weight)
+            o_self = wh.wh_prefix_attention(dev(q), H, prefix=wh.Keys(pred[l][..., :d], pred[l][..., d:]), own=own[l])
+            o_cross = wh.wh_prefix_attention(dev(q), H, prefix=wh.Keys(crossd[l][..., :d], crossd[l][..., d:]))
+            k, v = host(own[l].k), host(own[l].v)
+            ref, spread, _, wo = R.prefix_attention(q, 1, H, H, [(x[:, :d], x[:, d:]) for x in pre[l]], group,
+                                                    [(k[b, :at + 1], v[b, :at + 1]) for b in range(B)])
+            assert np.all(np.abs(host(o_self) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * spread)
+            add = host(own[l].weight)[:, :, :at + 1] - w0[:, :, :at + 1]
+            assert np.allclose(add, np.stack(wo), rtol=2.0 ** -11, atol=2.0 ** -20)
+            ref, spread, _, _ = R.prefix_attention(q, 1, H, H, [(x[:, :d], x[:, d:]) for x in cross[l]], group, [None] * B)
+            assert np.all(np.abs(host(o_cross) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -12) * spread)
+    assert wh.wh_status() == wh.WH_OK
+
+
 def test_refusals_of_the_binding():
     c = Case(heads=2, cap=10, counts=[10], budget=4, recent=1)
     cache = wh.Keys(c.k, c.v, c.n, c.w)

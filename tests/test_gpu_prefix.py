@@ -316,6 +316,30 @@ def test_huge_scores(beams):
         assert all(weight[0, h, t] == 0 for t in range(n) if t not in seen)
 
 
+def test_empty_batch():
+    k = torch.zeros(0, 9, 128, dtype=torch.bfloat16, device="cuda")
+    out = wh.wh_prefix_attention(torch.zeros(0, 128, dtype=torch.bfloat16, device="cuda"), 2, own=wh.Keys(k, k))
+    assert out.shape == (0, 128)
+
+
+def test_two_calls_at_once():
+    """Two streams, each its own calls over shared inputs: nothing in the library is shared between them."""
+    kw = dict(n_head=4, n_kv=2, nq=2, n_own=[40 + i for i in range(24)])
+    cases = [Case(17, groups=[8, 8, 8], n_pre=[900, 1000, 1100], **kw), Case(18, groups=[20, 4], n_pre=[3000, 50], **kw)]
+    refs = [c.run() for c in cases]
+    args = [dict(q=_dev(c.q), n_head=4, prefix=c.pk, own=c.ok, n_kv_head=2, n_query=2,
+                 group_start=torch.from_numpy(c.start).cuda()) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(wh.wh_prefix_attention(**args[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, refs[i]) for i in range(2) for x in outs[i]) and wh.wh_status() == wh.WH_OK
+
+
 def test_refusals_of_the_binding():
     c = Case(11, n_head=2, n_kv=2, nq=1, groups=[2, 2], n_pre=[8, 8], weigh=True)
     c.run()

@@ -64,6 +64,7 @@ def test_workspace(L):
 
 def test_empty_batch_is_a_no_op(L):
     assert _call(L, batch=0, prefix=_keys(), q=None, out=None, ws=None, ws_bytes=0) == wh.WH_OK
+    assert _call(L, batch=0, own=_keys(n_set=0, k=None, v=None), q=None, out=None, ws=None, ws_bytes=0) == wh.WH_OK
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device path")

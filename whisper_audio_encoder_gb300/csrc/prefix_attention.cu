@@ -699,13 +699,13 @@ extern "C" int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch
                                    wh_bf16 *out, void *workspace, size_t ws_bytes, void *stream) {
     if (!shape_ok(batch, n_query, n_head, n_kv_head) || q_stride < 64LL * n_head || q_stride % 8 != 0) return WH_EINVAL;
     if (!prefix && !own) return WH_EINVAL;
+    if (batch == 0) return WH_OK;
     PaArgs a = {};
     if (int rc = check_keys(prefix, n_kv_head, &a.pre)) return rc;
     if (int rc = check_keys(own, n_kv_head, &a.own)) return rc;
-    if (own && own->n_set != batch && batch > 0) return WH_EINVAL;
+    if (own && own->n_set != batch) return WH_EINVAL;
     if (group_start && (!prefix || !fits(group_start, 4))) return WH_EINVAL;
     if (prefix && !group_start && batch % prefix->n_set != 0) return WH_EINVAL;
-    if (batch == 0) return WH_OK;
     if (!fits(q, 16) || !fits(out, 16) || (workspace && !fits(workspace, 256))) return WH_EINVAL;
     a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
     a.q_stride = q_stride;
