@@ -58,12 +58,12 @@ def test_rejects_what_shares_memory(L):
 def test_workspace(L):
     size = L.wh_cache_evict_workspace
     assert size(3, 2, 100, 40) == 0                       # one kernel
-    need = size(3, 200, 100, 40)
-    assert need >= 3 * 4 + 3 * 200 * 40 * 4
-    wide = dict(row_stride=12800, set_stride=1280000, v=P + (1 << 26), weight=P + (1 << 27))
-    assert _call(L, _keys(**wide), n_kv=200, ws_bytes=need - 1) == wh.WH_ENOSPC
-    assert _call(L, _keys(**wide), n_kv=200, ws=None) == wh.WH_ENOSPC
-    for args in ((0, 200, 100, 40), (3, 0, 100, 40), (3, 200, 0, 40), (3, 200, 100, 0)):
+    need = size(3, 300, 100, 40)
+    assert need >= 3 * 4 + 3 * 300 * 40 * 4
+    wide = dict(row_stride=19200, set_stride=1920000, v=P + (1 << 26), weight=P + (1 << 27))
+    assert _call(L, _keys(**wide), n_kv=300, ws_bytes=need - 1) == wh.WH_ENOSPC
+    assert _call(L, _keys(**wide), n_kv=300, ws=None) == wh.WH_ENOSPC
+    for args in ((0, 300, 100, 40), (3, 0, 100, 40), (3, 300, 0, 40), (3, 300, 100, 0)):
         assert size(*args) == 0
 
 

@@ -20,12 +20,20 @@ namespace {
 
 constexpr int SM_THREADS = 256;      // k_evict_small
 constexpr int SM_MOST = 2048;        // its longest cache
-constexpr int SM_ROWS = 512;         // rows that a block of it moves without a second thought
-constexpr int SM_HEADS = 3 * 152;    // blocks of it that are resident at once
-constexpr int SEL_THREADS = 1024;    // k_evict_select
+// It is taken for up to SM_HEADS heads (what is resident at once) that move up to SM_ROWS rows, or for at least
+// half as many heads that move more; us a call in one kernel and in two, keys -> budget:
+//    12 heads  448 ->  224    8.9  10.3      480 heads  448 -> 224    17.1  20.5
+//   320 heads  448 ->  224   14.4  16.4      800 heads  448 -> 224    25.9  26.2
+//    12 heads 2000 ->  600   13.0  12.1      200 heads 2000 -> 1500   35.2  35.4
+//    12 heads 2000 -> 1500   17.1  10.9   (the second kernel costs the host 4 us more)
+constexpr int SM_ROWS = 1024;
+constexpr int SM_HEADS = 4 * 152;
+constexpr int SEL_THREADS = 1024;    // k_evict_select, one block a head
 constexpr int SEL_HELD = 32;         // keys that a thread of it holds: longer caches are read again for every bit
-constexpr int SEL_CTAS = 8;          // blocks of a cluster that choose from one long cache
-constexpr int SEL_SPREAD = 76;       // while there are at most as many heads
+// Clusters of SEL_CTAS blocks of 256 threads choose instead for few heads of long caches, and for the longest:
+// 20 heads x 9000 keys 26.0 us, 31.4 with a block each; 60 heads 47.3 and 42.2; 20 x 60000 43.8 and 155.
+constexpr int SEL_CTAS = 8;
+constexpr int SEL_SPREAD = 40;
 constexpr int MV_THREADS = 256;
 constexpr int MV_PIECES = 1024;      // 16-byte pieces (of keys, and of values) of a block of k_evict_move
 constexpr int SH_THREADS = 512;      // k_evict_shift
@@ -512,7 +520,6 @@ __global__ void k_evict_counts(const EvArgs p, int *n_out) {
         n_out[i] = min(count_of(p, i, false), p.budget);
 }
 
-// One kernel for short caches of as many heads as are resident at once, unless few of them move many rows.
 bool one_kernel(int n_set, int n_head, int max_keys, int budget) {
     const long long items = (long long)n_set * n_head;
     return max_keys <= SM_MOST && items <= SM_HEADS &&
@@ -640,7 +647,7 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
             rc = launch_ex(k_evict_select<SEL_THREADS, 8>, blocks, SEL_THREADS, 0, 1, true, s, a);
         else if (a.max_keys <= SEL_CTAS * 256 * 16 && items <= SEL_SPREAD)
             rc = launch_ex(k_evict_select<256, 16, SEL_CTAS>, dim3((unsigned)(items * SEL_CTAS)), 256, 0, SEL_CTAS, true, s, a);
-        else if (a.max_keys < SEL_CTAS * 256 * 32 && items <= SEL_SPREAD)
+        else if (a.max_keys < SEL_CTAS * 256 * 32 && (items <= SEL_SPREAD || a.max_keys > SEL_HELD * SEL_THREADS))
             rc = launch_ex(k_evict_select<256, 32, SEL_CTAS>, dim3((unsigned)(items * SEL_CTAS)), 256, 0, SEL_CTAS, true, s, a);
         else if (a.max_keys <= SEL_HELD * SEL_THREADS)
             rc = launch_ex(k_evict_select<SEL_THREADS, SEL_HELD>, blocks, SEL_THREADS, 0, 1, true, s, a);

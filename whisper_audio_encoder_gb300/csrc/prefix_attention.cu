@@ -20,7 +20,7 @@ constexpr int PA_RING = 4 * PA_SLOT;
 constexpr int PA_SMEM = PA_WARPS * PA_RING;
 constexpr int SO_ROW = 68;         // floats a row of the warps' staged results
 constexpr int PM_BATCH = 8;        // partial results that a merging thread loads at once
-constexpr int PM_ROWS = 4;         // rows of one merge block (16 threads a row)
+constexpr int PM_TEAMS = 8;        // teams of 16 threads in a merging block
 constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
 constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp step
 constexpr int PW_BLOCKS = 8 * 152; // weight kernel: blocks, some twice what is resident at once
@@ -356,15 +356,18 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     }
 }
 
-// o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the ranges of a row that hold keys, in order.  16
-// threads a row, PM_BATCH ranges at a time, all of their loads before any arithmetic.
-__global__ void __launch_bounds__(16 * PM_ROWS) k_prefix_merge(const PaArgs p) {
+// o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the ranges of a row that hold keys.  16 threads hold a
+// row's dims; TEAMS such teams share a row's ranges (team k takes ranges k PM_BATCH .. and so on, PM_BATCH at a
+// time, all of their loads before any arithmetic) and are joined in order at the end.
+template <int TEAMS>
+__global__ void __launch_bounds__(16 * PM_TEAMS) k_prefix_merge(const PaArgs p) {
+    constexpr int ROWS = PM_TEAMS / TEAMS;
     pdl_launch_dependents();
     const long long rows = (long long)p.batch * p.nq * p.n_head;
-    const long long mine = (long long)blockIdx.x * PM_ROWS + (threadIdx.x >> 4), row = min(mine, rows - 1);
-    const int lane = threadIdx.x & 15;
+    const int lane = threadIdx.x & 15, in_block = (threadIdx.x >> 4) % ROWS, team = (threadIdx.x >> 4) / ROWS;
+    const long long mine = (long long)blockIdx.x * ROWS + in_block, row = min(mine, rows - 1);
     const int b = (int)(row / ((long long)p.nq * p.n_head));
-    // (the two rows of a warp may belong to different sequences: one after the other)
+    // (the two teams of a warp may have rows of different sequences: one after the other)
     const int b0 = __shfl_sync(0xffffffffu, b, 0), b1 = __shfl_sync(0xffffffffu, b, 16);
     const int np0 = pre_parts_of(p, group_of(p, b0)), np1 = b1 == b0 ? np0 : pre_parts_of(p, group_of(p, b1));
     const int np = (threadIdx.x & 16) ? np1 : np0;
@@ -374,9 +377,25 @@ __global__ void __launch_bounds__(16 * PM_ROWS) k_prefix_merge(const PaArgs p) {
     pdl_wait();   // the partial results; what came before only reads the call's inputs
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = 0; i0 < n; i0 += PM_BATCH) {
-        float2 x[PM_BATCH];
-        float4 v[PM_BATCH];
+    auto add = [&](const float2 *x, const float4 *v, int count) {
+        float mn = m;
+#pragma unroll
+        for (int i = 0; i < PM_BATCH; ++i)
+            if (i < count) mn = fmaxf(mn, x[i].x);
+        const float f = m == -INFINITY ? 0.0f : ex2_approx((m - mn) * PA_SCALE);
+        l *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+        m = mn;
+#pragma unroll
+        for (int i = 0; i < PM_BATCH; ++i) {
+            if (i >= count) continue;
+            const float e = x[i].x == -INFINITY ? 0.0f : ex2_approx((x[i].x - m) * PA_SCALE);
+            l = fmaf(x[i].y, e, l);
+            o.x = fmaf(v[i].x, e, o.x), o.y = fmaf(v[i].y, e, o.y), o.z = fmaf(v[i].z, e, o.z), o.w = fmaf(v[i].w, e, o.w);
+        }
+    };
+    float2 x[PM_BATCH];
+    float4 v[PM_BATCH];
+    for (int i0 = team * PM_BATCH; i0 < n; i0 += TEAMS * PM_BATCH) {
 #pragma unroll
         for (int i = 0; i < PM_BATCH; ++i) {
             x[i] = make_float2(-INFINITY, 0.0f);
@@ -387,17 +406,19 @@ __global__ void __launch_bounds__(16 * PM_ROWS) k_prefix_merge(const PaArgs p) {
                 v[i] = __ldcg(po + s * 16);
             }
         }
-        float mn = m;
-#pragma unroll
-        for (int i = 0; i < PM_BATCH; ++i) mn = fmaxf(mn, x[i].x);
-        const float f = m == -INFINITY ? 0.0f : ex2_approx((m - mn) * PA_SCALE);
-        l *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-        m = mn;
-#pragma unroll
-        for (int i = 0; i < PM_BATCH; ++i) {
-            const float e = x[i].x == -INFINITY ? 0.0f : ex2_approx((x[i].x - m) * PA_SCALE);
-            l = fmaf(x[i].y, e, l);
-            o.x = fmaf(v[i].x, e, o.x), o.y = fmaf(v[i].y, e, o.y), o.z = fmaf(v[i].z, e, o.z), o.w = fmaf(v[i].w, e, o.w);
+        add(x, v, PM_BATCH);
+    }
+    if (TEAMS > 1) {
+        __shared__ float4 so[PM_TEAMS][16];
+        __shared__ float2 sml[PM_TEAMS];
+        so[threadIdx.x >> 4][lane] = o;
+        if (lane == 0) sml[threadIdx.x >> 4] = make_float2(m, l);
+        __syncthreads();
+        if (team > 0) return;
+        for (int k = 1; k < TEAMS; ++k) {
+            x[0] = sml[k * ROWS + in_block];
+            v[0] = so[k * ROWS + in_block][lane];
+            add(x, v, 1);
         }
     }
     if (mine >= rows) return;
@@ -516,26 +537,49 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
 
 size_t up256p(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Key ranges of a set: as many as are resident at once, in whole steps of a block, of at least `least` keys.  No more than one cluster's
-// blocks if those then take at most `cluster_keys` keys each: joining ranges in a cluster saves a kernel.
 constexpr long long PA_BLOCKS = 3 * 152;   // k_prefix_attention: 3 blocks on each of GB300's 152 SMs
 constexpr long long PT_BLOCKS = 2 * 152;   // k_prefix_tc: 2 on each
+// The prefix part goes to k_prefix_tc when its sets have more than PT_MIN_ROWS rows on average and there are at
+// least PT_MIN_WORK products of a 16-row tile with a key (k_prefix_attention's units) to do: below that its
+// blocks' longer set-up (TMEM, tensor maps) does not pay.  Measured, us a call, 20 key heads:
+//   rows x keys x sets   products   k_prefix_attention   k_prefix_tc
+//    40 x  400 x  1         24 k          10.3              12.3
+//   128 x 1500 x  1        240 k          15.7              17.7
+//    40 x 1500 x  4        360 k          18.4              17.7
+//    64 x 1500 x  4        480 k          21.7              18.5
+//    40 x 8000 x  1        480 k          22.6              20.9
+//   128 x 1500 x 16        3.8 M          97                47
+// Beside own keys, whose blocks hide the set-up, more than twice PT_MIN_ROWS rows are enough: 200 rows x 400
+// keys, 8 heads, with up to 224 own keys 22.3 and 20.0.
 constexpr int PT_MIN_ROWS = 16;
-constexpr int PA_CLUSTER = 16, PT_CLUSTER = 2;
-constexpr int PA_CLUSTER_KEYS = 512, PT_CLUSTER_KEYS = 0;
-// Clusters of k_prefix_attention's blocks by size that GB300 holds at once (cudaOccupancyMaxActiveClusters)
+constexpr long long PT_MIN_WORK = 300000;
+// Ranges of at least PT_LEAST keys (rounded down): a shorter block does not make up for joining one range more.
+// 128 rows x 800 keys x 4 sets: 16.4 us with one range, 20.5 with the three that would fill the device;
+// 40 rows x 8000 keys: 20.9 with 15, 58.8 with one.
+constexpr int PT_LEAST = 512;
+constexpr int PA_CLUSTER = 16, PT_CLUSTER = 2;   // ranges that a cluster's blocks join by themselves
+// Up to this many keys a block, one cluster instead of more ranges and the merge kernel: 5 rows x 2 heads x
+// 30000 keys 17.8 us in clusters of 16, 30 us in 228 ranges; 5 x 6 x 1500: 8.2 in 16, 11.7 in 24.
+constexpr int PA_CLUSTER_KEYS = 2048;
+// Clusters of k_prefix_attention's blocks, by size, that GB300 holds at once (cudaOccupancyMaxActiveClusters)
 constexpr int PA_CLUSTERS[PA_CLUSTER + 1] = {0, 456, 228, 148, 110, 87, 74, 59, 51, 46, 43, 36, 36, 28, 26, 26, 21};
-constexpr int PA_SCORE_BYTES = 8192;
-constexpr int PA_OWN_LEAST = 512;   // beside a prefix, shorter own keys are not cut into ranges: that saves the merge
-void split_keys(PaSet &s, long long items, long long blocks, int step, int least, int cluster, int cluster_keys) {
+constexpr int PA_SCORE_BYTES = 8192;   // own keys' scores kept by a block; three blocks still fit an SM
+// Beside a prefix, own keys are cut into ranges of at least this many: one range needs no merge kernel.  2
+// sequences x 6 heads x 900 keys: 12.4 us, 10.3 with ranges of 64 keys, but 4 us more of the host's time.
+constexpr int PA_OWN_LEAST = 512;
+
+// Key ranges of a set: as many as are resident at once, in whole steps of a block, `most` at most.
+void split_keys(PaSet &s, long long items, long long blocks, int step, long long most) {
     s.splits = s.chunk = 0;
     if (s.n_set <= 0) return;
     long long n = blocks / items;
-    const long long most = (s.max_keys + least - 1) / least;
-    n = n < 1 ? 1 : (n > most ? most : n);
-    if (n > cluster && (long long)cluster * cluster_keys >= s.max_keys) n = cluster;
-    if (cluster == PA_CLUSTER && n <= cluster)
-        while (n > 1 && items > PA_CLUSTERS[n]) --n;   // all clusters at once
+    n = n > most ? most : n;
+    n = n < 1 ? 1 : n;
+    if (blocks != PT_BLOCKS) {
+        if (n > PA_CLUSTER && (long long)PA_CLUSTER * PA_CLUSTER_KEYS >= s.max_keys) n = PA_CLUSTER;
+        if (n <= PA_CLUSTER)
+            while (n > 1 && items > PA_CLUSTERS[n]) --n;   // all clusters at once
+    }
     s.chunk = (int)(((s.max_keys + n - 1) / n + step - 1) / step * step);
     s.splits = (s.max_keys + s.chunk - 1) / s.chunk;
 }
@@ -552,25 +596,27 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     const long long per = (long long)a.nq * a.rep, all = a.batch * per;
     const long long rows_a_set = a.pre.n_set > 0 ? (all + a.pre.n_set - 1) / a.pre.n_set : 0;
     const bool has_pre = a.pre.n_set > 0, has_own = a.own.n_set > 0;
-    pl.tc = may_tc && rows_a_set > PT_MIN_ROWS;
+    const auto slots = [&](int tile) {   // row tiles of a key head over all sets, with ragged groups at most
+        return a.gsize == 0 ? a.pre.n_set + all / tile : a.pre.n_set * ((a.gsize * per + tile - 1) / tile);
+    };
+    const bool much = slots(PA_TILE) * a.n_kv * a.pre.max_keys >= PT_MIN_WORK;
+    pl.tc = may_tc && rows_a_set > PT_MIN_ROWS && (much || (has_own && rows_a_set > 2 * PT_MIN_ROWS));
     a.tile = !pl.tc ? PA_TILE : rows_a_set > 64 ? 128 : rows_a_set > 32 ? 64 : 32;
-    a.slots = 0;
-    if (has_pre)
-        a.slots = (int)(a.gsize == 0 ? a.pre.n_set + all / a.tile
-                                     : a.pre.n_set * ((a.gsize * per + a.tile - 1) / a.tile));
+    a.slots = has_pre ? (int)slots(a.tile) : 0;
     a.own_tiles = (int)((per + PA_TILE - 1) / PA_TILE);
+    const auto ranges = [](const PaSet &s, int least) { return ((long long)s.max_keys + least - 1) / least; };
+    constexpr int STEP = PA_WARPS * PA_SLOT_KEYS;
     if (pl.tc)
-        split_keys(a.pre, (long long)a.slots * a.n_kv, PT_BLOCKS, PT_KEYS, PT_KEYS, PT_CLUSTER, PT_CLUSTER_KEYS);
+        split_keys(a.pre, (long long)a.slots * a.n_kv, PT_BLOCKS, PT_KEYS, a.pre.max_keys / PT_LEAST);
     else
-        split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, PA_WARPS * PA_SLOT_KEYS, PA_WARPS * PA_SLOT_KEYS, PA_CLUSTER,
-                   PA_CLUSTER_KEYS);
+        split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, STEP, ranges(a.pre, STEP));
     // own keys: one warp an item when that fills the device, more warps, then key ranges, when it does not
     const long long items = (long long)a.own.n_set * a.n_kv * a.own_tiles;
     a.own_wpi = PA_WARPS;
     while (a.own_wpi > 1 && (items * a.own_wpi > PA_BLOCKS * PA_WARPS || (a.own_wpi - 1) * PA_KEYS >= a.own.max_keys))
         a.own_wpi /= 2;
     split_keys(a.own, items, PA_BLOCKS * (PA_WARPS / a.own_wpi), a.own_wpi * PA_KEYS,
-               has_pre ? PA_OWN_LEAST : PA_WARPS * PA_SLOT_KEYS, PA_CLUSTER, PA_CLUSTER_KEYS);
+               ranges(a.own, has_pre ? PA_OWN_LEAST : STEP));
     a.own_items = items * a.own.splits;
     const bool one_launch = a.own_wpi == PA_WARPS && a.own.splits <= PA_CLUSTER && !has_pre;
     a.own_cluster = has_own && (a.own.splits == 1 || one_launch) ? a.own.splits : 0;
@@ -637,7 +683,9 @@ int launch(PaArgs &a, const PaPlan &pl, const PtMaps &maps, uint8_t *ws, cudaStr
             return rc;
     }
     if (pl.merge)
-        if (int rc = launch_ex(k_prefix_merge, dim3((unsigned)((rows + PM_ROWS - 1) / PM_ROWS)), 16 * PM_ROWS, 0, 1, true, s, a))
+        if (int rc = a.n_part <= 4 * PM_BATCH
+                         ? launch_ex(k_prefix_merge<2>, dim3((unsigned)((rows + PM_TEAMS / 2 - 1) / (PM_TEAMS / 2))), 16 * PM_TEAMS, 0, 1, true, s, a)
+                         : launch_ex(k_prefix_merge<PM_TEAMS>, dim3((unsigned)rows), 16 * PM_TEAMS, 0, 1, true, s, a))
             return rc;
     for (int own = 0; own < 2; ++own) {
         const PaSet &ks = own ? a.own : a.pre;
