@@ -5,6 +5,13 @@
 //   s_t = q . k_t / 8,   p = softmax(s),   o = sum_t p_t v_t,   weight[t] += sum over the queries of p_t
 // A prefix key and value are read once for all the queries of the group (all sequences, queries and
 // query heads of its key head are the rows of one matrix product), not once per sequence.
+//
+// k_prefix_attention  16 rows a block: prefixes of few rows, and every sequence's own keys; below
+// k_prefix_tc         32, 64 or 128 rows a block on tcgen05 (prefix_attention_tc.cu): prefixes of many rows
+// k_prefix_merge      joins key ranges where no cluster or own block does
+// k_prefix_weight     the keys' weights, where the scores were not kept
+// Floors: 256 bytes a key and head once, 4 * 64 flops a (query, key) pair.  The device's copy rate is 6.8 TB/s,
+// but one cold read of 153 MB by TMA, with no arithmetic, takes 26 us (5.9 TB/s): short passes pay for the start.
 #include "prefix_attention.cuh"
 
 namespace wh {
@@ -23,7 +30,8 @@ constexpr int PM_BATCH = 8;        // partial results that a merging thread load
 constexpr int PM_TEAMS = 8;        // teams of 16 threads in a merging block
 constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
 constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp step
-constexpr int PW_BLOCKS = 8 * 152; // weight kernel: blocks, some twice what is resident at once
+constexpr int PW_BLOCKS = 8 * 152; // weight kernel: blocks, twice what is resident (four an SM: 37.7 us, eight: 34.9)
+
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -86,6 +94,12 @@ __device__ __forceinline__ void score8(const uint32_t (&a)[4][4], const uint4 &k
 }
 
 // OWN = false: the prefixes; true: the sequences' own keys.
+// One pass over the keys with a running maximum and sum per row.  Bound by HBM: a warp keeps 4 to 8 KB of keys
+// and values in flight by cp.async (96 KB an SM with three blocks of four warps), and the products run on
+// mma.sync because 16 rows would leave 7/8 of a tcgen05 tile empty, while 606 TFLOP/s of mma.sync are four times
+// what 16 rows need at the full HBM rate.  Steps of 32 keys: the maximum's shuffles and the rescaling vote are
+// paid once for two products.  16 prefixes x 5 rows x 20 heads x 1500 keys: 23.5 us, 123 MB, 5.2 TB/s, 78 % of
+// the copy rate; 256 sequences' 448 own keys x 20 heads: 91 us, 587 MB, 95 %.
 template <bool OWN>
 __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -430,7 +444,9 @@ __global__ void __launch_bounds__(16 * PM_TEAMS) k_prefix_merge(const PaArgs p) 
 
 // weight[t] += sum over the set's queries of 2^(s_t - m) / l: the scores again, with every row's final
 // maximum and sum.  A warp takes 32 keys at a time from a ring of two such steps and goes through the rows
-// 16 at a time; each sum has one fixed order.  Bound by the keys' bytes for few rows.
+// 16 at a time; each sum has one fixed order.  Bound by the keys' bytes for few rows.  Reading the keys again
+// costs half of what the attention reads; keeping the scores would cost 8 bytes a (row, key) pair.  16 prefixes of
+// 211 .. 1500 keys, 83 rows, 20 heads: about 10 us for 34 MB of keys, most of them still in L2.
 __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p, int own) {
     __shared__ __align__(128) uint8_t rings[PW_WARPS][2 * PW_KEYS * 128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -601,6 +617,8 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     };
     const bool much = slots(PA_TILE) * a.n_kv * a.pre.max_keys >= PT_MIN_WORK;
     pl.tc = may_tc && rows_a_set > PT_MIN_ROWS && (much || (has_own && rows_a_set > 2 * PT_MIN_ROWS));
+    // the smallest tile that holds an average group (us a call with tiles of 32, 64, 128 rows, 4 prefixes of 1500
+    // keys: 20 rows 16.3, 16.4, 17.3; 40 rows 19.4, 18.4, 18.5; 100 rows 31.9, 22.6, 22.5)
     a.tile = !pl.tc ? PA_TILE : rows_a_set > 64 ? 128 : rows_a_set > 32 ? 64 : 32;
     a.slots = has_pre ? (int)slots(a.tile) : 0;
     a.own_tiles = (int)((per + PA_TILE - 1) / PA_TILE);
@@ -610,7 +628,9 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
         split_keys(a.pre, (long long)a.slots * a.n_kv, PT_BLOCKS, PT_KEYS, a.pre.max_keys / PT_LEAST);
     else
         split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, STEP, ranges(a.pre, STEP));
-    // own keys: one warp an item when that fills the device, more warps, then key ranges, when it does not
+    // own keys: one warp an item when that fills the device, more warps, then key ranges, when it does not (us a
+    // call with one, two, four warps: 16 sequences x 20 heads x 448 keys 17.3, 14.2, 12.3; 80 sequences 35.0,
+    // 35.0, 41.2; 256 sequences x 64 keys 24.6, -, 49.0)
     const long long items = (long long)a.own.n_set * a.n_kv * a.own_tiles;
     a.own_wpi = PA_WARPS;
     while (a.own_wpi > 1 && (items * a.own_wpi > PA_BLOCKS * PA_WARPS || (a.own_wpi - 1) * PA_KEYS >= a.own.max_keys))
