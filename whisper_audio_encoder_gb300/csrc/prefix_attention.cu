@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     const int cluster = OWN ? p.own_cluster : p.pre_cluster;
     const int wpi = OWN ? p.own_wpi : PA_WARPS, iw = warp & (wpi - 1);
     Rows rw;
-    int set, split, r0;
+    int set, split, r0, nk;
     if (OWN) {
         long long x = (long long)blockIdx.x * (PA_WARPS / wpi) + warp / wpi;
         if (x >= p.own_items) {
@@ -128,6 +128,9 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         rw.seq0 = set;
         rw.n = p.nq * p.rep;
         r0 = tile * PA_TILE;
+        const int count = ks.n_keys ? __ldg(ks.n_keys + set) : ks.max_keys;
+        nk = min(max(count, 0), ks.max_keys);
+        if (count != nk && rw.hk == 0 && split == 0 && r0 == 0 && iw == 0 && lane == 0) set_status(p.ctl, WH_EBOUNDS);
     } else {
         unsigned x = blockIdx.x;
         split = x % ks.splits;
@@ -135,11 +138,8 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         const int slot = x % p.slots;
         rw.hk = x / p.slots;
         if (cluster && split == 0) finish_outside(p, slot, rw.hk);
-        if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw)) return;
+        if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw, nk)) return;
     }
-    const int nk = clamp_count(ks, set);
-    if (ks.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && iw == 0 && lane == 0 && __ldg(ks.n_keys + set) != nk)
-        set_status(p.ctl, WH_EBOUNDS);
     const int k0 = split * ks.chunk, k1 = min(nk, k0 + ks.chunk);
     if (k0 >= k1 && !cluster) {   // nothing here: the merge knows
         if (OWN) pdl_wait();
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
             lim[half] = nk - (p.nq - 1 - qi);
         }
     }
+    const int before = OWN && cluster && p.after_pre ? pre_parts_of(p, group_of(p, set)) : 0;   // partial results
     const int full = OWN ? nk - (p.nq - 1) : nk;   // every row sees the keys before this one
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, o[8][4] = {};
@@ -308,11 +309,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     }
     auto item_bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpi), "r"(32 * wpi) : "memory"); };
     item_bar();
-    int before = 0;
-    if (OWN && p.after_pre) {
-        if (cluster) before = pre_parts_of(p, group_of(p, set));
-        pdl_wait();   // the prefix's partial results are complete
-    }
+    if (OWN && p.after_pre) pdl_wait();   // the prefix's partial results are complete
     __shared__ float2 fin[PA_WARPS][PA_TILE];   // the block's maximum and sum; own weights: the row's maximum, 1 / sum
     const int w0 = warp - iw, rows = min(PA_TILE, rw.n - r0);
     for (int i = 32 * iw + lane; i < 8 * rows; i += 32 * wpi) {

@@ -105,29 +105,46 @@ __device__ __forceinline__ int pre_parts_of(const PaArgs &p, int g) {
     return g < 0 ? 0 : (clamp_count(p.pre, g) + p.pre.chunk - 1) / p.pre.chunk;
 }
 
-// Prefix work of one block: its group, the rows r0 .. of that group's tile, false if the slot is empty.  With
-// group_start, group g's tiles take the slots from start[g] (nq rep) / tile + g on, which end before group
-// g + 1's, so no block needs to know the other groups' sizes.  One block per group reports a bad range.
-__device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report, int &set, int &r0, Rows &rw) {
-    const int per = p.nq * p.rep;
-    int s, e;
-    if (p.group_start) {
-        if (report && slot < p.pre.n_set && threadIdx.x == 0) {
-            const int a = __ldg(p.group_start + slot), b = __ldg(p.group_start + slot + 1);
-            if (a < 0 || b < a || b > p.batch) set_status(p.ctl, WH_EBOUNDS);
-        }
-        set = warp_search(p.group_start, p.pre.n_set, per, p.tile, 1, slot);
-        group_range(p, set, s, e);
-        r0 = (slot - (int)((long long)s * per / p.tile) - set) * p.tile;
+// Prefix work of one block: its group, the rows r0 .. of that group's tile, the group's key count (clamped), false
+// if the slot is empty.  With group_start, group g's tiles take the slots from start[g] (nq rep) / tile + g on,
+// which end before group g + 1's, so no block needs to know the other groups' sizes.  `report`: one block per
+// group reports a bad range or count.  Whole warps.
+__device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report, int &set, int &r0, Rows &rw, int &nk) {
+    const int per = p.nq * p.rep, lane = threadIdx.x & 31;
+    int s, e, count;
+    if (p.group_start && p.pre.n_set <= 32) {
+        // a lane a group: bounds and counts arrive together, after one load's latency
+        const int g = min(lane, p.pre.n_set - 1);
+        const int a = __ldg(p.group_start + g), b = __ldg(p.group_start + g + 1);
+        const int c = p.pre.n_keys ? __ldg(p.pre.n_keys + g) : p.pre.max_keys;
+        const bool le = lane < p.pre.n_set && (long long)a * per / p.tile + g <= slot;
+        set = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+        const bool bad = __any_sync(0xffffffffu, lane == slot && lane < p.pre.n_set && (a < 0 || b < a || b > p.batch));
+        if (report && bad && threadIdx.x == 0) set_status(p.ctl, WH_EBOUNDS);
+        s = min(max(__shfl_sync(0xffffffffu, a, set), 0), p.batch);
+        e = min(max(__shfl_sync(0xffffffffu, b, set), s), p.batch);
+        count = __shfl_sync(0xffffffffu, c, set);
     } else {
-        const int tiles = (p.gsize * per + p.tile - 1) / p.tile;
-        set = slot / tiles;
+        if (p.group_start) {
+            if (report && slot < p.pre.n_set && threadIdx.x == 0) {
+                const int a = __ldg(p.group_start + slot), b = __ldg(p.group_start + slot + 1);
+                if (a < 0 || b < a || b > p.batch) set_status(p.ctl, WH_EBOUNDS);
+            }
+            set = warp_search(p.group_start, p.pre.n_set, per, p.tile, 1, slot);
+        } else {
+            set = slot / ((p.gsize * per + p.tile - 1) / p.tile);
+        }
+        count = p.pre.n_keys ? __ldg(p.pre.n_keys + set) : p.pre.max_keys;
         group_range(p, set, s, e);
-        r0 = (slot - set * tiles) * p.tile;
     }
+    r0 = p.group_start ? (slot - (int)((long long)s * per / p.tile) - set) * p.tile
+                       : (slot - set * ((p.gsize * per + p.tile - 1) / p.tile)) * p.tile;
     rw.seq0 = s;
     rw.n = (e - s) * per;
-    return r0 >= 0 && r0 < rw.n;
+    nk = min(max(count, 0), p.pre.max_keys);
+    const bool there = r0 >= 0 && r0 < rw.n;
+    if (there && report && r0 == 0 && count != nk && threadIdx.x == 0) set_status(p.ctl, WH_EBOUNDS);
+    return there;
 }
 
 // Partial result `part` of row r of a block: dims d0 .. d0 + 7, relative to the maximum mt, with sum lt.

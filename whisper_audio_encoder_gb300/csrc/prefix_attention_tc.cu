@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
     pdl_wait();   // what runs after this kernel's trigger may count on its inputs
     pdl_launch_dependents();
     Rows rw;
-    int set, r0;
+    int set, r0, nk;
     // a cluster's blocks are the ranges of one item; else neighbours are tiles and heads, which read the same
     // rows or the same DRAM pages at about the same time
     const int cluster = p.pre_cluster;
@@ -85,10 +85,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
     const int slot = item % p.slots;
     rw.hk = item / p.slots;
     if (cluster && split == 0) finish_outside(p, slot, rw.hk);
-    if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw)) return;
-    const int nk = clamp_count(p.pre, set);
-    if (p.pre.n_keys && rw.hk == 0 && split == 0 && r0 == 0 && threadIdx.x == 0 && __ldg(p.pre.n_keys + set) != nk)
-        set_status(p.ctl, WH_EBOUNDS);
+    if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw, nk)) return;
     const int k0 = split * p.pre.chunk, k1 = min(nk, k0 + p.pre.chunk);
     const int a = threadIdx.x - 128;   // the rows' threads: TMEM lane and matrix row
     float *so = reinterpret_cast<float *>(sKV);   // the epilogue's rows, then their maxima and sums
