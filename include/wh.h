@@ -303,6 +303,7 @@ int wh_decode_attention(const wh_bf16 *q, const wh_bf16 *k, const wh_bf16 *v, in
  *           clamped and recorded as WH_EBOUNDS, which wh_status() then returns.
  *   weight  device float32 [n_set][n_kv_head][max_keys], or NULL: accumulators of the attention
  *           weight that every key received.
+ * All max_keys rows of a set must be memory of the device: those past its count may be read too.
  *
  * wh_prefix_attention: each of batch sequences has n_query queries (its last n_query tokens; 1 in
  * an ordinary decode step), query row b * n_query + i, head h at q + row * q_stride + 64 h.  Query
@@ -364,7 +365,7 @@ int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch, int n_que
  *   n_out   device int32 [n_set]: the new counts, min(n, budget); may be cache->n_keys
  *   kept    device int32 [n_set][n_kv_head][budget] or NULL: the former index of every key that
  *           stays; entries past the new count are left as they were
- *   0 <= recent <= budget, 1 <= budget <= 2^30; within a wh_keys no two sets and no keys and values
+ *   1 <= n_set <= 65535, 0 <= recent <= budget, 1 <= budget <= 2^30; within a wh_keys no two sets and no keys and values
  *   may overlap (sets one after the other or side by side in a row; [K | V] rows are fine).
  *   workspace >= wh_cache_evict_workspace(n_set, n_kv_head, cache->max_keys, budget) bytes, 256-byte
  *           aligned, contents need not be initialised; not shared by concurrent calls.  May be NULL

@@ -77,3 +77,19 @@ def test_layouts_that_are_fine(L):
         assert _call(L, keys) == wh.WH_ENODEV
     assert _call(L, _keys(), out=_keys(at=far, max_keys=40)) == wh.WH_ENODEV
     assert _call(L, _keys(max_keys=30), budget=40, out=_keys(at=far, max_keys=30)) == wh.WH_ENODEV
+
+
+def test_interleaved_layouts_by_their_rows(L):
+    """Sets beside each other in rows, keys and values in the same rows: only what overlaps is refused."""
+    W = 2 * 128                                                # bytes of a row of a set (two heads)
+    beside = dict(n_set=2, row_stride=640, max_keys=100)
+    assert _call(L, _keys(v=P + W, set_stride=128, **beside)) == wh.WH_EINVAL          # set 1's keys are set 0's values
+    assert _call(L, _keys(v=P + 2 * W + 16, set_stride=256, **beside)) == wh.WH_EINVAL  # a part of them
+    assert _call(L, _keys(v=P + 4 * W, set_stride=128, n_set=2, row_stride=512)) == wh.WH_EINVAL   # the next row's keys
+    # sets half a row out of step: the last value row of set 0, 99 rows and a half on, is set 1's first key row
+    assert _call(L, _keys(v=P + W, n_set=2, row_stride=256, set_stride=99 * 256 + 128)) == wh.WH_EINVAL
+    if not torch.cuda.is_available():
+        assert _call(L, _keys(v=P + W, set_stride=256, **beside)) == wh.WH_ENODEV       # K0 V0 K1 V1
+        assert _call(L, _keys(v=P + 2 * W, set_stride=128, **beside)) == wh.WH_ENODEV   # K0 K1 V0 V1
+        assert _call(L, _keys(v=P - W, k=P, n_set=2, row_stride=512, set_stride=256)) == wh.WH_ENODEV   # V0 K0 V1 K1
+        assert _call(L, _keys(v=P + W, n_set=2, row_stride=256, set_stride=100 * 256 + 128)) == wh.WH_ENODEV

@@ -268,3 +268,29 @@ def test_refusals_of_the_binding():
         with pytest.raises(wh.WhError):
             wh.wh_cache_evict(**args)
     assert same(c.store, before) and wh.wh_status() == wh.WH_OK
+
+
+def test_numbers_past_the_library_s_types_are_refused():
+    """A count that a 32-bit argument would silently cut."""
+    c = Case(heads=2, cap=10, counts=[10], budget=4, recent=1)
+    cache = wh.Keys(c.k, c.v, c.n, c.w)
+    before = c.store.clone()
+    for kw in (dict(budget=(1 << 32) + 4), dict(recent=1 << 32), dict(n_kv_head=2 - (1 << 32)), dict(recent=-1)):
+        with pytest.raises(wh.WhError):
+            wh.wh_cache_evict(**{**dict(cache=cache, n_kv_head=2, budget=4, recent=1), **kw})
+    q = torch.zeros(1, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(wh.WhError):
+        wh.wh_prefix_attention(q, 2, prefix=wh.Keys(c.k, c.v), n_kv_head=2 - (1 << 32))
+    assert same(c.store, before) and wh.wh_status() == wh.WH_OK
+
+
+def test_no_sets_and_single_rows_of_odd_width():
+    e = torch.zeros(0, 9, 128, dtype=torch.bfloat16, device="cuda")
+    none = wh.Keys(e, e.clone(), None, torch.zeros(0, 2, 9, device="cuda"))
+    assert wh.wh_cache_evict(none, 2, 4, 1).shape == (0,)
+    # one key of a row of 131 values: the stride of a dimension of size one is not used
+    k, v = (torch.randn(1, 1, 131, device="cuda").bfloat16() for _ in range(2))
+    w = torch.ones(1, 2, 1, device="cuda")
+    assert wh.wh_cache_evict(wh.Keys(k, v, None, w), 2, 1, 0).tolist() == [1]
+    out = wh.wh_prefix_attention(torch.zeros(1, 128, dtype=torch.bfloat16, device="cuda"), 2, own=wh.Keys(k, v, None, w))
+    assert torch.equal(out, v[:, 0, :128]) and w.tolist() == [[[2.0], [2.0]]] and wh.wh_status() == wh.WH_OK

@@ -15,6 +15,8 @@
 //   k_evict_small   up to 2048 keys: a block chooses and moves one head of one set
 //   k_evict_select, then k_evict_move (other buffers: rows spread over the device) or k_evict_shift (within
 //   the cache: a block per head and keys or values), for long caches and where few heads move many rows
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -533,18 +535,31 @@ size_t up256e(size_t x) { return (x + 255) & ~(size_t)255; }
 
 bool fits(const void *p, size_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether no row of one set's keys (row t at t * row) meets a row of another's (at d + t * row).
+bool rows_apart(int64_t d, int64_t row, int64_t width, int64_t span) {
+    const int64_t at = (d % row + row) % row;
+    return d >= span || d <= -span || (at >= width && at <= row - width);
+}
+
 // What a caller may pass as the cache or as where it goes: no two sets, and no key and value, share memory.
 bool keys_ok(const wh_keys *s, int n_kv) {
     if (!s || s->n_set < 1 || s->n_set > 65535 || s->max_keys < 1 || s->max_keys > (1 << 30)) return false;
-    const int64_t row = s->row_stride, width = 64LL * n_kv;
-    if (row < width || row % 8 != 0 || s->set_stride < 0 || s->set_stride % 8 != 0) return false;
-    const bool apart = s->set_stride >= (s->max_keys - 1) * row + width;                            // [set][key]
-    const bool beside = s->set_stride >= width && (s->n_set - 1) * s->set_stride + width <= row;    // [key][set]
-    if (s->n_set > 1 && !apart && !beside) return false;
+    const int64_t row = s->row_stride, set = s->set_stride, width = 64LL * n_kv;
+    if (row < width || row % 8 != 0 || set < 0 || set % 8 != 0) return false;
     if (!fits(s->k, 16) || !fits(s->v, 16) || !fits(s->weight, 4) || (s->n_keys && !fits(s->n_keys, 4))) return false;
-    const int64_t end = (s->n_set - 1) * s->set_stride + (s->max_keys - 1) * row + width;
-    const int64_t gap = s->v > s->k ? s->v - s->k : s->k - s->v;
-    return gap >= end || (gap % row >= width && gap % row <= row - width);                          // [K | V] rows
+    const int64_t span = (s->max_keys - 1) * row + width, last = s->n_set - 1;
+    if (last > 0 && set == 0) return false;
+    for (int64_t i = 1; i <= last && i * set < span; ++i)   // (sets one after the other: none to look at)
+        if (!rows_apart(i * set, row, width, span)) return false;
+    const int64_t gap = s->v - s->k;
+    int64_t from = -last, to = last;   // value sets against a key set, by how many sets they are on
+    if (last > 0) {
+        from = std::max(from, (-span - gap) / set - 1);
+        to = std::min(to, (span - gap) / set + 1);
+    }
+    for (int64_t i = from; i <= to; ++i)
+        if (!rows_apart(gap + i * set, row, width, span)) return false;
+    return true;
 }
 
 struct Span {

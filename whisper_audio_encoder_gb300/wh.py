@@ -309,11 +309,11 @@ class Keys:
         self.k, self.v, self.n_keys, self.weight, self.device = k, v, n_keys, weight, dev
         self.n_set, self.max_keys, self.width = n_set, max_keys, d
         # (the stride of a dimension of size one is never used)
-        self.c = wh_keys(k.data_ptr(), v.data_ptr(), stride[1] if max_keys > 1 else d, stride[0] if n_set > 1 else 0,
+        self.c = wh_keys(k.data_ptr(), v.data_ptr(), stride[1] if max_keys > 1 else d & ~7, stride[0] if n_set > 1 else 0,
                          counts, accumulators, n_set, max_keys)
 
     def _check(self, n_kv_head, device, what):
-        _need(self.width >= 64 * n_kv_head, f"{what}: rows shorter than 64 n_kv_head")
+        _need(n_kv_head >= 1 and self.width >= 64 * n_kv_head, f"{what}: rows shorter than 64 n_kv_head")
         _need(self.weight is None or self.weight_heads == n_kv_head, f"{what}: weight [n_set][n_kv_head][max_keys]")
         _need(self.device == device, f"{what}: tensors on different devices")
 
@@ -415,13 +415,15 @@ def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, worksp
     cache._check(n_kv_head, dev, what)
     to._check(n_kv_head, dev, what)
     _need(cache.weight is not None and to.weight is not None, "wh_cache_evict: Keys without weight")
-    _need(budget >= 1, "wh_cache_evict: budget >= 1")
+    _need(0 <= recent <= budget and 1 <= budget <= 1 << 30, "wh_cache_evict: 0 <= recent <= budget, 1 <= budget <= 2^30")
     indices = None
     if kept is not None:
         _need(kept.dtype == torch.int32 and kept.shape == (n_set, n_kv_head, budget) and kept.is_contiguous() and
               kept.get_device() == dev, "wh_cache_evict: kept int32 [n_set][n_kv_head][budget]")
         indices = kept.data_ptr()
     n_out = to.n_keys if to.n_keys is not None else torch.empty(n_set, dtype=torch.int32, device=cache.k.device)
+    if n_set == 0 and to.n_set == 0:
+        return n_out
     s = _stream_handle(dev, stream)
     if workspace is None:
         need = _workspace_bytes("wh_cache_evict_workspace", n_set, n_kv_head, cache.max_keys, budget)
