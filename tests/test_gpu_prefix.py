@@ -135,6 +135,9 @@ CASES = {
     "long prefix and own keys": dict(n_head=1, n_kv=1, nq=1, groups=[3], n_pre=[30000], n_own=[900, 0, 4000], weigh=True),
     "long prefix of many rows and own keys": dict(n_head=1, n_kv=1, nq=1, groups=[20], n_pre=[40000], n_own=[9 * i for i in range(20)], weigh=True),
     "many queries": dict(n_head=2, n_kv=1, nq=41, groups=[1, 2], n_pre=[50, 77], n_own=[41, 43, 100], weigh=True),
+    "two ranges a cluster, the second often empty": dict(
+        n_head=6, n_kv=6, nq=1, groups=[24, 20, 0, 31, 24, 24, 24, 24, 24, 24, 24, 45],
+        n_pre=[1700, 0, 1699, 5, 895, 896, 897, 1024, 1, 128, 900, 640], weigh=True),
     "wide group": dict(n_head=2, n_kv=1, nq=1, groups=[201], n_pre=[333], n_own=[i % 7 for i in range(201)], weigh=True),
 }
 

@@ -101,6 +101,9 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
     float2 *sml = reinterpret_cast<float2 *>(sKV + 128 * SO_ROW * 4);
     const int rows = min(TILE, rw.n - r0);
     if (k0 >= k1) {                   // no keys here
+        // An SM takes no second block before the first has given up its right to allocate TMEM, and this one may
+        // stay for its cluster: 24 sets of 300 .. 1500 keys x 80 rows x 6 heads 18.7 us, 28.3 without this.
+        if (warp == 1) tmem_relinquish();
         if (cluster) {
             for (int i = threadIdx.x; i < rows * SO_ROW; i += PT_THREADS) so[i] = 0.0f;
             for (int i = threadIdx.x; i < rows; i += PT_THREADS) sml[i] = make_float2(-INFINITY, 0.0f);
@@ -149,6 +152,8 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
         for (int j = 0; j < nt && j < PT_STAGES; ++j) load_step(j);
     }
     if (warp == 1) {
+        // (not first of all: an SM's second block starts after this, and two that start together, both loading,
+        // then both computing, take longer: 35.4 us against 33.3 at 32 rows x 20 heads x 30000 keys)
         tmem_alloc(tmem_slot, PT_COLS);
         tmem_relinquish();
     }
