@@ -133,9 +133,9 @@ struct Team {
         const int tx = __reduce_add_sync(0xffffffffu, vx), ty = __reduce_add_sync(0xffffffffu, vy);
         __syncthreads();
         if (CTAS > 1) {
-            const int gx = gather(tx), gy = gather(ty);
-            bx += __reduce_add_sync(0xffffffffu, lane < rank() ? gx : 0);
-            by += __reduce_add_sync(0xffffffffu, lane < rank() ? gy : 0);
+            const int both = gather(tx | ty << 16);   // (a block holds fewer than 65536 in all)
+            bx += __reduce_add_sync(0xffffffffu, lane < rank() ? both & 0xffff : 0);
+            by += __reduce_add_sync(0xffffffffu, lane < rank() ? (int)((uint32_t)both >> 16) : 0);
         }
     }
 };
@@ -230,8 +230,8 @@ __device__ __forceinline__ void find_threshold_radix(T &team, int need, const ui
     ties = need;
 }
 
-// The weights of the keys that stay, to wo (which may be w): a step's reads are before its writes, and a
-// key's place is never behind it.
+// The weights of the keys that stay, to wo (which may be w: then a step's reads are before its writes, and a
+// key's place is never behind it).
 template <class T>
 __device__ __forceinline__ void move_weights(T &team, const float *w, const int *src, int rows, float *wo) {
     const int tid = team.thread();
@@ -240,7 +240,7 @@ __device__ __forceinline__ void move_weights(T &team, const float *w, const int 
         float x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) x[u] = base + u * T::ALL + tid < rows ? w[src[base + u * T::ALL + tid]] : 0.0f;
-        team.sync();
+        if (wo == w) team.sync();
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (base + u * T::ALL + tid < rows) wo[base + u * T::ALL + tid] = x[u];
