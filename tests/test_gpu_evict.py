@@ -127,6 +127,22 @@ def test_lengths(n):
     Case(heads=2, cap=n, counts=[n, n // 2], budget=max(1, n // 3), recent=min(5, max(1, n // 3)), seed=n).check(n % 2 == 0)
 
 
+@pytest.mark.parametrize("in_place", [False, True], ids=["out", "in_place"])
+def test_weights_of_any_size(in_place):
+    """Long caches, whose threshold is looked for by ranges of sizes: a set each of small, large, negative and mixed
+    weights, of weights next to the powers of two and of two values only."""
+    cap = 9000
+    c = Case(heads=2, cap=cap, counts=[cap] * 8 + [8999], budget=4000, recent=10)
+    rng = np.random.default_rng(3)
+    for i, f in enumerate((1e-30, 2.0 ** -25, 8.0, 1e30, -1.0)):
+        c.w[i] *= f
+    powers = np.float32(2.0) ** rng.integers(-30, 8, (2, cap)).astype(np.float32)
+    c.w[5] = torch.from_numpy(np.nextafter(powers, powers * rng.choice([0.0, 1.0, 2.0], (2, cap)).astype(np.float32)))
+    c.w[6] = torch.from_numpy(rng.choice(np.float32([2.0 ** -25, 8.0]), (2, cap)))
+    c.w[7] = torch.from_numpy(np.where(rng.random((2, cap)) < 0.44, np.float32(8.0), np.float32(2.0 ** -26)))
+    c.check(in_place)
+
+
 def test_into_a_larger_cache_on_another_stream_without_indices():
     torch.cuda.synchronize()
     s = torch.cuda.Stream()

@@ -163,20 +163,28 @@ __device__ __forceinline__ void find_threshold(int need, uint32_t most, uint32_t
 
 // The same for a cluster, four bits at a time: every thread counts its images under the decided bits in 16 bins of
 // 8 bits, the warps, blocks and the cluster add them in bins of 16 (fewer than 65536 images in all).  A step
-// costs little more than one bit's count would, most of it the cluster barrier.
+// costs little more than one bit's count would, most of it the cluster barrier.  The first step guesses that the
+// threshold lies in 2^-25 .. 8, where weights mostly do, and then knows eight bits of it; else the steps begin anew.
 template <int E, class T>
 __device__ __forceinline__ void find_threshold_radix(T &team, int need, const uint32_t (&key)[E], uint32_t &W, int &ties) {
     static_assert(E < 256 && T::WARPS == 8 && T::BLOCKS == 8, "the bins' widths, the lanes' shares");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, word = lane & 7, part = lane >> 3;
+    constexpr int GUESS = 0xb2;   // images' first byte: 0xb3 .. 0xc0 (2^-25 .. 8) get bins 1 .. 14, the rest bins 0 and 15
     uint32_t prefix = 0;
-    for (int shift = 28, turn = 0; shift >= 0; shift -= 4, turn ^= 1) {
+    bool guess = true;
+    for (int shift = 24, turn = 0; shift >= 0; turn ^= 1) {
         unsigned long long c[2] = {0, 0};
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const uint32_t x = (key[j] ^ prefix) >> shift;   // below 16: the decided bits agree, these are the next
+        const auto count = [&](uint32_t x) {
             const unsigned long long one = x < 16u ? 1ull << (8 * (x & 7u)) : 0ull;
             c[0] += x & 8u ? 0ull : one;
             c[1] += x & 8u ? one : 0ull;
+        };
+        if (guess) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) count((uint32_t)min(max((int)(key[j] >> 24) - GUESS, 0), 15));
+        } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j) count((key[j] ^ prefix) >> shift);   // below 16: the decided bits agree, these are the next
         }
         // bins 4i and 4i + 2 in word 2i, 4i + 1 and 4i + 3 in word 2i + 1
         uint32_t *mine = team.bins + turn * 64;
@@ -207,8 +215,8 @@ __device__ __forceinline__ void find_threshold_radix(T &team, int need, const ui
         v += __shfl_xor_sync(0xffffffffu, v, 16);
         // lane b: bin b's count, then how many images lie in bins b .. 15
         const int b = lane & 15;
-        const int count = (int)((__shfl_sync(0xffffffffu, v, 2 * (b >> 2) + (b & 1)) >> (16 * ((b >> 1) & 1))) & 0xffffu);
-        int upward = count;
+        const int held = (int)((__shfl_sync(0xffffffffu, v, 2 * (b >> 2) + (b & 1)) >> (16 * ((b >> 1) & 1))) & 0xffffu);
+        int upward = held;
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) {
             const int up = __shfl_down_sync(0xffffffffu, upward, o, 16);
@@ -216,9 +224,19 @@ __device__ __forceinline__ void find_threshold_radix(T &team, int need, const ui
         }
         const uint32_t reach = __ballot_sync(0xffffffffu, upward >= need) & 0xffffu;
         const int digit = 31 - __clz(reach | 1u);
-        const int in_bin = __shfl_sync(0xffffffffu, count, digit);
+        const int in_bin = __shfl_sync(0xffffffffu, held, digit);
         const int above = __shfl_sync(0xffffffffu, upward, digit) - in_bin;
-        prefix |= (uint32_t)digit << shift;
+        if (guess) {
+            guess = false;
+            if (digit == 0 || digit == 15) {   // somewhere else
+                shift = 28;
+                continue;
+            }
+            prefix = (uint32_t)(GUESS + digit) << 24;
+        } else {
+            prefix |= (uint32_t)digit << shift;
+        }
+        shift -= 4;
         need -= above;
         if (in_bin == need && prefix != 0) {   // all of them stay: the next smaller image is below prefix
             W = prefix - 1;
