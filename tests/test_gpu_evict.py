@@ -134,13 +134,22 @@ def test_weights_of_any_size(in_place):
     cap = 9000
     c = Case(heads=2, cap=cap, counts=[cap] * 8 + [8999], budget=4000, recent=10)
     rng = np.random.default_rng(3)
-    for i, f in enumerate((1e-30, 2.0 ** -25, 8.0, 1e30, -1.0)):
+    for i, f in enumerate((1e-30, 2.0 ** -19, 512.0, 1e30, -1.0)):
         c.w[i] *= f
-    powers = np.float32(2.0) ** rng.integers(-30, 8, (2, cap)).astype(np.float32)
+    powers = np.float32(2.0) ** rng.integers(-24, 13, (2, cap)).astype(np.float32)
     c.w[5] = torch.from_numpy(np.nextafter(powers, powers * rng.choice([0.0, 1.0, 2.0], (2, cap)).astype(np.float32)))
-    c.w[6] = torch.from_numpy(rng.choice(np.float32([2.0 ** -25, 8.0]), (2, cap)))
-    c.w[7] = torch.from_numpy(np.where(rng.random((2, cap)) < 0.44, np.float32(8.0), np.float32(2.0 ** -26)))
+    c.w[6] = torch.from_numpy(rng.choice(np.float32([2.0 ** -19, 512.0]), (2, cap)))
+    c.w[7] = torch.from_numpy(np.where(rng.random((2, cap)) < 0.44, np.float32(512.0), np.float32(2.0 ** -20)))
     c.check(in_place)
+
+
+@pytest.mark.parametrize("kept", [1, 2, 65534])
+@pytest.mark.parametrize("value", [0.0, float("nan"), -1.0, 1.0])
+def test_as_many_equal_weights_as_a_cluster_counts(value, kept):
+    """65535 keys of one weight: their number is the largest that the choice's counters hold."""
+    c = Case(heads=1, cap=65535, counts=[65535], budget=kept, recent=0)
+    c.w.fill_(value)
+    c.check(False)
 
 
 def test_into_a_larger_cache_on_another_stream_without_indices():

@@ -162,14 +162,15 @@ __device__ __forceinline__ void find_threshold(int need, uint32_t most, uint32_t
 }
 
 // The same for a cluster, four bits at a time: every thread counts its images under the decided bits in 16 bins of
-// 8 bits, the warps, blocks and the cluster add them in bins of 16 (fewer than 65536 images in all).  A step
+// 8 bits, the warps, blocks and the cluster add them in bins of 16 (fewer than 65536 older keys: the `pads` zero images
+// of a thread that stand for none are not counted).  A step
 // costs little more than one bit's count would, most of it the cluster barrier.  The first step guesses that the
-// threshold lies in 2^-25 .. 8, where weights mostly do, and then knows eight bits of it; else the steps begin anew.
+// threshold lies in 2^-19 .. 512, where weights of long caches mostly do, and then knows eight bits of it; else the steps begin anew.
 template <int E, class T>
-__device__ __forceinline__ void find_threshold_radix(T &team, int need, const uint32_t (&key)[E], uint32_t &W, int &ties) {
+__device__ __forceinline__ void find_threshold_radix(T &team, int need, const uint32_t (&key)[E], int pads, uint32_t &W, int &ties) {
     static_assert(E < 256 && T::WARPS == 8 && T::BLOCKS == 8, "the bins' widths, the lanes' shares");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, word = lane & 7, part = lane >> 3;
-    constexpr int GUESS = 0xb2;   // images' first byte: 0xb3 .. 0xc0 (2^-25 .. 8) get bins 1 .. 14, the rest bins 0 and 15
+    constexpr int GUESS = 0xb5;   // images' first byte: 0xb6 .. 0xc3 (2^-19 .. 512) get bins 1 .. 14, the rest bins 0 and 15
     uint32_t prefix = 0;
     bool guess = true;
     for (int shift = 24, turn = 0; shift >= 0; turn ^= 1) {
@@ -186,6 +187,7 @@ __device__ __forceinline__ void find_threshold_radix(T &team, int need, const ui
 #pragma unroll
             for (int j = 0; j < E; ++j) count((key[j] ^ prefix) >> shift);   // below 16: the decided bits agree, these are the next
         }
+        if (prefix == 0) c[0] -= pads;   // they are in bin 0 as long as nothing is decided
         // bins 4i and 4i + 2 in word 2i, 4i + 1 and 4i + 3 in word 2i + 1
         uint32_t *mine = team.bins + turn * 64;
 #pragma unroll
@@ -288,7 +290,8 @@ __device__ __forceinline__ void choose(T &team, const float *w, int n, int budge
     uint32_t W = 0xffffffffu;
     int ties = 0;
     if constexpr (T::BLOCKS > 1) {
-        if (need > 0) find_threshold_radix<E>(team, need, key, W, ties);
+        const int held = (old - first + 31) / 32;   // this thread's older keys
+        if (need > 0) find_threshold_radix<E>(team, need, key, E - min(max(held, 0), E), W, ties);
     } else if (need > 0) {
         hi = team.largest(hi);
         lo = ~team.largest(lo);
