@@ -275,10 +275,13 @@ __device__ __forceinline__ void choose(T &team, const float *w, int n, int budge
                                        float *wo) {
     const int lane = threadIdx.x & 31, first = (team.thread() >> 5) * 32 * E + lane;
     const int old = n - recent, need = budget - recent;   // 0 <= need < old
+    // Up to 16 a thread: the weights stay in registers too and go to another buffer from there (20 heads x 9000 keys
+    // 21.1 us, 20.1 so; 60 heads with 32 a thread 38.3, 40.4 so).
+    constexpr bool DIRECT = E <= 16;
     uint32_t key[E];   // past the older keys: 0, which no candidate reaches
     float raw[E];
 #pragma unroll
-    for (int j = 0; j < E; ++j) raw[j] = first + 32 * j < old ? w[first + 32 * j] : 0.0f;
+    for (int j = 0; j < E; ++j) raw[j] = first + 32 * j < (DIRECT ? n : old) ? w[first + 32 * j] : 0.0f;
     uint32_t hi = 0, lo = 0;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
@@ -341,8 +344,10 @@ __device__ __forceinline__ void choose(T &team, const float *w, int n, int budge
         if (stays) {
             src[at] = i;
             if (kept) kept[at] = i;
+            if (DIRECT && wo != w) wo[at] = raw[j];
         }
     }
+    if (DIRECT && wo != w) return;
     team.sync();
     move_weights(team, w, src, budget, wo);
 }
