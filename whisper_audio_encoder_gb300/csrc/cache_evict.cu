@@ -35,10 +35,11 @@ constexpr int SM_ROWS = 1024;
 constexpr int SM_HEADS = 4 * 152;
 constexpr int SEL_THREADS = 1024;    // k_evict_select, one block a head
 constexpr int SEL_HELD = 32;         // keys that a thread of it holds: longer caches are read again for every bit
-// Clusters of SEL_CTAS blocks of 256 threads choose instead for few heads of long caches, and for the longest:
-// 20 heads x 9000 keys 26.0 us, 31.4 with a block each; 60 heads 47.3 and 42.2; 20 x 60000 43.8 and 155.
+// Clusters of SEL_CTAS blocks of 256 threads choose instead for as many heads of long caches as are resident at
+// once, and for the longest: 60 heads x 9000 keys 35.0 us, 38.3 with a block each; 80 heads 42.5 and 41.1; 60 x 30000
+// 46.0 and 50.5; 20 x 60000 36.6 and 155.
 constexpr int SEL_CTAS = 8;
-constexpr int SEL_SPREAD = 40;
+constexpr int SEL_SPREAD = 72;
 constexpr int MV_THREADS = 256;
 constexpr int MV_PIECES = 1024;      // 16-byte pieces (of keys, and of values) of a block of k_evict_move
 constexpr int SH_THREADS = 512;      // k_evict_shift
@@ -452,8 +453,10 @@ __global__ void __launch_bounds__(SM_THREADS) k_evict_small(const EvArgs p) {
 }
 
 // Chooses only: a warp (of four), a block or a cluster of CTAS blocks per head and set.
+// (64 registers for the blocks of a cluster with 16 weights a thread: 72 clusters at once instead of 36; 40 heads x
+// 9000 keys 31.2 us -> 27.5)
 template <int CHOOSERS, int E, int CTAS = 1>
-__global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS) k_evict_select(const EvArgs p) {
+__global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS, CTAS > 1 && E == 16 ? 4 : 1) k_evict_select(const EvArgs p) {
     __shared__ int buf[2 * SEL_THREADS / 32], peers[2 * CTAS];
     __shared__ uint32_t bins[CTAS > 1 ? 256 : 1];
     pdl_wait();
