@@ -272,11 +272,21 @@ def wh_decode_attention(q, k, v, row_stride, seq_stride, max_keys, n_head, n_key
     return out
 
 
-def _need(ok, what):
-    if not ok:
-        raise WhError(WH_EINVAL, what)
+_torch = None
 
 
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+
+
+def _refuse(what):
+    raise WhError(WH_EINVAL, what)
+
+
+# (The calls below are short on the GPU, so their checks are written for the host's time: no call, format or import
+# before something is found wrong.)
 class Keys:
     """The keys and values of n_set sets (the C struct wh_keys) as views of torch tensors.
 
@@ -288,23 +298,27 @@ class Keys:
     __slots__ = ("k", "v", "n_keys", "weight", "device", "n_set", "max_keys", "width", "weight_heads", "c")
 
     def __init__(self, k, v, n_keys=None, weight=None):
-        import torch
-        shape, stride, dev = k.shape, k.stride(), k.get_device()
-        _need(len(shape) == 3 and v.shape == shape and v.stride() == stride and stride[2] == 1 and
-              k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16, "Keys: k, v bf16 [n_set][max_keys][d], equal strides")
+        if _torch is None:
+            _load_torch()
+        shape, stride, dev, bf16 = k.shape, k.stride(), k.get_device(), _torch.bfloat16
+        if not (len(shape) == 3 and v.shape == shape and v.stride() == stride and stride[2] == 1 and k.dtype is bf16 and
+                v.dtype is bf16):
+            _refuse("Keys: k, v bf16 [n_set][max_keys][d], equal strides")
+        if dev < 0 or v.get_device() != dev:
+            _refuse("Keys: k and v must be on one CUDA device")
         n_set, max_keys, d = shape
-        _need(dev >= 0 and v.get_device() == dev, "Keys: k and v must be on one CUDA device")
         counts = accumulators = None
         self.weight_heads = 0
         if n_keys is not None:
-            _need(n_keys.dtype == torch.int32 and n_keys.shape == (n_set,) and n_keys.is_contiguous() and
-                  n_keys.get_device() == dev, "Keys: n_keys int32 [n_set]")
+            if not (n_keys.dtype is _torch.int32 and n_keys.shape == (n_set,) and n_keys.is_contiguous() and
+                    n_keys.get_device() == dev):
+                _refuse("Keys: n_keys int32 [n_set]")
             counts = n_keys.data_ptr()
         if weight is not None:
             ws = weight.shape
-            _need(weight.dtype == torch.float32 and len(ws) == 3 and ws[0] == n_set and ws[2] == max_keys and
-                  weight.is_contiguous() and weight.get_device() == dev,
-                  "Keys: weight float32 [n_set][n_kv_head][max_keys]")
+            if not (weight.dtype is _torch.float32 and len(ws) == 3 and ws[0] == n_set and ws[2] == max_keys and
+                    weight.is_contiguous() and weight.get_device() == dev):
+                _refuse("Keys: weight float32 [n_set][n_kv_head][max_keys]")
             self.weight_heads, accumulators = ws[1], weight.data_ptr()
         self.k, self.v, self.n_keys, self.weight, self.device = k, v, n_keys, weight, dev
         self.n_set, self.max_keys, self.width = n_set, max_keys, d
@@ -313,17 +327,20 @@ class Keys:
                          counts, accumulators, n_set, max_keys)
 
     def _check(self, n_kv_head, device, what):
-        _need(n_kv_head >= 1 and self.width >= 64 * n_kv_head, f"{what}: rows shorter than 64 n_kv_head")
-        _need(self.weight is None or self.weight_heads == n_kv_head, f"{what}: weight [n_set][n_kv_head][max_keys]")
-        _need(self.device == device, f"{what}: tensors on different devices")
+        if not (n_kv_head >= 1 and self.width >= 64 * n_kv_head):
+            _refuse(f"{what}: rows shorter than 64 n_kv_head")
+        if self.weight is not None and self.weight_heads != n_kv_head:
+            _refuse(f"{what}: weight [n_set][n_kv_head][max_keys]")
+        if self.device != device:
+            _refuse(f"{what}: tensors on different devices")
 
 
 def _stream_handle(dev, stream):
     """The handle of `stream`, or of device dev's current stream.  dev must be the current device: the
     library launches there."""
-    import torch
-    _need(torch._C._cuda_getDevice() == dev, "the tensors' device is not the current one (torch.cuda.set_device)")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if _torch._C._cuda_getDevice() != dev:
+        _refuse("the tensors' device is not the current one (torch.cuda.set_device)")
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 @functools.lru_cache(maxsize=4096)
@@ -338,13 +355,11 @@ class _Scratch:
     __slots__ = ("ptr",)
 
     def __init__(self, need, stream):
-        import torch
-        self.ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream) if need else None
+        self.ptr = _torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream) if need else None
 
     def __del__(self):
         if self.ptr:
-            import torch
-            torch._C._cuda_cudaCachingAllocator_raw_delete(self.ptr)
+            _torch._C._cuda_cudaCachingAllocator_raw_delete(self.ptr)
 
 
 def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_start=None, n_query=1, out=None,
@@ -354,12 +369,13 @@ def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_
     group_start: int32 device [prefix sets + 1] or None (equal groups in order).  Adds the attention
     weight of every key to prefix.weight / own.weight where given.  Returns bf16
     [batch * n_query][64 n_head]."""
-    import torch
+    if _torch is None:
+        _load_torch()
     what = "wh_prefix_attention"
     shape, stride, dev = q.shape, q.stride(), q.get_device()
-    _need(len(shape) == 2 and q.dtype == torch.bfloat16 and dev >= 0 and stride[1] == 1 and n_head >= 1 and
-          shape[1] >= 64 * n_head and n_query >= 1 and shape[0] % n_query == 0,
-          "wh_prefix_attention: q bf16 [batch * n_query][64 n_head]")
+    if not (len(shape) == 2 and q.dtype is _torch.bfloat16 and dev >= 0 and stride[1] == 1 and n_head >= 1 and
+            shape[1] >= 64 * n_head and n_query >= 1 and shape[0] % n_query == 0):
+        _refuse("wh_prefix_attention: q bf16 [batch * n_query][64 n_head]")
     rows = shape[0]
     batch = rows // n_query
     if n_kv_head is None:
@@ -375,23 +391,25 @@ def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_
             needs |= WH_OWN_WEIGHT
     table = None
     if group_start is not None:
-        _need(group_start.dtype == torch.int32 and group_start.get_device() == dev and group_start.is_contiguous() and
-              group_start.shape == (n_pre + 1,) and n_pre > 0, "wh_prefix_attention: group_start int32 [prefix sets + 1]")
+        if not (group_start.dtype is _torch.int32 and group_start.get_device() == dev and group_start.is_contiguous() and
+                group_start.shape == (n_pre + 1,) and n_pre > 0):
+            _refuse("wh_prefix_attention: group_start int32 [prefix sets + 1]")
         table = group_start.data_ptr()
         needs |= WH_GROUP_TABLE
     if out is None:
-        out = torch.empty(rows, 64 * n_head, dtype=torch.bfloat16, device=q.device)
-    else:
-        _need(out.dtype == torch.bfloat16 and out.shape == (rows, 64 * n_head) and out.is_contiguous() and
-              out.get_device() == dev, "wh_prefix_attention: out bf16 [batch * n_query][64 n_head]")
+        out = _torch.empty(rows, 64 * n_head, dtype=_torch.bfloat16, device=q.device)
+    elif not (out.dtype is _torch.bfloat16 and out.shape == (rows, 64 * n_head) and out.is_contiguous() and
+              out.get_device() == dev):
+        _refuse("wh_prefix_attention: out bf16 [batch * n_query][64 n_head]")
     s = _stream_handle(dev, stream)
     if workspace is None:
         need = _workspace_bytes("wh_prefix_attention_workspace", batch, n_query, n_head, n_kv_head, n_pre, max_pre, max_own,
                                 needs)
-        scratch = _Scratch(need, s)
-        at = scratch.ptr
+        scratch = _Scratch(need, s) if need else None
+        at = scratch.ptr if need else None
     else:
-        _need(workspace.get_device() == dev and workspace.is_contiguous(), "wh_prefix_attention: workspace")
+        if not (workspace.get_device() == dev and workspace.is_contiguous()):
+            _refuse("wh_prefix_attention: workspace")
         need, at = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     rc = (_lib or lib()).wh_prefix_attention(
         q.data_ptr(), stride[0] if rows > 1 else 64 * n_head, batch, n_query, n_head, n_kv_head,
@@ -408,29 +426,37 @@ def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, worksp
     or, without one, to the front of the cache itself.  kept: optional int32
     [n_set][n_kv_head][budget], the former index of every key that stays.  Returns the new counts:
     out.n_keys or cache.n_keys, updated, or a new int32 [n_set] where that is None."""
-    import torch
     what = "wh_cache_evict"
     to = cache if out is None else out
     dev, n_set = cache.device, cache.n_set
     cache._check(n_kv_head, dev, what)
-    to._check(n_kv_head, dev, what)
-    _need(cache.weight is not None and to.weight is not None, "wh_cache_evict: Keys without weight")
-    _need(0 <= recent <= budget and 1 <= budget <= 1 << 30, "wh_cache_evict: 0 <= recent <= budget, 1 <= budget <= 2^30")
+    if cache.weight is None:
+        _refuse("wh_cache_evict: Keys without weight")
+    if out is not None:
+        out._check(n_kv_head, dev, what)
+        if out.weight is None:
+            _refuse("wh_cache_evict: Keys without weight")
+    if not (0 <= recent <= budget and 1 <= budget <= 1 << 30):
+        _refuse("wh_cache_evict: 0 <= recent <= budget, 1 <= budget <= 2^30")
     indices = None
     if kept is not None:
-        _need(kept.dtype == torch.int32 and kept.shape == (n_set, n_kv_head, budget) and kept.is_contiguous() and
-              kept.get_device() == dev, "wh_cache_evict: kept int32 [n_set][n_kv_head][budget]")
+        if not (kept.dtype is _torch.int32 and kept.shape == (n_set, n_kv_head, budget) and kept.is_contiguous() and
+                kept.get_device() == dev):
+            _refuse("wh_cache_evict: kept int32 [n_set][n_kv_head][budget]")
         indices = kept.data_ptr()
-    n_out = to.n_keys if to.n_keys is not None else torch.empty(n_set, dtype=torch.int32, device=cache.k.device)
+    n_out = to.n_keys
+    if n_out is None:
+        n_out = _torch.empty(n_set, dtype=_torch.int32, device=cache.k.device)
     if n_set == 0 and to.n_set == 0:
         return n_out
     s = _stream_handle(dev, stream)
     if workspace is None:
         need = _workspace_bytes("wh_cache_evict_workspace", n_set, n_kv_head, cache.max_keys, budget)
-        scratch = _Scratch(need, s)
-        at = scratch.ptr
+        scratch = _Scratch(need, s) if need else None
+        at = scratch.ptr if need else None
     else:
-        _need(workspace.get_device() == dev and workspace.is_contiguous(), "wh_cache_evict: workspace")
+        if not (workspace.get_device() == dev and workspace.is_contiguous()):
+            _refuse("wh_cache_evict: workspace")
         need, at = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     rc = (_lib or lib()).wh_cache_evict(cache.c, n_kv_head, budget, recent, None if out is None else out.c,
                                         n_out.data_ptr(), indices, at, need, s)
