@@ -37,7 +37,7 @@ constexpr int SEL_THREADS = 1024;    // k_evict_select, one block a head
 constexpr int SEL_HELD = 32;         // keys that a thread of it holds: longer caches are read again for every bit
 // Clusters of SEL_CTAS blocks of 256 threads choose instead for as many heads of long caches as are resident at
 // once, and for the longest: 60 heads x 9000 keys 35.0 us, 38.3 with a block each; 80 heads 42.5 and 41.1; 60 x 30000
-// 46.0 and 50.5; 20 x 60000 36.6 and 155.
+// 46.0 and 50.5; 20 x 60000 35.0 and 155.
 constexpr int SEL_CTAS = 8;
 constexpr int SEL_SPREAD = 72;
 constexpr int MV_THREADS = 256;
@@ -453,10 +453,10 @@ __global__ void __launch_bounds__(SM_THREADS) k_evict_small(const EvArgs p) {
 }
 
 // Chooses only: a warp (of four), a block or a cluster of CTAS blocks per head and set.
-// (64 registers for the blocks of a cluster with 16 weights a thread: 72 clusters at once instead of 36; 40 heads x
-// 9000 keys 31.2 us -> 27.5)
+// (Four blocks of a cluster to an SM with 16 weights a thread, 72 clusters at once instead of 36: 40 heads x 9000 keys
+// 31.2 us -> 27.5; two with 32 a thread.)
 template <int CHOOSERS, int E, int CTAS = 1>
-__global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS, CTAS > 1 && E == 16 ? 4 : 1) k_evict_select(const EvArgs p) {
+__global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS, CTAS == 1 ? 0 : E == 16 ? 4 : 2) k_evict_select(const EvArgs p) {
     __shared__ int buf[2 * SEL_THREADS / 32], peers[2 * CTAS];
     __shared__ uint32_t bins[CTAS > 1 ? 256 : 1];
     pdl_wait();
