@@ -110,6 +110,8 @@ CASES = {
     "a few long heads": dict(heads=2, cap=1900, counts=[1900, 1025, 1024], budget=900, recent=50, kind="ties"),
     "many long heads": dict(heads=8, cap=1030, counts=[1030 - 7 * i for i in range(40)], budget=700, recent=50, kind="odd"),
     "long, many heads": dict(heads=20, cap=9001, counts=[9001, 9000, 8193, 700], budget=333, recent=3, kind="ties"),
+    "longer, many heads": dict(heads=20, cap=17001, counts=[17001, 16385, 15000, 333], budget=500, recent=3, kind="odd"),
+    "thousands of keys, many heads": dict(heads=20, cap=4001, counts=[4001 - 37 * i for i in range(31)], budget=133, recent=3, kind="ties"),
     "long, equal": dict(heads=1, cap=33333, counts=[33333], budget=32768, recent=0, kind="equal"),
     "long, odd weights": dict(heads=2, cap=50001, counts=[50001, 40000], budget=49999, recent=7, kind="odd"),
     "many sets": dict(heads=2, cap=64, counts=[(7 * i) % 65 for i in range(300)], budget=31, recent=4, kind="ties"),
@@ -122,7 +124,7 @@ def test_choice(name, in_place):
     Case(seed=len(name), **CASES[name]).check(in_place)
 
 
-@pytest.mark.parametrize("n", [1, 31, 32, 33, 255, 256, 257, 511, 512, 513, 1023, 1024, 1025, 2047, 2048, 2049, 8191, 8192, 8193, 32768, 32769, 65535, 65536])
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 255, 256, 257, 511, 512, 513, 1023, 1024, 1025, 2047, 2048, 2049, 4096, 4097, 8191, 8192, 8193, 16384, 16385, 32768, 32769, 65535, 65536])
 def test_lengths(n):
     Case(heads=2, cap=n, counts=[n, n // 2], budget=max(1, n // 3), recent=min(5, max(1, n // 3)), seed=n).check(n % 2 == 0)
 

@@ -33,11 +33,12 @@ constexpr int SM_MOST = 2048;        // its longest cache
 //    12 heads 2000 -> 1500   17.1  10.9   (the second kernel costs the host 4 us more)
 constexpr int SM_ROWS = 1024;
 constexpr int SM_HEADS = 4 * 152;
-constexpr int SEL_THREADS = 1024;    // k_evict_select, one block a head
-constexpr int SEL_HELD = 32;         // keys that a thread of it holds: longer caches are read again for every bit
-// Clusters of SEL_CTAS blocks of 256 threads choose instead for as many heads of long caches as are resident at
-// once, and for the longest: 60 heads x 9000 keys 35.0 us, 38.3 with a block each; 80 heads 42.5 and 41.1; 60 x 30000
-// 46.0 and 50.5; 20 x 60000 35.0 and 155.
+constexpr int SEL_THREADS = 1024;    // k_evict_select: the most threads of one block a head
+// Up to 16 keys a thread where that many threads can hold them (up to 4096 keys a block of 256: 1000 heads x 3000 keys
+// 62 us, 99 with 1024 threads of 8 keys; up to 8192 one of 512; up to 16384 one of 1024: 200 heads x 9000 keys 62 us,
+// 80 with 32 keys a thread).  Clusters of SEL_CTAS blocks of 256 threads choose instead for as many heads of long
+// caches as are resident at once, and for the longest: 20 heads x 9000 keys 16.3 us, 19.7 with a block each; 60 heads
+// 27.8 and 28.3; 60 x 30000 46.2 and 50.5; 20 x 60000 35 and 155.
 constexpr int SEL_CTAS = 8;
 constexpr int SEL_SPREAD = 72;
 constexpr int MV_THREADS = 256;
@@ -453,10 +454,10 @@ __global__ void __launch_bounds__(SM_THREADS) k_evict_small(const EvArgs p) {
 }
 
 // Chooses only: a warp (of four), a block or a cluster of CTAS blocks per head and set.
-// (Four blocks of a cluster to an SM with 16 weights a thread, 72 clusters at once instead of 36: 40 heads x 9000 keys
-// 31.2 us -> 27.5; two with 32 a thread.)
+// (Four blocks of a cluster to an SM with up to 16 weights a thread, 72 clusters at once instead of 36: 40 heads x
+// 30000 keys 40.3 us -> 35.8; two with 32 a thread.)
 template <int CHOOSERS, int E, int CTAS = 1>
-__global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS, CTAS == 1 ? 0 : E == 16 ? 4 : 2) k_evict_select(const EvArgs p) {
+__global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS, CTAS == 1 ? 0 : E <= 16 ? 4 : 2) k_evict_select(const EvArgs p) {
     __shared__ int buf[2 * SEL_THREADS / 32], peers[2 * CTAS];
     __shared__ uint32_t bins[CTAS > 1 ? 256 : 1];
     pdl_wait();
@@ -690,14 +691,20 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
             rc = launch_ex(k_evict_select<32, 32>, warps, 128, 0, 1, true, s, a);
         else if (a.max_keys <= 2048)
             rc = launch_ex(k_evict_select<256, 8>, blocks, 256, 0, 1, true, s, a);
+        else if (a.max_keys <= 4096)
+            rc = launch_ex(k_evict_select<256, 16>, blocks, 256, 0, 1, true, s, a);
         else if (a.max_keys <= 8192)
-            rc = launch_ex(k_evict_select<SEL_THREADS, 8>, blocks, SEL_THREADS, 0, 1, true, s, a);
-        else if (a.max_keys <= SEL_CTAS * 256 * 16 && items <= SEL_SPREAD)
+            rc = launch_ex(k_evict_select<512, 16>, blocks, 512, 0, 1, true, s, a);
+        else if (a.max_keys <= 16384 && items <= SEL_SPREAD)
+            rc = launch_ex(k_evict_select<256, 8, SEL_CTAS>, dim3((unsigned)(items * SEL_CTAS)), 256, 0, SEL_CTAS, true, s, a);
+        else if (a.max_keys <= 16384)
+            rc = launch_ex(k_evict_select<SEL_THREADS, 16>, blocks, SEL_THREADS, 0, 1, true, s, a);
+        else if (a.max_keys <= 32768 && items <= SEL_SPREAD)
             rc = launch_ex(k_evict_select<256, 16, SEL_CTAS>, dim3((unsigned)(items * SEL_CTAS)), 256, 0, SEL_CTAS, true, s, a);
-        else if (a.max_keys < SEL_CTAS * 256 * 32 && (items <= SEL_SPREAD || a.max_keys > SEL_HELD * SEL_THREADS))
+        else if (a.max_keys <= 32768)
+            rc = launch_ex(k_evict_select<SEL_THREADS, 32>, blocks, SEL_THREADS, 0, 1, true, s, a);
+        else if (a.max_keys < 65536)
             rc = launch_ex(k_evict_select<256, 32, SEL_CTAS>, dim3((unsigned)(items * SEL_CTAS)), 256, 0, SEL_CTAS, true, s, a);
-        else if (a.max_keys <= SEL_HELD * SEL_THREADS)
-            rc = launch_ex(k_evict_select<SEL_THREADS, SEL_HELD>, blocks, SEL_THREADS, 0, 1, true, s, a);
         else
             rc = launch_ex(k_evict_select<SEL_THREADS, 0>, blocks, SEL_THREADS, 0, 1, true, s, a);
         if (!rc)
