@@ -112,6 +112,8 @@ CASES = {
     "long, many heads": dict(heads=20, cap=9001, counts=[9001, 9000, 8193, 700], budget=333, recent=3, kind="ties"),
     "longer, many heads": dict(heads=20, cap=17001, counts=[17001, 16385, 15000, 333], budget=500, recent=3, kind="odd"),
     "thousands of keys, many heads": dict(heads=20, cap=4001, counts=[4001 - 37 * i for i in range(31)], budget=133, recent=3, kind="ties"),
+    "most of it stays": dict(heads=20, cap=1500, counts=[1500 - 11 * i for i in range(16)], budget=1200, recent=3, kind="ties"),
+    "few heads, most of it stays": dict(heads=1, cap=30000, counts=[30000, 20000, 16001], budget=16000, recent=500, layout="kv"),
     "long, equal": dict(heads=1, cap=33333, counts=[33333], budget=32768, recent=0, kind="equal"),
     "long, odd weights": dict(heads=2, cap=50001, counts=[50001, 40000], budget=49999, recent=7, kind="odd"),
     "many sets": dict(heads=2, cap=64, counts=[(7 * i) % 65 for i in range(300)], budget=31, recent=4, kind="ties"),

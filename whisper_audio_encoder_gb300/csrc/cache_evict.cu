@@ -9,12 +9,12 @@
 // few equal to W, the recent ones.
 // Moving is a copy of 128-byte rows, 16 bytes a thread, bound by HBM: within the cache every key moves towards
 // the front, so going up the rows with each step's reads before its writes is safe.
-// 512 sets x 20 heads of 301 .. 448 keys to 224: 190 us, 1.21 GB, 94 % of the copy rate (choosing takes 15 us of
-// it, mostly instructions: 1600 a warp of 448 keys); 20 heads x 30000 keys to 4001: 27 us for 44 MB, of which
-// choosing takes 15 (six steps of counts and a cluster barrier).
+// 512 sets x 20 heads of 301 .. 448 keys to 224: 189 us, 1.21 GB, 94 % of the copy rate (choosing takes 15 us of
+// it, mostly instructions: 1600 a warp of 448 keys); 20 heads x 30000 keys to 4001: 24 us for 44 MB, of which
+// choosing takes 13 (five steps of counts and a cluster barrier).
 //   k_evict_small   up to 2048 keys: a block chooses and moves one head of one set
 //   k_evict_select, then k_evict_move (other buffers: rows spread over the device) or k_evict_shift (within
-//   the cache: a block per head and keys or values), for long caches and where few heads move many rows
+//   the cache: a cluster per head and keys or values), for long caches and where few heads move many rows
 #include <algorithm>
 
 #include "common.cuh"
@@ -25,12 +25,13 @@ namespace {
 
 constexpr int SM_THREADS = 256;      // k_evict_small
 constexpr int SM_MOST = 2048;        // its longest cache
-// It is taken for up to SM_HEADS heads (what is resident at once) that move up to SM_ROWS rows, or for at least
-// half as many heads that move more; us a call in one kernel and in two, keys -> budget:
-//    12 heads  448 ->  224    8.9  10.3      480 heads  448 -> 224    17.1  20.5
-//   320 heads  448 ->  224   14.4  16.4      800 heads  448 -> 224    25.9  26.2
-//    12 heads 2000 ->  600   13.0  12.1      200 heads 2000 -> 1500   35.2  35.4
-//    12 heads 2000 -> 1500   17.1  10.9   (the second kernel costs the host 4 us more)
+// It is taken for up to SM_HEADS heads (what is resident at once) that move up to SM_ROWS rows, and within the cache for
+// at least half as many heads that move more; us a replayed call in one kernel and in two, keys -> budget:
+//    12 heads  448 ->  224    8.2  10.3      480 heads  448 -> 224    16.7  18.5
+//   320 heads  448 ->  224   13.4  16.4      800 heads  448 -> 224    24.7  25.4
+//    12 heads 2000 ->  600   12.4  11.0   (the second kernel costs the host 4 us more)
+//    12 heads 2000 -> 1500   16.7  11.6      320 heads 2000 -> 1500   53.0  49.2
+//   within the cache, the copy of it that the caller makes included: 320 heads 1500 -> 1200 84.1 and 94.3
 constexpr int SM_ROWS = 1024;
 constexpr int SM_HEADS = 4 * 152;
 constexpr int SEL_THREADS = 1024;    // k_evict_select: the most threads of one block a head
@@ -43,7 +44,12 @@ constexpr int SEL_CTAS = 8;
 constexpr int SEL_SPREAD = 72;
 constexpr int MV_THREADS = 256;
 constexpr int MV_PIECES = 1024;      // 16-byte pieces (of keys, and of values) of a block of k_evict_move
-constexpr int SH_THREADS = 512;      // k_evict_shift
+// k_evict_shift.  20 heads 30000 keys -> 15000, the caller's copy of the cache (about 80 us) included: 241 us with one
+// block of 512 threads and 4 rows a thread for each head, 144 with clusters of eight, 123 with four blocks of 256
+// threads an SM, 118 with six rows a thread, 141 with eight (registers).
+constexpr int SH_THREADS = 256;
+constexpr int SH_ROWS = 6;           // rows of a thread that are under way together
+constexpr int SH_RESIDENT = 4;       // blocks of an SM
 
 struct EvArgs {
     const __nv_bfloat16 *k, *v;
@@ -398,8 +404,9 @@ __device__ __forceinline__ int count_of(const EvArgs &p, int set, bool report) {
     return n;
 }
 
-// One head of one set: choose (warp 0, or the whole block for more than 32 E keys), then move.
-template <int CHOOSERS, int E>
+// One head of one set: the block chooses, E keys a thread, then moves.  (A warp that chose among 900 keys took 14.4 us
+// for 12 heads, the block 10.3; among 448 9.0 and 8.2.)
+template <int E>
 __global__ void __launch_bounds__(SM_THREADS) k_evict_small(const EvArgs p) {
     extern __shared__ int src[];   // [budget]
     __shared__ int buf[2 * SM_THREADS / 32];
@@ -419,8 +426,8 @@ __global__ void __launch_bounds__(SM_THREADS) k_evict_small(const EvArgs p) {
             if (kept) kept[i] = i;
             if (!p.in_place) wo[i] = w[i];
         }
-    } else if (CHOOSERS != 32 || tid < 32) {
-        Team<CHOOSERS> team{buf, nullptr, 0, nullptr};
+    } else {
+        Team<SM_THREADS> team{buf, nullptr, 0, nullptr};
         choose<E>(team, w, n, p.budget, p.recent, src, kept, wo);
     }
     if (all && p.in_place) return;
@@ -522,16 +529,19 @@ __global__ void __launch_bounds__(MV_THREADS) k_evict_move(const EvArgs p) {
         }
 }
 
-// The same within the cache, one block per (head, set, keys or values).
-__global__ void __launch_bounds__(SH_THREADS) k_evict_shift(const EvArgs p) {
+// The same within the cache: the blocks of a cluster per (head, set, keys or values).  A step's rows are all read
+// before any is written, and no later row comes from where it writes.
+template <int CTAS>
+__global__ void __launch_bounds__(SH_THREADS, SH_RESIDENT) k_evict_shift(const EvArgs p) {
     pdl_wait();
-    const int h = blockIdx.x, set = blockIdx.y, n0 = __ldcg(p.count + set), n = min(n0, p.budget);
-    if (h == 0 && blockIdx.z == 0 && threadIdx.x == 0) p.n_out[set] = n;
+    const int item = blockIdx.x / CTAS, h = item % p.n_head, set = item / p.n_head, rank = blockIdx.x % CTAS;
+    const int n0 = __ldcg(p.count + set), n = min(n0, p.budget), place = rank * SH_THREADS + threadIdx.x;
+    if (h == 0 && blockIdx.y == 0 && place == 0) p.n_out[set] = n;
     if (n0 <= p.budget) return;
-    __nv_bfloat16 *x = (blockIdx.z ? p.v_out : p.k_out) + (long long)set * p.set_stride + h * 64 + 8 * (threadIdx.x & 7);
+    __nv_bfloat16 *x = (blockIdx.y ? p.v_out : p.k_out) + (long long)set * p.set_stride + h * 64 + 8 * (threadIdx.x & 7);
     const int *src = p.kept + ((long long)set * p.n_head + h) * p.budget;
-    constexpr int U = 4, STEP = SH_THREADS / 8;
-    for (int base = threadIdx.x >> 3; base < (n + U * STEP - 1) / (U * STEP) * (U * STEP); base += U * STEP) {
+    constexpr int U = SH_ROWS, STEP = CTAS * SH_THREADS / 8;
+    for (int base = place >> 3; base < (n + U * STEP - 1) / (U * STEP) * (U * STEP); base += U * STEP) {
         int t[U];
         uint4 a[U];
 #pragma unroll
@@ -541,7 +551,12 @@ __global__ void __launch_bounds__(SH_THREADS) k_evict_shift(const EvArgs p) {
             if (t[u] == base + u * STEP) t[u] = -1;   // where it was
             if (t[u] >= 0) a[u] = __ldcg(reinterpret_cast<const uint4 *>(x + (long long)t[u] * p.row_stride));
         }
-        __syncthreads();
+        if (CTAS > 1) {
+            __syncwarp();
+            cluster_sync();
+        } else {
+            __syncthreads();
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (t[u] >= 0) *reinterpret_cast<uint4 *>(x + (long long)(base + u * STEP) * p.row_stride) = a[u];
@@ -555,10 +570,20 @@ __global__ void k_evict_counts(const EvArgs p, int *n_out) {
         n_out[i] = min(count_of(p, i, false), p.budget);
 }
 
-bool one_kernel(int n_set, int n_head, int max_keys, int budget) {
+// The largest clusters that are resident at once and have rows for all their blocks (200 heads 9000 keys -> 3000: 234 us,
+// copy included, 245 with clusters twice as large).
+int launch_shift(const EvArgs &a, int most, long long items, cudaStream_t s) {
+    const int steps = (most + SH_ROWS * SH_THREADS / 8 - 1) / (SH_ROWS * SH_THREADS / 8);
+    int ctas = 8;
+    while (ctas > 1 && (2 * items * ctas > SH_RESIDENT * 152 || ctas / 2 >= steps)) ctas /= 2;
+    auto *kernel = ctas == 8 ? k_evict_shift<8> : ctas == 4 ? k_evict_shift<4> : ctas == 2 ? k_evict_shift<2> : k_evict_shift<1>;
+    return launch_ex(kernel, dim3((unsigned)(items * ctas), 2), SH_THREADS, 0, ctas, true, s, a);
+}
+
+bool one_kernel(int n_set, int n_head, int max_keys, int budget, bool in_place) {
     const long long items = (long long)n_set * n_head;
     return max_keys <= SM_MOST && items <= SM_HEADS &&
-           (budget <= SM_ROWS || max_keys <= SM_ROWS || 2 * items >= SM_HEADS);
+           (budget <= SM_ROWS || max_keys <= SM_ROWS || (in_place && 2 * items >= SM_HEADS));
 }
 
 size_t up256e(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -608,7 +633,7 @@ using namespace wh;
 
 extern "C" size_t wh_cache_evict_workspace(int n_set, int n_kv_head, int max_keys, int budget) {
     if (n_set < 1 || n_set > 65535 || n_kv_head < 1 || n_kv_head > 1024 || max_keys < 1 || max_keys > (1 << 30) ||
-        budget < 1 || budget > (1 << 30) || one_kernel(n_set, n_kv_head, max_keys, budget))
+        budget < 1 || budget > (1 << 30) || one_kernel(n_set, n_kv_head, max_keys, budget, false))
         return 0;
     return up256e((size_t)n_set * 4) + up256e((size_t)n_set * n_kv_head * budget * 4);
 }
@@ -674,12 +699,11 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
     int rc;
     trace_begin(TR_DEC_OTHER, s);
     const long long items = (long long)n_kv_head * a.n_set;
-    if (one_kernel(a.n_set, n_kv_head, a.max_keys, budget)) {
+    if (one_kernel(a.n_set, n_kv_head, a.max_keys, budget, a.in_place)) {
         const bool same = n_out == a.n_keys;
         a.kept = kept;
         a.n_out = same ? nullptr : n_out;
-        auto *kernel = a.max_keys <= 512 ? k_evict_small<32, 16>
-                       : a.max_keys <= 1024 ? k_evict_small<32, 32> : k_evict_small<SM_THREADS, 8>;
+        auto *kernel = a.max_keys <= 512 ? k_evict_small<2> : a.max_keys <= 1024 ? k_evict_small<4> : k_evict_small<8>;
         rc = launch_ex(kernel, heads, SM_THREADS, most * (int)sizeof(int), 1, true, s, a);
         if (!rc && same) rc = launch_ex(k_evict_counts, dim3((a.n_set + 255) / 256), 256, 0, 1, true, s, a, n_out);
     } else {
@@ -708,7 +732,7 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
         else
             rc = launch_ex(k_evict_select<SEL_THREADS, 0>, blocks, SEL_THREADS, 0, 1, true, s, a);
         if (!rc)
-            rc = a.in_place ? launch_ex(k_evict_shift, dim3(n_kv_head, a.n_set, 2), SH_THREADS, 0, 1, true, s, a)
+            rc = a.in_place ? launch_shift(a, most, items, s)
                             : launch_ex(k_evict_move, dim3((unsigned)(((long long)most * n_kv_head * 8 + MV_PIECES - 1) / MV_PIECES), a.n_set),
                                         MV_THREADS, 0, 1, true, s, a);
     }
