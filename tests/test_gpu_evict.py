@@ -310,6 +310,9 @@ def test_numbers_past_the_library_s_types_are_refused():
     q = torch.zeros(1, 128, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(wh.WhError):
         wh.wh_prefix_attention(q, 2, prefix=wh.Keys(c.k, c.v), n_kv_head=2 - (1 << 32))
+    for shape in ((1, (1 << 32) + 1, 128), ((1 << 32) + 1, 1, 128), (65536, 1, 128)):
+        with pytest.raises(wh.WhError):
+            wh.Keys(q[None].expand(*shape), q[None].expand(*shape))
     assert same(c.store, before) and wh.wh_status() == wh.WH_OK
 
 

@@ -79,3 +79,8 @@ def test_binding_checks_its_tensors():
             wh.Keys(*args)
     with pytest.raises(wh.WhError):
         wh.wh_prefix_attention(k[0], 2)
+
+
+def test_keys_are_packed_field_by_field():
+    c = wh.wh_keys.from_buffer_copy(wh._pack_keys(1 << 40, 2, 3, 4, 5, 0, 7, 8))
+    assert [getattr(c, f) for f, _ in wh.wh_keys._fields_] == [1 << 40, 2, 3, 4, 5, None, 7, 8]
