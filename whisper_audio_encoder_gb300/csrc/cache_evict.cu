@@ -11,7 +11,7 @@
 // the front, so going up the rows with each step's reads before its writes is safe.
 // 512 sets x 20 heads of 301 .. 448 keys to 224: 189 us, 1.21 GB, 94 % of the copy rate (choosing takes 15 us of
 // it, mostly instructions: 1600 a warp of 448 keys); 20 heads x 30000 keys to 4001: 24 us for 44 MB, of which
-// choosing takes 13 (five steps of counts and a cluster barrier).
+// choosing takes 15 (a search of four or five steps of 3100 cycles, numbering 5500).
 //   k_evict_small   up to 2048 keys: a block chooses and moves one head of one set
 //   k_evict_select, then k_evict_move (other buffers: rows spread over the device) or k_evict_shift (within
 //   the cache: a cluster per head and keys or values), for long caches and where few heads move many rows
@@ -171,9 +171,10 @@ __device__ __forceinline__ void find_threshold(int need, uint32_t most, uint32_t
 
 // The same for a cluster, four bits at a time: every thread counts its images under the decided bits in 16 bins of
 // 8 bits, the warps, blocks and the cluster add them in bins of 16 (fewer than 65536 older keys: the `pads` zero images
-// of a thread that stand for none are not counted).  A step
-// costs little more than one bit's count would, most of it the cluster barrier.  The first step guesses that the
-// threshold lies in 2^-19 .. 512, where weights of long caches mostly do, and then knows eight bits of it; else the steps begin anew.
+// of a thread that stand for none are not counted).  A step takes 3100 cycles with 16 images a thread: counting 1100,
+// adding in the warps 630, the cluster barrier 570.  (Bins counted by ballots: 24.2 -> 25.3 us for 20 heads x 30000.)
+// The first step guesses that the threshold lies in 2^-19 .. 512, where weights of long caches mostly do, and then
+// knows eight bits of it; else the steps begin anew.
 template <int E, class T>
 __device__ __forceinline__ void find_threshold_radix(T &team, int need, const uint32_t (&key)[E], int pads, uint32_t &W, int &ties) {
     static_assert(E < 256 && T::WARPS == 8 && T::BLOCKS == 8, "the bins' widths, the lanes' shares");
