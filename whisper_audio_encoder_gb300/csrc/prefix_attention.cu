@@ -568,8 +568,9 @@ constexpr int PT_MIN_ROWS = 16;
 constexpr long long PT_MIN_WORK = 300000;
 // Ranges of at least PT_LEAST keys (rounded down): a shorter block does not make up for joining one range more.
 // 128 rows x 800 keys x 4 sets: 16.4 us with one range, 20.5 with the three that would fill the device;
-// 40 rows x 8000 keys: 20.9 with 15, 58.8 with one.
-constexpr int PT_LEAST = 512;
+// 40 rows x 8000 keys: 20.9 with 15, 58.8 with one.  Beside own keys, whose blocks join them anyway, PT_LEAST_OWN: 256
+// rows x 900 keys, 8 heads, 24.0 us and 20.7; 8 groups of 45 queries x 2 heads x 1000 keys, 6 key heads, 20.5 and 18.1.
+constexpr int PT_LEAST = 512, PT_LEAST_OWN = 384;
 constexpr int PA_CLUSTER = 16, PT_CLUSTER = 2;   // ranges that a cluster's blocks join by themselves
 // Up to this many keys a block, one cluster instead of more ranges and the merge kernel: 5 rows x 2 heads x
 // 30000 keys 17.8 us in clusters of 16, 30 us in 228 ranges; 5 x 6 x 1500: 8.2 in 16, 11.7 in 24.
@@ -621,8 +622,10 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     a.own_tiles = (int)((per + PA_TILE - 1) / PA_TILE);
     const auto ranges = [](const PaSet &s, int least) { return ((long long)s.max_keys + least - 1) / least; };
     constexpr int STEP = PA_WARPS * PA_SLOT_KEYS;
+    // (with ragged groups the slots are more than the tiles that there will be, by half a tile a set on average)
+    const long long tiles = a.slots - (a.gsize == 0 && has_own ? a.pre.n_set / 2 : 0);
     if (pl.tc)
-        split_keys(a.pre, (long long)a.slots * a.n_kv, PT_BLOCKS, PT_KEYS, a.pre.max_keys / PT_LEAST);
+        split_keys(a.pre, tiles * a.n_kv, PT_BLOCKS, PT_KEYS, a.pre.max_keys / (has_own ? PT_LEAST_OWN : PT_LEAST));
     else
         split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, STEP, ranges(a.pre, STEP));
     // own keys: one warp an item when that fills the device, more warps, then key ranges, when it does not (us a
