@@ -568,9 +568,9 @@ constexpr int PT_MIN_ROWS = 16;
 constexpr long long PT_MIN_WORK = 300000;
 // Ranges of at least PT_LEAST keys (rounded down): a shorter block does not make up for joining one range more.
 // 128 rows x 800 keys x 4 sets: 16.4 us with one range, 20.5 with the three that would fill the device;
-// 40 rows x 8000 keys: 20.9 with 15, 58.8 with one.  Beside own keys, whose blocks join them anyway, PT_LEAST_OWN: 256
+// 40 rows x 8000 keys: 20.9 with 15, 58.8 with one.  Beside own keys, whose blocks join them anyway, PT_LEAST_BESIDE: 256
 // rows x 900 keys, 8 heads, 24.0 us and 20.7; 8 groups of 45 queries x 2 heads x 1000 keys, 6 key heads, 20.5 and 18.1.
-constexpr int PT_LEAST = 512, PT_LEAST_OWN = 384;
+constexpr int PT_LEAST = 512, PT_LEAST_BESIDE = 384;
 constexpr int PA_CLUSTER = 16, PT_CLUSTER = 2;   // ranges that a cluster's blocks join by themselves
 // Up to this many keys a block, one cluster instead of more ranges and the merge kernel: 5 rows x 2 heads x
 // 30000 keys 17.8 us in clusters of 16, 30 us in 228 ranges; 5 x 6 x 1500: 8.2 in 16, 11.7 in 24.
@@ -580,7 +580,10 @@ constexpr int PA_CLUSTERS[PA_CLUSTER + 1] = {0, 456, 228, 148, 110, 87, 74, 59, 
 constexpr int PA_SCORE_BYTES = 8192;   // own keys' scores kept by a block; three blocks still fit an SM
 // Beside a prefix, own keys are cut into ranges of at least this many: one range needs no merge kernel.  2
 // sequences x 6 heads x 900 keys: 12.4 us, 10.3 with ranges of 64 keys, but 4 us more of the host's time.
-constexpr int PA_OWN_LEAST = 512;
+constexpr int OWN_LEAST = 512;
+// The prefix's own ranges then, which the own keys' blocks join: 8 rows x 6 heads x 447 keys, up to 200 own keys 10.3 us
+// with ranges of 64 keys, 8.2 with 256; 2 sequences x 3 queries x 1500 keys, 8 heads, up to 400 12.0 and 10.3.
+constexpr int PA_LEAST_BESIDE = 256;
 
 // Key ranges of a set: as many as are resident at once, in whole steps of a block, `most` at most.
 void split_keys(PaSet &s, long long items, long long blocks, int step, long long most) {
@@ -625,9 +628,9 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     // (with ragged groups the slots are more than the tiles that there will be, by half a tile a set on average)
     const long long tiles = a.slots - (a.gsize == 0 && has_own ? a.pre.n_set / 2 : 0);
     if (pl.tc)
-        split_keys(a.pre, tiles * a.n_kv, PT_BLOCKS, PT_KEYS, a.pre.max_keys / (has_own ? PT_LEAST_OWN : PT_LEAST));
+        split_keys(a.pre, tiles * a.n_kv, PT_BLOCKS, PT_KEYS, a.pre.max_keys / (has_own ? PT_LEAST_BESIDE : PT_LEAST));
     else
-        split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, STEP, ranges(a.pre, STEP));
+        split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, STEP, ranges(a.pre, has_own ? PA_LEAST_BESIDE : STEP));
     // own keys: one warp an item when that fills the device, more warps, then key ranges, when it does not (us a
     // call with one, two, four warps: 16 sequences x 20 heads x 448 keys 17.3, 14.2, 12.3; 80 sequences 35.0,
     // 35.0, 41.2; 256 sequences x 64 keys 24.6, -, 49.0)
@@ -636,7 +639,7 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     while (a.own_wpi > 1 && (items * a.own_wpi > PA_BLOCKS * PA_WARPS || (a.own_wpi - 1) * PA_KEYS >= a.own.max_keys))
         a.own_wpi /= 2;
     split_keys(a.own, items, PA_BLOCKS * (PA_WARPS / a.own_wpi), a.own_wpi * PA_KEYS,
-               ranges(a.own, has_pre ? PA_OWN_LEAST : STEP));
+               ranges(a.own, has_pre ? OWN_LEAST : STEP));
     a.own_items = items * a.own.splits;
     const bool one_launch = a.own_wpi == PA_WARPS && a.own.splits <= PA_CLUSTER && !has_pre;
     a.own_cluster = has_own && (a.own.splits == 1 || one_launch) ? a.own.splits : 0;
