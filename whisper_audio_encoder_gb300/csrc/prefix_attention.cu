@@ -634,9 +634,14 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     // own keys: one warp an item when that fills the device, more warps, then key ranges, when it does not (us a
     // call with one, two, four warps: 16 sequences x 20 heads x 448 keys 17.3, 14.2, 12.3; 80 sequences 35.0,
     // 35.0, 41.2; 256 sequences x 64 keys 24.6, -, 49.0)
+    // (warps without keys still finish rows beside a prefix: 2 sequences x 16 queries x 1500 keys and 17 own, 20 heads 12.0
+    // us with four warps, 16.4 with one)
     const long long items = (long long)a.own.n_set * a.n_kv * a.own_tiles;
+    const long long pieces = has_pre ? 8 * (per < PA_TILE ? per : PA_TILE) : 0;   // of 16 bytes that an item finishes
     a.own_wpi = PA_WARPS;
-    while (a.own_wpi > 1 && (items * a.own_wpi > PA_BLOCKS * PA_WARPS || (a.own_wpi - 1) * PA_KEYS >= a.own.max_keys))
+    while (a.own_wpi > 1 &&
+           (items * a.own_wpi > PA_BLOCKS * PA_WARPS ||
+            ((a.own_wpi - 1) * PA_KEYS >= a.own.max_keys && 32 * (a.own_wpi - 1) >= pieces)))
         a.own_wpi /= 2;
     split_keys(a.own, items, PA_BLOCKS * (PA_WARPS / a.own_wpi), a.own_wpi * PA_KEYS,
                ranges(a.own, has_pre ? OWN_LEAST : STEP));
