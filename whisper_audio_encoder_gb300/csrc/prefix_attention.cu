@@ -84,6 +84,11 @@ __device__ __forceinline__ void load_q(const PaArgs &p, const Rows &rw, int r0, 
     }
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
 // Scores of 16 rows x 8 keys: lane (g, c) gives keys 2c, 2c+1 of rows g (0, 1) and g + 8 (2, 3).
 __device__ __forceinline__ void score8(const uint32_t (&a)[4][4], const uint4 &k0, const uint4 &k1, float (&s)[4]) {
     s[0] = s[1] = s[2] = s[3] = 0.0f;
@@ -444,10 +449,11 @@ __global__ void __launch_bounds__(16 * PM_TEAMS) k_prefix_merge(const PaArgs p) 
 // 16 at a time; each sum has one fixed order.  Bound by the keys' bytes for few rows.  Reading the keys again
 // costs half of what the attention reads; keeping the scores would cost 8 bytes a (row, key) pair.  16 prefixes of
 // 211 .. 1500 keys, 83 rows, 20 heads: about 10 us for 34 MB of keys, most of them still in L2.
-__global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p, int own) {
+template <bool OWN>
+__global__ void __launch_bounds__(32 * PW_WARPS, 4) k_prefix_weight(const PaArgs p) {
     __shared__ __align__(128) uint8_t rings[PW_WARPS][2 * PW_KEYS * 128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const PaSet &ks = own ? p.own : p.pre;
+    const PaSet &ks = OWN ? p.own : p.pre;
     Rows rw;
     rw.hk = blockIdx.y;
     const int set = blockIdx.z;
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
         return;
     }
     int s0 = set, e0 = set + 1;
-    if (!own) group_range(p, set, s0, e0);
+    if (!OWN) group_range(p, set, s0, e0);
     rw.seq0 = s0;
     rw.n = (e0 - s0) * p.nq * p.rep;
     const int crow = lane >> 3, piece = lane & 7;
@@ -477,24 +483,27 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
     };
     fetch(t0, 0);
     pdl_wait();
-    uint32_t qa[4][4];
-    float2 st[2];
-    int lim[2];
-    auto load_rows = [&](int r0) {
-        load_q(p, rw, r0, qa);
+    struct Queries {   // of rows r0 + g, r0 + g + 8
+        uint32_t a[4][4];
+        float2 st[2];   // their maximum and 1 / sum; rows past the last: zeros, and their scores are zero
+        int lim[2];     // own keys: the first key that the row does not see
+    };
+    auto load_rows = [&](int r0, Queries &x) {
+        load_q(p, rw, r0, x.a);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            st[half] = make_float2(0.0f, 0.0f);
-            lim[half] = 0;   // rows past the last: no key
+            x.st[half] = make_float2(0.0f, 0.0f);
+            x.lim[half] = 0;
             if (r0 + g + 8 * half < rw.n) {
                 int qrow, head, qi;
                 rw.locate(p, r0 + g + 8 * half, qrow, head, qi);
-                st[half] = __ldcg(p.stats + (long long)qrow * p.n_head + head);
-                lim[half] = own ? nk - (p.nq - 1 - qi) : nk;
+                x.st[half] = __ldcg(p.stats + (long long)qrow * p.n_head + head);
+                x.lim[half] = nk - (p.nq - 1 - qi);
             }
         }
     };
-    load_rows(0);
+    Queries now;
+    load_rows(0, now);
     // the key whose sum this lane ends up with
     const int mine = ((lane & 16) ? 16 : 0) + ((lane & 8) ? 8 : 0) + 2 * c + ((lane & 4) ? 1 : 0);
     float *w = ks.weight + ((long long)set * p.n_kv + rw.hk) * ks.max_keys + mine;
@@ -511,23 +520,38 @@ __global__ void __launch_bounds__(32 * PW_WARPS) k_prefix_weight(const PaArgs p,
             kr[j][1] = lds128(kk + (((c + 4) ^ ((g & 1) << 2)) << 4));
         }
         __syncwarp();
-        float acc[4][2] = {};
+        uint64_t sum2[4] = {};   // of keys 8j + 2c, 8j + 2c + 1
         for (int r0 = 0; r0 < rw.n; r0 += 16) {
-            if (rw.n > 16) load_rows(r0);
+            Queries next;   // on their way while these are worked on (after the last the first: the next step's)
+            if (rw.n > 16) load_rows(r0 + 16 < rw.n ? r0 + 16 : 0, next);
+            float s[4][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float s[4];
-                score8(qa, kr[j][0], kr[j][1], s);
+            for (int j = 0; j < 4; ++j) score8(now.a, kr[j][0], kr[j][1], s[j]);
+            const uint64_t scale = f2_pack(PA_SCALE, PA_SCALE);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = t0 + 8 * j + 2 * c + (i & 1);
+            for (int half = 0; half < 2; ++half) {
+                const uint64_t less = f2_pack(-now.st[half].x, -now.st[half].x), inv = f2_pack(now.st[half].y, now.st[half].y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float e0, e1;
+                    f2_unpack(mul_f2(add_f2(f2_pack(s[j][2 * half], s[j][2 * half + 1]), less), scale), e0, e1);
+                    f2_unpack(mul_f2(f2_pack(ex2_approx(e0), ex2_approx(e1)), inv), e0, e1);
                     // (no weight is above 1: where scores are so large that another kernel's rounding of the same
-                    // score is far off this one's, the difference must not run away)
-                    const float e = ex2_approx((s[i] - st[i >> 1].x) * PA_SCALE) * st[i >> 1].y;
-                    if (key < lim[i >> 1]) acc[j][i & 1] += e > 1.0f ? 1.0f : e;
+                    // score is far off this one's, the difference must not run away; NaN stays NaN)
+                    e0 = min_nan(e0, 1.0f), e1 = min_nan(e1, 1.0f);
+                    if (OWN) {
+                        const int key = t0 + 8 * j + 2 * c;
+                        e0 = key < now.lim[half] ? e0 : 0.0f;
+                        e1 = key + 1 < now.lim[half] ? e1 : 0.0f;
+                    }
+                    sum2[j] = add_f2(sum2[j], f2_pack(e0, e1));
                 }
             }
+            if (rw.n > 16) now = next;
         }
+        float acc[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f2_unpack(sum2[j], acc[j][0], acc[j][1]);
         // the eight row lanes' sums, each lane keeping half of its keys at every exchange
         float x[2][2], y[2];
 #pragma unroll
@@ -720,8 +744,8 @@ int launch(PaArgs &a, const PaPlan &pl, const PtMaps &maps, uint8_t *ws, cudaStr
         if (!ks.weight || (own && a.score_floats)) continue;
         const int most = (ks.max_keys + PW_WARPS * PW_KEYS - 1) / (PW_WARPS * PW_KEYS);
         const long long fill = (PW_BLOCKS + (long long)a.n_kv * ks.n_set - 1) / ((long long)a.n_kv * ks.n_set);
-        if (int rc = launch_ex(k_prefix_weight, dim3(fill < most ? (unsigned)fill : most, a.n_kv, ks.n_set),
-                               32 * PW_WARPS, 0, 1, true, s, a, own))
+        if (int rc = launch_ex(own ? k_prefix_weight<true> : k_prefix_weight<false>, dim3(fill < most ? (unsigned)fill : most, a.n_kv, ks.n_set),
+                               32 * PW_WARPS, 0, 1, true, s, a))
             return rc;
     }
     return cudaGetLastError() == cudaSuccess ? WH_OK : WH_ECUDA;

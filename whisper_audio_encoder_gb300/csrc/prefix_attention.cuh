@@ -84,7 +84,12 @@ __device__ __forceinline__ void group_range(const PaArgs &p, int g, int &s, int 
 struct Rows {
     int seq0, n, hk;
     __device__ __forceinline__ void locate(const PaArgs &p, int r, int &qrow, int &head, int &qi) const {
-        const int per = p.nq * p.rep, s = r / per, w = r - s * per;
+        const int per = p.nq * p.rep;
+        if (per == 1) {   // (no division)
+            qi = 0, qrow = seq0 + r, head = hk;
+            return;
+        }
+        const int s = r / per, w = r - s * per;
         qi = w / p.rep;
         qrow = (seq0 + s) * p.nq + qi;
         head = hk * p.rep + (w - qi * p.rep);
