@@ -30,7 +30,7 @@ constexpr int PM_BATCH = 8;        // partial results that a merging thread load
 constexpr int PM_TEAMS = 8;        // teams of 16 threads in a merging block
 constexpr int PW_WARPS = 4;        // weight kernel: warps of a block
 constexpr int PW_KEYS = 32;        // weight kernel: keys of one warp step
-constexpr int PW_BLOCKS = 8 * 152; // weight kernel: blocks, twice what is resident (four an SM: 37.7 us, eight: 34.9)
+constexpr int PW_BLOCKS = 8 * 152; // weight kernel: blocks, twice what is resident (four an SM: 35.4 us, eight: 33.6)
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -446,9 +446,11 @@ __global__ void __launch_bounds__(16 * PM_TEAMS) k_prefix_merge(const PaArgs p) 
 
 // weight[t] += sum over the set's queries of 2^(s_t - m) / l: the scores again, with every row's final
 // maximum and sum.  A warp takes 32 keys at a time from a ring of two such steps and goes through the rows
-// 16 at a time; each sum has one fixed order.  Bound by the keys' bytes for few rows.  Reading the keys again
-// costs half of what the attention reads; keeping the scores would cost 8 bytes a (row, key) pair.  16 prefixes of
-// 211 .. 1500 keys, 83 rows, 20 heads: about 10 us for 34 MB of keys, most of them still in L2.
+// 16 at a time, the next 16 on their way meanwhile; each sum has one fixed order.  Bound by the keys' bytes for few
+// rows, by instructions for many (packed pairs; 102 rows x 4874 keys x 40 heads: 47 us with the attention, 66 with
+// single values and rows fetched when needed).  Reading the keys again costs half of what the attention reads; keeping
+// the scores would cost 8 bytes a (row, key) pair.  16 prefixes of 211 .. 1500 keys, 83 rows, 20 heads: 6 us behind
+// the attention for 34 MB of keys, most of them still in L2.
 template <bool OWN>
 __global__ void __launch_bounds__(32 * PW_WARPS, 4) k_prefix_weight(const PaArgs p) {
     __shared__ __align__(128) uint8_t rings[PW_WARPS][2 * PW_KEYS * 128];
