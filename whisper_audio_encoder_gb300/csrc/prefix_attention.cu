@@ -637,6 +637,8 @@ struct PaPlan {
 PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     PaPlan pl;
     const long long per = (long long)a.nq * a.rep, all = a.batch * per;
+    a.by_per = divisor((int)per);
+    a.by_rep = divisor(a.rep);
     const long long rows_a_set = a.pre.n_set > 0 ? (all + a.pre.n_set - 1) / a.pre.n_set : 0;
     const bool has_pre = a.pre.n_set > 0, has_own = a.own.n_set > 0;
     const auto slots = [&](int tile) {   // row tiles of a key head over all sets, with ragged groups at most

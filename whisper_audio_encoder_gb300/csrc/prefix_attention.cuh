@@ -10,6 +10,19 @@ namespace wh {
 // comes first, so that it is exact near the maximum however large the scores are.
 constexpr float PA_SCALE = 0.125f * 1.4426950408889634f;
 
+// n / d for 0 <= n < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d) with 2^l >= d is off by less than one
+// part in 2^31 of 1 / d, so the quotient is exact.
+struct Divisor {
+    uint32_t mul;
+    int shift;
+    __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
+};
+inline Divisor divisor(int d) {
+    int l = 0;
+    while ((1LL << l) < d) ++l;
+    return {(uint32_t)(((1ULL << (31 + l)) + d - 1) / d), 31 + l};
+}
+
 struct PaSet {
     const __nv_bfloat16 *k, *v;
     long long row_stride, set_stride;   // elements
@@ -25,6 +38,7 @@ struct PaArgs {
     long long q_stride;
     const int *group_start;   // device [pre.n_set + 1] or null: gsize sequences each
     int gsize, batch, nq, n_head, n_kv, rep;
+    Divisor by_per, by_rep;   // nq rep (rows of a sequence), rep
     int tile;                 // prefix: rows of a row tile
     int slots;                // prefix: row-tile slots of a key head over all groups
     int own_tiles;            // row tiles of a sequence
@@ -84,13 +98,8 @@ __device__ __forceinline__ void group_range(const PaArgs &p, int g, int &s, int 
 struct Rows {
     int seq0, n, hk;
     __device__ __forceinline__ void locate(const PaArgs &p, int r, int &qrow, int &head, int &qi) const {
-        const int per = p.nq * p.rep;
-        if (per == 1) {   // (no division)
-            qi = 0, qrow = seq0 + r, head = hk;
-            return;
-        }
-        const int s = r / per, w = r - s * per;
-        qi = w / p.rep;
+        const int s = p.by_per.of(r), w = r - s * p.nq * p.rep;
+        qi = p.by_rep.of(w);
         qrow = (seq0 + s) * p.nq + qi;
         head = hk * p.rep + (w - qi * p.rep);
     }
