@@ -115,21 +115,19 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
     // A work item is done by `wpi` neighbouring warps: all four for a prefix, p.own_wpi for own keys.
     const PaSet &ks = OWN ? p.own : p.pre;
     const int cluster = OWN ? p.own_cluster : p.pre_cluster;
-    const int wpi = OWN ? p.own_wpi : PA_WARPS, iw = warp & (wpi - 1);
+    const int wpi = OWN ? p.own_wpi : PA_WARPS, iw = warp & (wpi - 1), wlog = 31 - __clz(wpi), team = OWN ? warp >> wlog : 0;
     Rows rw;
     int set, split, r0, nk;
     if (OWN) {
-        long long x = (long long)blockIdx.x * (PA_WARPS / wpi) + warp / wpi;
+        int x = blockIdx.x * (PA_WARPS >> wlog) + team;
         if (x >= p.own_items) {
             pdl_wait();   // on every path: the kernel after this one counts on the one before it too
             return;
         }
-        split = x % ks.splits;
-        x /= ks.splits;
-        const int tile = x % p.own_tiles;
-        x /= p.own_tiles;
-        rw.hk = x % p.n_kv;
-        set = x / p.n_kv;
+        split = remainder(ks.by_splits, ks.splits, x);
+        const int tile = remainder(p.by_own_tiles, p.own_tiles, x);
+        rw.hk = remainder(p.by_kv, p.n_kv, x);
+        set = x;
         rw.seq0 = set;
         rw.n = p.nq * p.rep;
         r0 = tile * PA_TILE;
@@ -137,11 +135,10 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         nk = min(max(count, 0), ks.max_keys);
         if (count != nk && rw.hk == 0 && split == 0 && r0 == 0 && iw == 0 && lane == 0) set_status(p.ctl, WH_EBOUNDS);
     } else {
-        unsigned x = blockIdx.x;
-        split = x % ks.splits;
-        x /= ks.splits;
-        const int slot = x % p.slots;
-        rw.hk = x / p.slots;
+        int x = blockIdx.x;
+        split = remainder(ks.by_splits, ks.splits, x);
+        const int slot = remainder(p.by_slots, p.slots, x);
+        rw.hk = x;
         if (cluster && split == 0) finish_outside(p, slot, rw.hk);
         if (!find_tile(p, slot, rw.hk == 0 && split == 0, set, r0, rw, nk)) return;
     }
@@ -182,7 +179,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
             }
         }
     };
-    float *scores = reinterpret_cast<float *>(ring_all + PA_SMEM) + (warp / wpi) * p.score_floats;
+    float *scores = reinterpret_cast<float *>(ring_all + PA_SMEM) + team * p.score_floats;
     const int stride = wpi * PA_KEYS;
     int t0 = k0 + iw * PA_KEYS, half_ring = 0;
     fetch(t0, 0);
@@ -312,7 +309,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         for (int j = 0; j < 8; ++j)
             *reinterpret_cast<float2 *>(so(warp, r) + 8 * j + 2 * c) = make_float2(o[j][2 * half], o[j][2 * half + 1]);
     }
-    auto item_bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpi), "r"(32 * wpi) : "memory"); };
+    auto item_bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * wpi) : "memory"); };
     item_bar();
     if (OWN && p.after_pre) pdl_wait();   // the prefix's partial results are complete
     __shared__ float2 fin[PA_WARPS][PA_TILE];   // the block's maximum and sum; own weights: the row's maximum, 1 / sum
@@ -382,12 +379,12 @@ __global__ void __launch_bounds__(16 * PM_TEAMS) k_prefix_merge(const PaArgs p) 
     const long long rows = (long long)p.batch * p.nq * p.n_head;
     const int lane = threadIdx.x & 15, in_block = (threadIdx.x >> 4) % ROWS, team = (threadIdx.x >> 4) / ROWS;
     const long long mine = (long long)blockIdx.x * ROWS + in_block, row = min(mine, rows - 1);
-    const int b = (int)(row / ((long long)p.nq * p.n_head));
+    const int b = p.by_seq.of((int)row);
     // (the two teams of a warp may have rows of different sequences: one after the other)
     const int b0 = __shfl_sync(0xffffffffu, b, 0), b1 = __shfl_sync(0xffffffffu, b, 16);
     const int np0 = pre_parts_of(p, group_of(p, b0)), np1 = b1 == b0 ? np0 : pre_parts_of(p, group_of(p, b1));
     const int np = (threadIdx.x & 16) ? np1 : np0;
-    const int n = np + (p.own.n_set > 0 ? (clamp_count(p.own, b) + p.own.chunk - 1) / p.own.chunk : 0);
+    const int n = np + (p.own.n_set > 0 ? parts_of(p.own, b) : 0);
     const float2 *ml = p.part_ml + row * p.n_part;
     const float4 *po = reinterpret_cast<const float4 *>(p.part_o + row * p.n_part * 64) + lane;
     pdl_wait();   // the partial results; what came before only reads the call's inputs
@@ -625,6 +622,8 @@ void split_keys(PaSet &s, long long items, long long blocks, int step, long long
     }
     s.chunk = (int)(((s.max_keys + n - 1) / n + step - 1) / step * step);
     s.splits = (s.max_keys + s.chunk - 1) / s.chunk;
+    s.by_splits = divisor(s.splits);
+    s.by_chunk = divisor(s.chunk);
 }
 
 struct PaPlan {
@@ -639,6 +638,9 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     const long long per = (long long)a.nq * a.rep, all = a.batch * per;
     a.by_per = divisor((int)per);
     a.by_rep = divisor(a.rep);
+    a.by_seq = divisor(a.nq * a.n_head);
+    a.by_gsize = divisor(a.gsize);
+    a.by_kv = divisor(a.n_kv);
     const long long rows_a_set = a.pre.n_set > 0 ? (all + a.pre.n_set - 1) / a.pre.n_set : 0;
     const bool has_pre = a.pre.n_set > 0, has_own = a.own.n_set > 0;
     const auto slots = [&](int tile) {   // row tiles of a key head over all sets, with ragged groups at most
@@ -651,6 +653,11 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     a.tile = !pl.tc ? PA_TILE : rows_a_set > 64 ? 128 : rows_a_set > 32 ? 64 : 32;
     a.slots = has_pre ? (int)slots(a.tile) : 0;
     a.own_tiles = (int)((per + PA_TILE - 1) / PA_TILE);
+    a.tile_shift = a.tile == 128 ? 7 : a.tile == 64 ? 6 : a.tile == 32 ? 5 : 4;
+    a.group_tiles = (int)((a.gsize * per + a.tile - 1) / a.tile);
+    a.by_group_tiles = divisor(a.group_tiles);
+    a.by_slots = divisor(a.slots);
+    a.by_own_tiles = divisor(a.own_tiles);
     const auto ranges = [](const PaSet &s, int least) { return ((long long)s.max_keys + least - 1) / least; };
     constexpr int STEP = PA_WARPS * PA_SLOT_KEYS;
     // (with ragged groups the slots are more than the tiles that there will be, by half a tile a set on average)
@@ -720,13 +727,14 @@ bool shape_ok(int batch, int n_query, int n_head, int n_kv) {
 }
 
 int launch(PaArgs &a, const PaPlan &pl, const PtMaps &maps, uint8_t *ws, cudaStream_t s) {
+    a.by_pre_tiles = divisor((int)((long long)a.slots * a.n_kv > 0x7fffffffLL ? 1 : a.slots * a.n_kv));
     a.part_o = reinterpret_cast<float *>(ws + pl.part_o);
     a.part_ml = reinterpret_cast<float2 *>(ws + pl.part_ml);
     a.stats = pl.total > pl.stats ? reinterpret_cast<float2 *>(ws + pl.stats) : nullptr;
     const long long pre_blocks = (long long)a.slots * a.n_kv * a.pre.splits;
     const long long own_blocks = (a.own_items * a.own_wpi + PA_WARPS - 1) / PA_WARPS;
     const long long rows = (long long)a.batch * a.nq * a.n_head;
-    if (pre_blocks > 0x7fffffffLL || own_blocks > 0x7fffffffLL) return WH_EINVAL;
+    if (pre_blocks > 0x7fffffffLL || a.own_items > 0x7ffffff0LL) return WH_EINVAL;
     if (pre_blocks > 0) {
         if (int rc = pl.tc ? prefix_tc_launch(a, maps, s)
                            : launch_ex(k_prefix_attention<false>, dim3((unsigned)pre_blocks), PA_THREADS, PA_SMEM,

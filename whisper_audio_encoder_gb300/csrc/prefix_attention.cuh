@@ -10,17 +10,23 @@ namespace wh {
 // comes first, so that it is exact near the maximum however large the scores are.
 constexpr float PA_SCALE = 0.125f * 1.4426950408889634f;
 
-// n / d for 0 <= n < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d) with 2^l >= d is off by less than one
-// part in 2^31 of 1 / d, so the quotient is exact.
+// n / d for 0 <= n < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d) with 2^(l - 1) < d <= 2^l.  mul / 2^(31 + l)
+// exceeds 1 / d by less than 2^-(31 + l), so n times it exceeds n / d by less than 2^-l <= 1 / d: the same integer part.
 struct Divisor {
     uint32_t mul;
     int shift;
     __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
 };
-inline Divisor divisor(int d) {
-    int l = 0;
-    while ((1LL << l) < d) ++l;
+inline Divisor divisor(int d) {   // (0, where there is nothing to divide, as 1)
+    const int l = d > 1 ? 32 - __builtin_clz((unsigned)d - 1u) : 0;
+    d = d < 1 ? 1 : d;
     return {(uint32_t)(((1ULL << (31 + l)) + d - 1) / d), 31 + l};
+}
+// x mod d; x becomes x / d.
+__device__ __forceinline__ int remainder(const Divisor &by, int d, int &x) {
+    const int q = by.of(x), r = x - q * d;
+    x = q;
+    return r;
 }
 
 struct PaSet {
@@ -30,6 +36,7 @@ struct PaSet {
     float *weight;                      // device [n_set][n_kv][max_keys] or null
     int n_set, max_keys;
     int splits, chunk;                  // key ranges of one set and keys of a range
+    Divisor by_splits, by_chunk;
 };
 
 struct PaArgs {
@@ -38,8 +45,10 @@ struct PaArgs {
     long long q_stride;
     const int *group_start;   // device [pre.n_set + 1] or null: gsize sequences each
     int gsize, batch, nq, n_head, n_kv, rep;
-    Divisor by_per, by_rep;   // nq rep (rows of a sequence), rep
-    int tile;                 // prefix: rows of a row tile
+    Divisor by_per, by_rep, by_seq;   // nq rep (rows of a sequence), rep, nq n_head
+    Divisor by_gsize, by_group_tiles, by_slots, by_pre_tiles, by_own_tiles, by_kv;
+    int tile, tile_shift;     // prefix: rows of a row tile, a power of two
+    int group_tiles;          // row tiles of a group, without group_start
     int slots;                // prefix: row-tile slots of a key head over all groups
     int own_tiles;            // row tiles of a sequence
     int own_wpi;              // own keys: warps of a work item
@@ -63,8 +72,8 @@ __device__ __forceinline__ int clamp_count(const PaSet &s, int set) {
     return s.n_keys ? min(max(__ldg(s.n_keys + set), 0), s.max_keys) : s.max_keys;
 }
 
-// Largest g in [0, n) with start[g] * mul / div + g * add <= x, by the whole warp, 32 probes at a time.
-__device__ __forceinline__ int warp_search(const int *start, int n, int mul, int div, int add, long long x) {
+// Largest g in [0, n) with start[g] * mul / 2^shift + g * add <= x, by the whole warp, 32 probes at a time.
+__device__ __forceinline__ int warp_search(const int *start, int n, int mul, int shift, int add, long long x) {
     int lo = 0, len = n;
     const int lane = threadIdx.x & 31;
     while (len > 1) {
@@ -72,7 +81,7 @@ __device__ __forceinline__ int warp_search(const int *start, int n, int mul, int
         bool le = false;
         if (i < len) {
             const int g = lo + i;
-            le = (long long)__ldg(start + g) * mul / div + (long long)g * add <= x;
+            le = ((long long)__ldg(start + g) * mul >> shift) + (long long)g * add <= x;
         }
         const uint32_t m = __ballot_sync(0xffffffffu, le) | 1u;
         const int top = (31 - __clz(m)) * step;
@@ -108,15 +117,16 @@ struct Rows {
 // The prefix set of sequence b, or -1.  Whole warp, one b.
 __device__ __forceinline__ int group_of(const PaArgs &p, int b) {
     if (p.pre.n_set <= 0) return -1;
-    if (!p.group_start) return b / p.gsize;
-    const int g = warp_search(p.group_start, p.pre.n_set, 1, 1, 0, b);
+    if (!p.group_start) return p.by_gsize.of(b);
+    const int g = warp_search(p.group_start, p.pre.n_set, 1, 0, 0, b);
     int s, e;
     group_range(p, g, s, e);
     return b >= s && b < e ? g : -1;
 }
 // Partial results that the prefix blocks leave for a sequence of set g.
+__device__ __forceinline__ int parts_of(const PaSet &s, int set) { return s.by_chunk.of(clamp_count(s, set) + s.chunk - 1); }
 __device__ __forceinline__ int pre_parts_of(const PaArgs &p, int g) {
-    return g < 0 ? 0 : (clamp_count(p.pre, g) + p.pre.chunk - 1) / p.pre.chunk;
+    return g < 0 ? 0 : parts_of(p.pre, g);
 }
 
 // Prefix work of one block: its group, the rows r0 .. of that group's tile, the group's key count (clamped), false
@@ -131,7 +141,7 @@ __device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report
         const int g = min(lane, p.pre.n_set - 1);
         const int a = __ldg(p.group_start + g), b = __ldg(p.group_start + g + 1);
         const int c = p.pre.n_keys ? __ldg(p.pre.n_keys + g) : p.pre.max_keys;
-        const bool le = lane < p.pre.n_set && (long long)a * per / p.tile + g <= slot;
+        const bool le = lane < p.pre.n_set && ((long long)a * per >> p.tile_shift) + g <= slot;
         set = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
         const bool bad = __any_sync(0xffffffffu, lane == slot && lane < p.pre.n_set && (a < 0 || b < a || b > p.batch));
         if (report && bad && threadIdx.x == 0) set_status(p.ctl, WH_EBOUNDS);
@@ -144,15 +154,14 @@ __device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report
                 const int a = __ldg(p.group_start + slot), b = __ldg(p.group_start + slot + 1);
                 if (a < 0 || b < a || b > p.batch) set_status(p.ctl, WH_EBOUNDS);
             }
-            set = warp_search(p.group_start, p.pre.n_set, per, p.tile, 1, slot);
+            set = warp_search(p.group_start, p.pre.n_set, per, p.tile_shift, 1, slot);
         } else {
-            set = slot / ((p.gsize * per + p.tile - 1) / p.tile);
+            set = p.by_group_tiles.of(slot);
         }
         count = p.pre.n_keys ? __ldg(p.pre.n_keys + set) : p.pre.max_keys;
         group_range(p, set, s, e);
     }
-    r0 = p.group_start ? (slot - (int)((long long)s * per / p.tile) - set) * p.tile
-                       : (slot - set * ((p.gsize * per + p.tile - 1) / p.tile)) * p.tile;
+    r0 = (slot - (p.group_start ? (int)((long long)s * per >> p.tile_shift) + set : set * p.group_tiles)) * p.tile;
     rw.seq0 = s;
     rw.n = (e - s) * per;
     nk = min(max(count, 0), p.pre.max_keys);

@@ -77,15 +77,20 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
     // a cluster's blocks are the ranges of one item; else neighbours are tiles and heads, which read the same
     // rows or the same DRAM pages at about the same time
     const int cluster = p.pre_cluster;
-    const unsigned tiles = p.slots * p.n_kv;
-    const int split = cluster > 1 ? blockIdx.x % cluster : blockIdx.x / tiles;
-    const unsigned item = cluster > 1 ? blockIdx.x / cluster : blockIdx.x % tiles;
-    const int slot = item % p.slots;
-    rw.hk = item / p.slots;
+    int x = blockIdx.x, item, split;
+    if (cluster > 1) {
+        split = remainder(p.pre.by_splits, p.pre.splits, x);
+        item = x;
+    } else {
+        item = remainder(p.by_pre_tiles, p.slots * p.n_kv, x);
+        split = x;
+    }
+    const int slot = remainder(p.by_slots, p.slots, item);
+    rw.hk = item;
     if (!p.group_start) {
         // the first step's rows (below max_keys: the cache's own, what they hold is not looked at) are on their way
         // to L2 before the inputs may be read: 1 us of 35 at 32 rows x 20 heads x 30000 keys
-        set = slot / ((p.gsize * p.nq * p.rep + TILE - 1) / TILE);
+        set = p.by_group_tiles.of(slot);
         const int t = split * p.pre.chunk + (threadIdx.x & 127);
         if (t < p.pre.max_keys)
             prefetch_l2((threadIdx.x >= 128 ? p.pre.v : p.pre.k) + (long long)set * p.pre.set_stride +
