@@ -62,6 +62,7 @@ struct EvArgs {
     int *kept;                 // [n_set][n_head][budget]: source index of every key that stays
     int *count;                // [n_set]: keys before, as clamped
     int max_keys, out_keys, n_set, n_head, budget, recent, in_place;
+    Divisor by_row;            // 16-byte pieces of a row
     int *status;
 };
 
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS, CTAS == 1 ? 0
     const int tid = team.thread();
     const long long sh = CHOOSERS == 32 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x / CTAS;
     if (sh >= (long long)p.n_set * p.n_head) return;
-    const int set = (int)(sh / p.n_head), h = (int)(sh % p.n_head);
+    const int set = (int)sh / p.n_head, h = (int)sh - set * p.n_head;
     const int n = count_of(p, set, h == 0 && tid == 0);
     if (h == 0 && tid == 0) p.count[set] = n;
     const float *w = p.weight + sh * p.max_keys;
@@ -494,23 +495,24 @@ __global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS, CTAS == 1 ? 0
     }
 }
 
-// Row j of head h of a set <- row kept[j] of the cache, for keys and values; other buffers.
+// Row j of head h of a set <- row kept[j] of the cache, for keys and values; other buffers.  I counts 16-byte pieces.
+template <class I>
 __global__ void __launch_bounds__(MV_THREADS) k_evict_move(const EvArgs p) {
     pdl_wait();
     const int set = blockIdx.y, n = min(__ldcg(p.count + set), p.budget);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.n_out[set] = n;
     const int per_row = p.n_head * 8;   // 16-byte pieces of a row
-    const long long todo = (long long)n * per_row, base = (long long)blockIdx.x * MV_PIECES + threadIdx.x;
+    const I todo = (I)n * per_row, base = (I)blockIdx.x * MV_PIECES + threadIdx.x;
     constexpr int U = MV_PIECES / MV_THREADS;
     int x[U], j[U], t[U];
     uint4 a[U], b[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const long long i = base + u * MV_THREADS;
+        const I i = base + u * MV_THREADS;
         t[u] = -1;
         if (i < todo) {
-            j[u] = (int)(i / per_row);
-            x[u] = (int)(i - (long long)j[u] * per_row);
+            j[u] = sizeof(I) == 4 ? p.by_row.of((int)i) : (int)(i / per_row);
+            x[u] = (int)(i - (I)j[u] * per_row);
             t[u] = __ldcg(p.kept + ((long long)set * p.n_head + (x[u] >> 3)) * p.budget + j[u]);
         }
     }
@@ -693,6 +695,7 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
     a.budget = budget;
     a.recent = recent;
     a.in_place = out == nullptr;
+    a.by_row = divisor(n_kv_head * 8);
     a.status = ctl.status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int most = budget < a.max_keys ? budget : a.max_keys;
@@ -732,10 +735,13 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
             rc = launch_ex(k_evict_select<256, 32, SEL_CTAS>, dim3((unsigned)(items * SEL_CTAS)), 256, 0, SEL_CTAS, true, s, a);
         else
             rc = launch_ex(k_evict_select<SEL_THREADS, 0>, blocks, SEL_THREADS, 0, 1, true, s, a);
-        if (!rc)
-            rc = a.in_place ? launch_shift(a, most, items, s)
-                            : launch_ex(k_evict_move, dim3((unsigned)(((long long)most * n_kv_head * 8 + MV_PIECES - 1) / MV_PIECES), a.n_set),
-                                        MV_THREADS, 0, 1, true, s, a);
+        if (!rc && a.in_place) {
+            rc = launch_shift(a, most, items, s);
+        } else if (!rc) {
+            const long long pieces = (long long)most * n_kv_head * 8;
+            rc = launch_ex(pieces > 0x7fff0000LL ? k_evict_move<long long> : k_evict_move<int>,
+                           dim3((unsigned)((pieces + MV_PIECES - 1) / MV_PIECES), a.n_set), MV_THREADS, 0, 1, true, s, a);
+        }
     }
     const double held = (double)a.n_set * n_kv_head;
     trace_end(TR_DEC_OTHER, s, 0.0, held * (4.0 * a.max_keys + 520.0 * most));

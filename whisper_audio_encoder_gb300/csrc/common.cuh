@@ -37,6 +37,25 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// n / d for 0 <= n < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d) with 2^(l - 1) < d <= 2^l.  mul / 2^(31 + l)
+// exceeds 1 / d by less than 2^-(31 + l), so n times it exceeds n / d by less than 2^-l <= 1 / d: the same integer part.
+struct Divisor {
+    uint32_t mul;
+    int shift;
+    __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
+};
+inline Divisor divisor(int d) {   // (0, where there is nothing to divide, as 1)
+    const int l = d > 1 ? 32 - __builtin_clz((unsigned)d - 1u) : 0;
+    d = d < 1 ? 1 : d;
+    return {(uint32_t)(((1ULL << (31 + l)) + d - 1) / d), 31 + l};
+}
+// x mod d; x becomes x / d.
+__device__ __forceinline__ int remainder(const Divisor &by, int d, int &x) {
+    const int q = by.of(x), r = x - q * d;
+    x = q;
+    return r;
+}
+
 // Brings the line at p into L2 (and its translation into the TLBs); nothing waits for it.
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 

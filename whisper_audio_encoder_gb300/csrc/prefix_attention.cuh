@@ -10,25 +10,6 @@ namespace wh {
 // comes first, so that it is exact near the maximum however large the scores are.
 constexpr float PA_SCALE = 0.125f * 1.4426950408889634f;
 
-// n / d for 0 <= n < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d) with 2^(l - 1) < d <= 2^l.  mul / 2^(31 + l)
-// exceeds 1 / d by less than 2^-(31 + l), so n times it exceeds n / d by less than 2^-l <= 1 / d: the same integer part.
-struct Divisor {
-    uint32_t mul;
-    int shift;
-    __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
-};
-inline Divisor divisor(int d) {   // (0, where there is nothing to divide, as 1)
-    const int l = d > 1 ? 32 - __builtin_clz((unsigned)d - 1u) : 0;
-    d = d < 1 ? 1 : d;
-    return {(uint32_t)(((1ULL << (31 + l)) + d - 1) / d), 31 + l};
-}
-// x mod d; x becomes x / d.
-__device__ __forceinline__ int remainder(const Divisor &by, int d, int &x) {
-    const int q = by.of(x), r = x - q * d;
-    x = q;
-    return r;
-}
-
 struct PaSet {
     const __nv_bfloat16 *k, *v;
     long long row_stride, set_stride;   // elements
