@@ -103,8 +103,8 @@ __device__ __forceinline__ void score8(const uint32_t (&a)[4][4], const uint4 &k
 // and values in flight by cp.async (96 KB an SM with three blocks of four warps), and the products run on
 // mma.sync because 16 rows would leave 7/8 of a tcgen05 tile empty, while 606 TFLOP/s of mma.sync are four times
 // what 16 rows need at the full HBM rate.  Steps of 32 keys: the maximum's shuffles and the rescaling vote are
-// paid once for two products.  16 prefixes x 5 rows x 20 heads x 1500 keys: 23.5 us, 123 MB, 5.2 TB/s, 78 % of
-// the copy rate; 256 sequences' 448 own keys x 20 heads: 91 us, 587 MB, 95 %.
+// paid once for two products.  16 prefixes x 5 rows x 20 heads x 1500 keys: 23 us, 123 MB, 5.3 TB/s, 79 % of
+// the copy rate; 256 sequences' 448 own keys x 20 heads: 87 us a call, 587 MB, 99 %.
 template <bool OWN>
 __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -579,14 +579,14 @@ constexpr long long PT_BLOCKS = 2 * 152;   // k_prefix_tc: 2 on each
 // least PT_MIN_WORK products of a 16-row tile with a key (k_prefix_attention's units) to do: below that its
 // blocks' longer set-up (TMEM, tensor maps) does not pay.  Measured, us a call, 20 key heads:
 //   rows x keys x sets   products   k_prefix_attention   k_prefix_tc
-//    40 x  400 x  1         24 k          10.3              12.3
-//   128 x 1500 x  1        240 k          15.7              17.7
-//    40 x 1500 x  4        360 k          18.4              17.7
-//    64 x 1500 x  4        480 k          21.7              18.5
-//    40 x 8000 x  1        480 k          22.6              20.9
-//   128 x 1500 x 16        3.8 M          97                47
+//    40 x  400 x  1         24 k           9.3              10.9
+//   128 x 1500 x  1        240 k          16.4              17.7
+//    40 x 1500 x  4        360 k          18.4              18.1
+//    64 x 1500 x  4        480 k          20.6              18.1
+//    40 x 8000 x  1        480 k          22.6              20.3
+//   128 x 1500 x 16        3.8 M          96                45
 // Beside own keys, whose blocks hide the set-up, more than twice PT_MIN_ROWS rows are enough: 200 rows x 400
-// keys, 8 heads, with up to 224 own keys 22.3 and 20.0.
+// keys, 8 heads, with up to 224 own keys 20.5 and 18.7.
 constexpr int PT_MIN_ROWS = 16;
 constexpr long long PT_MIN_WORK = 300000;
 // Ranges of at least PT_LEAST keys (rounded down): a shorter block does not make up for joining one range more.
@@ -649,7 +649,7 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     const bool much = slots(PA_TILE) * a.n_kv * a.pre.max_keys >= PT_MIN_WORK;
     pl.tc = may_tc && rows_a_set > PT_MIN_ROWS && (much || (has_own && rows_a_set > 2 * PT_MIN_ROWS));
     // the smallest tile that holds an average group (us a call with tiles of 32, 64, 128 rows, 4 prefixes of 1500
-    // keys: 20 rows 16.3, 16.4, 17.3; 40 rows 19.4, 18.4, 18.5; 100 rows 31.9, 22.6, 22.5)
+    // keys: 20 rows 16.4, 16.5, 16.6; 40 rows 18.9, 18.1, 18.5; 100 rows 30.8, 22.1, 20.7)
     a.tile = !pl.tc ? PA_TILE : rows_a_set > 64 ? 128 : rows_a_set > 32 ? 64 : 32;
     a.slots = has_pre ? (int)slots(a.tile) : 0;
     a.own_tiles = (int)((per + PA_TILE - 1) / PA_TILE);
@@ -667,8 +667,8 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     else
         split_keys(a.pre, (long long)a.slots * a.n_kv, PA_BLOCKS, STEP, ranges(a.pre, has_own ? PA_LEAST_BESIDE : STEP));
     // own keys: one warp an item when that fills the device, more warps, then key ranges, when it does not (us a
-    // call with one, two, four warps: 16 sequences x 20 heads x 448 keys 17.3, 14.2, 12.3; 80 sequences 35.0,
-    // 35.0, 41.2; 256 sequences x 64 keys 24.6, -, 49.0)
+    // call with one, two, four warps: 16 sequences x 20 heads x 448 keys 16.5, 13.0, 12.3; 80 sequences 33.8,
+    // 34.9, 39.0; 256 sequences x 64 keys 23.2, 28.2, 41.0)
     // (warps without keys still finish rows beside a prefix: 2 sequences x 16 queries x 1500 keys and 17 own, 20 heads 12.0
     // us with four warps, 16.4 with one)
     const long long items = (long long)a.own.n_set * a.n_kv * a.own_tiles;
