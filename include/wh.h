@@ -319,8 +319,7 @@ int wh_decode_attention(const wh_bf16 *q, const wh_bf16 *k, const wh_bf16 *v, in
  * not NULL.  A query that sees no key gives zeros.  Keys at and past a set's count are not used, whatever
  * they hold.  Keys and values that are used must be finite (an infinity there gives NaN).
  * Precision: products of bf16 operands summed in fp32, softmax statistics and weights in fp32; in the
- * product with the values the softmax weights have 16 bits of mantissa where a prefix has at most 16
- * rows (queries x query heads of a key head) on average, 8 where it has more.
+ * product with the values the softmax weights have 16 bits of mantissa, whatever the kernel.
  *   out     device bf16 [batch * n_query][64 n_head]; may not alias the inputs
  *   prefix or own may be NULL (not both).
  *   workspace >= wh_prefix_attention_workspace(batch, n_query, n_head, n_kv_head, prefix sets or 0,

@@ -3,14 +3,16 @@
 // A block takes up to 128 rows (queries of a group's sequences and of a key head's query heads) and a range
 // of the prefix's keys, in steps of 128 keys:
 //   S = Q K^T      tcgen05.mma M = 128, N = 128, K = 64 into TMEM, Q and the TMA-loaded K in shared memory
-//   P = 2^(S - m)  one row a thread: read from TMEM, running maximum and sum, bf16 pairs back into TMEM
-//   O += P V       tcgen05.mma M = 128, N = 64, K = 128, P from TMEM, V as loaded (MN-major), O in TMEM
+//   P = 2^(S - m)  one row a thread: read from TMEM, running maximum and sum, back into TMEM
+//   O += P V       tcgen05.mma M = 128, N = 64, K = 64 twice, P from TMEM, V as loaded (MN-major), O in TMEM
 // With 32 or 64 rows the matrix product's 128 lanes hold 4 or 2 copies of them, each taking a quarter or
 // half of the keys' columns (its P is zero elsewhere): the exponentials, not the padded products, are what
 // takes time, and so none is spent on padding.  The copies are merged at the end like key ranges.
 // O is rescaled only when a row's maximum has grown by more than 2^8.
-// P is rounded to bf16 because both operands of the product have one type: half a step is 2^-9 of a weight
-// or less, as much as the output's own rounding, and averages out over the keys.
+// Both operands of the product have one type, bf16, whose half step is up to 2^-8 of a weight.  So P goes in as the
+// sum of two bf16, 16 bits of mantissa (half a step: 2^-16), like k_prefix_attention's: a query's precision does not
+// depend on how many share its keys.  The two take the columns of 128 keys, so a step's keys go in two halves: the
+// second half's exponentials run beside the first half's products.
 //
 // Warp 0 loads (TMA), warp 1 issues the products (2 and 3 idle), warps 4 .. 7 are the rows' (warp w reads the
 // TMEM lanes 32 (w % 4) and up).  Two blocks are resident on an SM, so one's softmax runs beside the other's products.
@@ -35,7 +37,7 @@ constexpr int TILE_BYTES = 128 * 128;                       // 128 rows of 64 bf
 constexpr int OFF_RING = TILE_BYTES;                        // Q first
 constexpr int OFF_BARS = OFF_RING + PT_STAGES * 2 * TILE_BYTES;
 constexpr int PT_SMEM = OFF_BARS + 1024;                    // two blocks fill an SM's shared memory
-constexpr uint32_t PT_COLS = 256;                           // S [0, 128), O [128, 192), P [192, 256)
+constexpr uint32_t PT_COLS = 256;   // S [0, 128), O [128, 192), P of 64 keys: high parts [192, 224), low parts [224, 256)
 constexpr int SO_ROW = 68;                                  // floats a row of the epilogue's staging
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -54,11 +56,19 @@ __device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr) {
     d |= (uint64_t)2 << 61;
     return d;
 }
+// (by the array's size, for the columns of a thread)
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) { tmem_st8(taddr, r); }
 __device__ __forceinline__ void rows_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 template <int COPIES>
 __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_constant__ PtMaps tm, const PaArgs p) {
-    constexpr int TILE = 128 / COPIES, COLS = 128 / COPIES;   // rows of the block, columns a thread takes
+    constexpr int TILE = 128 / COPIES;          // rows of the block
+    constexpr int HALF = 64 / COPIES;           // columns that a thread takes of each 64 keys
+    constexpr int W = HALF < 32 ? HALF : 32;    // columns of one TMEM access
+    constexpr int BLOCKS = HALF / W;            // and accesses of a half
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *sQ = smem, *sKV = smem + OFF_RING;   // stage s: K at s * 32 KB, V 16 KB behind it
     uint64_t *kv_full = reinterpret_cast<uint64_t *>(smem + OFF_BARS);
@@ -226,15 +236,20 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
                     tc_fence_after();
                     issue_s((j + 1) % PT_STAGES);
                 }
-                ok = !*abort_flag && mbar_wait(p_full, j & 1u, p.ctl);
-                if (!ok) break;
-                tc_fence_after();
                 const uint32_t vb = skv + (j % PT_STAGES) * 2 * TILE_BYTES + TILE_BYTES;
+                for (int h = 0; h < 2; ++h) {   // the halves are phases 2j and 2j + 1 of p_full and o_full
+                    ok = !*abort_flag && mbar_wait(p_full, h, p.ctl);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < PT_KEYS / 16; ++kk)
-                    umma_bf16_tmem_a(tmem + 128u, tmem + 192u + 8u * kk, sdesc_sw128_mn(vb + kk * 2048), IDESC_O,
-                                     (j | kk) != 0);
-                umma_commit(o_full);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t vd = sdesc_sw128_mn(vb + (4 * h + kk) * 2048);
+                        umma_bf16_tmem_a(tmem + 128u, tmem + 192u + 8u * kk, vd, IDESC_O, (j | h | kk) != 0);
+                        umma_bf16_tmem_a(tmem + 128u, tmem + 224u + 8u * kk, vd, IDESC_O, 1u);
+                    }
+                    umma_commit(o_full);
+                }
+                if (!ok) break;
                 umma_commit(kv_empty + j % PT_STAGES);
             }
             if (!ok) *abort_flag = 1;
@@ -249,7 +264,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
       }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HIGH));
-        const int col0 = (a / TILE) * COLS;   // the columns of this copy
+        const int col0 = (a / TILE) * HALF;   // the columns of this copy in every 64
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + (uint32_t)col0, tO = tmem + lanes + 128u, tP = tmem + lanes + 192u;
         if (COPIES > 1) {   // the other copies' columns of P stay zero
@@ -264,9 +279,11 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
             ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(s_full, j & 1u, p.ctl));
             if (!ok) break;
             tc_fence_after();
-            uint32_t sv[COLS / 32][32];
+            uint32_t sv[2][BLOCKS][W];   // scores of keys 64 h + col0 + W i + k of the step
 #pragma unroll
-            for (int i = 0; i < COLS / 32; ++i) tmem_ld32(tS + 32u * i, sv[i]);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < BLOCKS; ++i) tmem_ld(tS + 64u * h + (uint32_t)(W * i), sv[h][i]);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
@@ -274,10 +291,11 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
             const int valid = k1 - k0 - j * PT_KEYS;   // keys of this step inside the range
             if (valid < PT_KEYS) {
 #pragma unroll
-                for (int i = 0; i < COLS / 32; ++i)
+                for (int i = 0; i < 2 * BLOCKS; ++i)
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (col0 + 32 * i + k >= valid) sv[i][k] = 0xff800000u;   // -inf
+                    for (int k = 0; k < W; ++k)
+                        if (64 * (i / BLOCKS) + col0 + W * (i % BLOCKS) + k >= valid)
+                            sv[i / BLOCKS][i % BLOCKS][k] = 0xff800000u;   // -inf
                 // values past the range may be anything, NaN too, and 0 * NaN is NaN: clear them
                 ok = __all_sync(0xffffffffu, mbar_wait(kv_full + j % PT_STAGES, (j / PT_STAGES) & 1u, p.ctl));
                 if (!ok) break;
@@ -292,16 +310,18 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
 #pragma unroll
             for (int k = 0; k < 4; ++k) pm[k] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < COLS / 32; ++i)
+            for (int i = 0; i < 2 * BLOCKS; ++i)
 #pragma unroll
-                for (int k = 0; k < 32; k += 2)
-                    pm[(k >> 1) & 3] = max3(pm[(k >> 1) & 3], __uint_as_float(sv[i][k]), __uint_as_float(sv[i][k + 1]));
+                for (int k = 0; k < W; k += 2) {
+                    const uint32_t *x = sv[i / BLOCKS][i % BLOCKS] + k;
+                    pm[(k >> 1) & 3] = max3(pm[(k >> 1) & 3], __uint_as_float(x[0]), __uint_as_float(x[1]));
+                }
             const float m_new = fmaxf(m, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));
             if (j == 0) {
                 m = m_new;
             } else {
-                // the product of the step before is done: O is stable and P may be overwritten
-                ok = __all_sync(0xffffffffu, mbar_wait(o_full, (j - 1) & 1u, p.ctl));
+                // the products of the step before are done: O is stable and P may be overwritten
+                ok = __all_sync(0xffffffffu, mbar_wait(o_full, 1u, p.ctl));
                 if (!ok) break;
                 tc_fence_after();
                 const bool need = (m_new - m) * PA_SCALE > 8.0f;
@@ -328,28 +348,42 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
             const uint64_t scale2 = f2_pack(PA_SCALE, PA_SCALE), minus2 = f2_pack(-ms, -ms);
             uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-            for (int i = 0; i < COLS / 32; ++i) {
-                uint32_t pk[16];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t hi[BLOCKS][W / 2], lo[BLOCKS][W / 2];   // the weights as a sum of two bf16 each
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    float x0, x1;
-                    f2_unpack(mul_f2(add_f2(f2_pack(__uint_as_float(sv[i][2 * k]), __uint_as_float(sv[i][2 * k + 1])), minus2), scale2),
-                              x0, x1);
-                    const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-                    sum2[k & 1] = add_f2(sum2[k & 1], f2_pack(e0, e1));
-                    pk[k] = pack_bf16(e0, e1);
+                for (int i = 0; i < BLOCKS; ++i)
+#pragma unroll
+                    for (int k = 0; k < W / 2; ++k) {
+                        const uint32_t *x = sv[h][i] + 2 * k;
+                        float x0, x1;
+                        f2_unpack(mul_f2(add_f2(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), minus2), scale2), x0, x1);
+                        const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+                        sum2[k & 1] = add_f2(sum2[k & 1], f2_pack(e0, e1));
+                        const uint32_t top = pack_bf16(e0, e1);
+                        hi[i][k] = top;
+                        lo[i][k] = pack_bf16(e0 - __uint_as_float(top << 16), e1 - __uint_as_float(top & 0xffff0000u));
+                    }
+                if (h == 1) {   // the first half's products are done with P
+                    ok = __all_sync(0xffffffffu, mbar_wait(o_full, 0u, p.ctl));
+                    if (!ok) break;
+                    tc_fence_after();
                 }
-                tmem_st16(tP + (uint32_t)(col0 / 2 + 16 * i), pk);
+#pragma unroll
+                for (int i = 0; i < BLOCKS; ++i) {
+                    tmem_st(tP + (uint32_t)(col0 / 2 + W / 2 * i), hi[i]);
+                    tmem_st(tP + 32u + (uint32_t)(col0 / 2 + W / 2 * i), lo[i]);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
             }
+            if (!ok) break;
             float x0, x1;
             f2_unpack(add_f2(sum2[0], sum2[1]), x0, x1);
             l += x0 + x1;
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
         }
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full, (nt - 1) & 1u, p.ctl));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full, 1u, p.ctl));
         if (!ok) *abort_flag = 1;
         tc_fence_after();
         // every product is done, so the ring is free: stage O, merge the copies, then the ranges
