@@ -345,6 +345,22 @@ typedef struct {
 enum { WH_GROUP_TABLE = 1, WH_PREFIX_WEIGHT = 2, WH_OWN_WEIGHT = 4 };
 size_t wh_prefix_attention_workspace(int batch, int n_query, int n_head, int n_kv_head, int n_prefix,
                                      int max_prefix, int max_own, int needs);
+/* What a call of these sizes (as for the workspace) runs; no device is needed.  Where the tcgen05 kernel is named,
+ * keys whose strides no tensor map can hold take 16 rows a block instead.  WH_EINVAL: no such call. */
+typedef struct {
+    int prefix_rows;       /* rows of a prefix block: 16 (mma.sync), 32, 64 or 128 (tcgen05); 0: no prefix */
+    int prefix_ranges;     /* key ranges of a prefix set, a block each */
+    int prefix_cluster;    /* how they are joined: by clusters of so many blocks, 1: one range finishes its rows,
+                              0: partial results */
+    int own_warps;         /* warps of a sequence's key head; 0: no own keys */
+    int own_ranges;
+    int own_cluster;       /* as prefix_cluster */
+    int own_scores_kept;   /* the own keys' weights come from scores kept on chip */
+    int merge;             /* a kernel of its own joins partial results (else the own keys' blocks do) */
+    int launches;
+} wh_prefix_plan;
+int wh_prefix_attention_plan(int batch, int n_query, int n_head, int n_kv_head, int n_prefix, int max_prefix,
+                             int max_own, int needs, wh_prefix_plan *plan);
 int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch, int n_query, int n_head, int n_kv_head,
                         const wh_keys *prefix, const int *group_start, const wh_keys *own, wh_bf16 *out,
                         void *workspace, size_t ws_bytes, void *stream);

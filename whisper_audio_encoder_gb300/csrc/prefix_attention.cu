@@ -779,12 +779,12 @@ int prefix_attention_prepare() {
 
 using namespace wh;
 
-extern "C" size_t wh_prefix_attention_workspace(int batch, int n_query, int n_head, int n_kv_head, int n_prefix,
-                                                int max_prefix, int max_own, int needs) {
+// The sizes of a call as plan() takes them; false: no such call.
+static bool sizes_of(int batch, int n_query, int n_head, int n_kv_head, int n_prefix, int max_prefix, int max_own, int needs,
+                     PaArgs &a) {
     if (!shape_ok(batch, n_query, n_head, n_kv_head) || batch == 0 || n_prefix < 0 || n_prefix > 65535 ||
         max_prefix < 0 || max_prefix > (1 << 30) || max_own < 0 || max_own > (1 << 30) || (needs & ~7))
-        return 0;
-    PaArgs a = {};
+        return false;
     a.batch = batch;
     a.nq = n_query;
     a.n_head = n_head;
@@ -795,15 +795,47 @@ extern "C" size_t wh_prefix_attention_workspace(int batch, int n_query, int n_he
     a.own.n_set = max_own > 0 ? batch : 0;
     a.own.max_keys = max_own;
     if (a.pre.n_set > 0 && !(needs & WH_GROUP_TABLE)) {
-        if (batch % a.pre.n_set != 0) return 0;
+        if (batch % a.pre.n_set != 0) return false;
         a.gsize = batch / a.pre.n_set;
     }
+    return true;
+}
+
+extern "C" size_t wh_prefix_attention_workspace(int batch, int n_query, int n_head, int n_kv_head, int n_prefix,
+                                                int max_prefix, int max_own, int needs) {
+    PaArgs a = {};
+    if (!sizes_of(batch, n_query, n_head, n_kv_head, n_prefix, max_prefix, max_own, needs, a)) return 0;
     size_t most = 0;   // the prefix part may run on either kernel
     for (int tc = 0; tc < 2; ++tc) {
         const size_t t = plan(a, tc, needs & WH_PREFIX_WEIGHT, needs & WH_OWN_WEIGHT).total;
         most = t > most ? t : most;
     }
     return most;
+}
+
+extern "C" int wh_prefix_attention_plan(int batch, int n_query, int n_head, int n_kv_head, int n_prefix, int max_prefix,
+                                        int max_own, int needs, wh_prefix_plan *out) {
+    PaArgs a = {};
+    if (!out || !sizes_of(batch, n_query, n_head, n_kv_head, n_prefix, max_prefix, max_own, needs, a)) return WH_EINVAL;
+    const bool has_pre = a.pre.n_set > 0, has_own = a.own.n_set > 0;
+    const bool pre_weight = has_pre && (needs & WH_PREFIX_WEIGHT), own_weight = has_own && (needs & WH_OWN_WEIGHT);
+    if (!has_pre && !has_own) return WH_EINVAL;
+    const PaPlan pl = plan(a, true, pre_weight, own_weight);
+    *out = {};
+    if (has_pre) {
+        out->prefix_rows = a.tile;
+        out->prefix_ranges = a.pre.splits;
+        out->prefix_cluster = a.pre_cluster;
+    }
+    if (has_own) {
+        out->own_warps = a.own_wpi;
+        out->own_ranges = a.own.splits;
+        out->own_cluster = a.own_cluster;
+        out->own_scores_kept = a.score_floats > 0;
+    }
+    out->merge = pl.merge;
+    out->launches = has_pre + has_own + pl.merge + pre_weight + (own_weight && !a.score_floats);
+    return WH_OK;
 }
 
 extern "C" int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch, int n_query, int n_head,

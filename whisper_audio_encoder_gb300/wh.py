@@ -65,6 +65,11 @@ class wh_keys(ctypes.Structure):
                 ("weight", _p), ("n_set", ctypes.c_int), ("max_keys", ctypes.c_int)]
 
 
+class wh_prefix_plan(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("prefix_rows", "prefix_ranges", "prefix_cluster", "own_warps", "own_ranges",
+                                            "own_cluster", "own_scores_kept", "merge", "launches")]
+
+
 _pack_keys = struct.Struct("PPqqPPii").pack   # wh_keys' fields: copied whole in half the time of setting each
 
 
@@ -108,6 +113,7 @@ def lib():
         "wh_decode_attention": (ctypes.c_int, [_p, _p, _p, ctypes.c_int64, ctypes.c_int64, _p, ctypes.c_int,
                                                ctypes.c_int, ctypes.c_int, _p, _p, ctypes.c_size_t, _p]),
         "wh_prefix_attention_workspace": (ctypes.c_size_t, [ctypes.c_int] * 8),
+        "wh_prefix_attention_plan": (ctypes.c_int, [ctypes.c_int] * 8 + [ctypes.POINTER(wh_prefix_plan)]),
         "wh_prefix_attention": (ctypes.c_int, [_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                ctypes.c_int, ctypes.POINTER(wh_keys), _p, ctypes.POINTER(wh_keys), _p,
                                                _p, ctypes.c_size_t, _p]),
@@ -424,6 +430,15 @@ def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_
     if rc != WH_OK:
         raise WhError(rc, what)
     return out
+
+
+def wh_prefix_attention_plan(batch, n_query, n_head, n_kv_head=None, n_prefix=0, max_prefix=0, max_own=0, needs=0):
+    """What a call of these sizes runs: the fields of the C struct wh_prefix_plan as a dict.  needs: a sum of
+    WH_GROUP_TABLE, WH_PREFIX_WEIGHT and WH_OWN_WEIGHT.  No device is needed."""
+    plan = wh_prefix_plan()
+    _check(lib().wh_prefix_attention_plan(batch, n_query, n_head, n_kv_head or n_head, n_prefix, max_prefix, max_own, needs,
+                                          plan), "wh_prefix_attention_plan")
+    return {f: getattr(plan, f) for f, _ in wh_prefix_plan._fields_}
 
 
 def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, workspace=None, stream=None):
