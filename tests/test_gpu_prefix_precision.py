@@ -93,3 +93,23 @@ def test_own_keys():
         over = np.abs(out[i] - ref[0]) / _tol(ref[0], spread[0], counts[i])
         assert over.max() <= 1.0, f"{counts[i]} keys: {over.max():.1f} times the tolerance"
     assert wh.wh_status() == wh.WH_OK
+
+
+@pytest.mark.parametrize("n_query, rep, n", [(4, 4, 100), (8, 2, 120), (1, 1, 120), (3, 5, 60)])
+def test_weights_are_added_to_large_accumulators_once(n_query, rep, n):
+    """The sum over the queries is made first: an accumulator of several hundred is rounded once, by half a step, however
+    many rows there are.  Sums off by 2^-20 + (keys + rows) 2^-24 of themselves as they come in (exponential, sum, order)."""
+    rng = np.random.default_rng(n)
+    B, KV = 9, 2
+    assert wh.wh_prefix_attention_plan(B, n_query, KV * rep, KV, max_own=n, needs=wh.WH_OWN_WEIGHT)["own_scores_kept"]
+    q = rng.integers(-1, 2, (B * n_query, 64 * KV * rep)).astype(np.float32)
+    own = [(rng.integers(-1, 2, (n, 64 * KV)).astype(np.float32), rng.standard_normal((n, 64 * KV))) for _ in range(B)]
+    w0 = (512 + 500 * rng.random((B, KV, n))).astype(np.float32)
+    weight = torch.from_numpy(w0).cuda()
+    keys = wh.Keys(_dev(np.stack([k for k, _ in own])), _dev(np.stack([v for _, v in own])), None, weight)
+    wh.wh_prefix_attention(_dev(q), KV * rep, own=keys, n_kv_head=KV, n_query=n_query)
+    _, _, _, w = R.prefix_attention(q, n_query, KV * rep, KV, [], [None] * B, own)
+    exact = w0 + np.stack(w)
+    tol = 2.0 ** -24 * exact + (2.0 ** -20 + (n + n_query * rep) * 2.0 ** -24) * np.stack(w)
+    over = np.abs(weight.cpu().numpy() - exact) / tol
+    assert over.max() <= 1.0, f"{over.max():.1f} times the tolerance, {(over > 1).sum()} of {over.size}"

@@ -352,9 +352,9 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         float *w = ks.weight + ((long long)set * p.n_kv + rw.hk) * ks.max_keys;
         constexpr int U = 4;   // keys of a thread at a time: their accumulators are read together
         for (int t = 32 * iw + lane; t < k1; t += U * 32 * wpi) {
-            float add[U];
+            float before[U], add[U] = {};   // (the rows' sum first: the accumulator is rounded once, not by every row)
 #pragma unroll
-            for (int u = 0; u < U; ++u) add[u] = t + u * 32 * wpi < k1 ? __ldcg(w + t + u * 32 * wpi) : 0.0f;
+            for (int u = 0; u < U; ++u) before[u] = t + u * 32 * wpi < k1 ? __ldcg(w + t + u * 32 * wpi) : 0.0f;
             for (int r = 0; r < rows; ++r) {
                 const float2 st = fin[w0][r];
                 const float *sr = scores + r * ks.chunk + t;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (t + u * 32 * wpi < k1) w[t + u * 32 * wpi] = add[u];
+                if (t + u * 32 * wpi < k1) w[t + u * 32 * wpi] = before[u] + add[u];
         }
     }
 }
