@@ -190,3 +190,28 @@ def test_huge_scores(beams):
         # (the second pass rounds the same score in another order: off by 64 2^-24 of 1e13 or so, and cut to 1)
         assert np.all(got[count == 0] == 0) and np.all(got <= count)
     assert wh.wh_status() == wh.WH_OK
+
+
+@pytest.mark.parametrize("sets", [3, 40])
+@pytest.mark.parametrize("rows", [16, 64])
+@pytest.mark.parametrize("bad", [-1, 701])
+def test_counts_of_groups_without_sequences_are_reported(sets, rows, bad):
+    H, cap = 2, 700
+    sizes = [0] + [1 if rows == 16 else 80 if sets > 3 else 150] * (sets - 2) + [0]
+    B = sum(sizes)
+    k = torch.zeros(sets, cap, 64 * H, dtype=torch.bfloat16, device="cuda")
+    own = wh.Keys(k[:1, :4].expand(B, 4, 64 * H).contiguous(), k[:1, :4].expand(B, 4, 64 * H).contiguous())
+    plan = wh.wh_prefix_attention_plan(B, 1, H, n_prefix=sets, max_prefix=cap, max_own=4, needs=wh.WH_GROUP_TABLE)
+    assert (plan["prefix_rows"] == 16) == (rows == 16)
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device="cuda")
+    n = torch.full((sets,), cap, dtype=torch.int32, device="cuda")
+    q = torch.zeros(B, 64 * H, dtype=torch.bfloat16, device="cuda")
+    call = lambda: wh.wh_prefix_attention(q, H, prefix=wh.Keys(k, k, n), own=own, group_start=starts)  # noqa: E731
+    call()
+    assert wh.wh_status() == wh.WH_OK
+    for g in (0, sets - 1):
+        n.fill_(cap)
+        n[g] = bad
+        call()
+        assert wh.wh_status() == wh.WH_EBOUNDS, g
+        assert wh.wh_status() == wh.WH_OK

@@ -113,7 +113,7 @@ __device__ __forceinline__ int pre_parts_of(const PaArgs &p, int g) {
 // Prefix work of one block: its group, the rows r0 .. of that group's tile, the group's key count (clamped), false
 // if the slot is empty.  With group_start, group g's tiles take the slots from start[g] (nq rep) / tile + g on,
 // which end before group g + 1's, so no block needs to know the other groups' sizes.  `report`: one block per
-// group reports a bad range or count.  Whole warps.
+// group reports a bad range or count (with group_start the block of slot g, since a group may have no rows).  Whole warps.
 __device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report, int &set, int &r0, Rows &rw, int &nk) {
     const int per = p.nq * p.rep, lane = threadIdx.x & 31;
     int s, e, count;
@@ -124,7 +124,8 @@ __device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report
         const int c = p.pre.n_keys ? __ldg(p.pre.n_keys + g) : p.pre.max_keys;
         const bool le = lane < p.pre.n_set && ((long long)a * per >> p.tile_shift) + g <= slot;
         set = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
-        const bool bad = __any_sync(0xffffffffu, lane == slot && lane < p.pre.n_set && (a < 0 || b < a || b > p.batch));
+        const bool bad = __any_sync(0xffffffffu, lane == slot && lane < p.pre.n_set &&
+                                                     (a < 0 || b < a || b > p.batch || c < 0 || c > p.pre.max_keys));
         if (report && bad && threadIdx.x == 0) set_status(p.ctl, WH_EBOUNDS);
         s = min(max(__shfl_sync(0xffffffffu, a, set), 0), p.batch);
         e = min(max(__shfl_sync(0xffffffffu, b, set), s), p.batch);
@@ -133,7 +134,8 @@ __device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report
         if (p.group_start) {
             if (report && slot < p.pre.n_set && threadIdx.x == 0) {
                 const int a = __ldg(p.group_start + slot), b = __ldg(p.group_start + slot + 1);
-                if (a < 0 || b < a || b > p.batch) set_status(p.ctl, WH_EBOUNDS);
+                const int c = p.pre.n_keys ? __ldg(p.pre.n_keys + slot) : 0;
+                if (a < 0 || b < a || b > p.batch || c < 0 || c > p.pre.max_keys) set_status(p.ctl, WH_EBOUNDS);
             }
             set = warp_search(p.group_start, p.pre.n_set, per, p.tile_shift, 1, slot);
         } else {
@@ -147,7 +149,7 @@ __device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report
     rw.n = (e - s) * per;
     nk = min(max(count, 0), p.pre.max_keys);
     const bool there = r0 >= 0 && r0 < rw.n;
-    if (there && report && r0 == 0 && count != nk && threadIdx.x == 0) set_status(p.ctl, WH_EBOUNDS);
+    if (!p.group_start && report && r0 == 0 && count != nk && threadIdx.x == 0) set_status(p.ctl, WH_EBOUNDS);
     return there;
 }
 
