@@ -215,3 +215,26 @@ def test_counts_of_groups_without_sequences_are_reported(sets, rows, bad):
         call()
         assert wh.wh_status() == wh.WH_EBOUNDS, g
         assert wh.wh_status() == wh.WH_OK
+
+
+@pytest.mark.parametrize("cap", [33, 64, 65, 80, 96, 97])
+@pytest.mark.parametrize("nq", [1, 2])
+def test_short_own_caches_of_few_sequences(cap, nq):
+    rng = np.random.default_rng(cap)
+    B, H = 3, 6
+    counts = [cap, cap // 2, 0]
+    own = [(_whole(rng, -2, 2, n, 64 * H), synth.bf16_round(rng.standard_normal((n, 64 * H)).astype(np.float32))) for n in counts]
+    q = _whole(rng, -2, 2, B * nq, 64 * H)
+    k, v = _buffers(B, cap, 64 * H, "apart")
+    for i, (x, y) in enumerate(own):
+        k[i, :len(x)], v[i, :len(x)] = _dev(x), _dev(y)
+    weight = torch.zeros(B, H, cap, device="cuda")
+    wh.lib().wh_launch_count()                         # (counts from here on)
+    out = wh.wh_prefix_attention(_dev(q), H, n_query=nq, own=wh.Keys(k, v, torch.tensor(counts, dtype=torch.int32, device="cuda"), weight))
+    launches = wh.lib().wh_launch_count()
+    assert launches == wh.wh_prefix_attention_plan(B, nq, H, max_own=cap, needs=wh.WH_OWN_WEIGHT)["launches"]
+    ref, spread, _, w = R.prefix_attention(q, nq, H, H, [], [None] * B, own)
+    assert np.all(np.abs(out.float().cpu().numpy() - ref) <= out_tol(ref, spread, cap))
+    for i, x in enumerate(w):
+        assert np.all(np.abs(weight[i, :, :counts[i]].cpu().numpy() - x) <= (2.0 ** -20 + (cap + nq) * 2.0 ** -24) * x + 1e-30)
+    assert wh.wh_status() == wh.WH_OK

@@ -44,3 +44,19 @@ def test_refusals():
     for args in ((0, 1, 6, 6, 2, 100, 0, 0), (4, 1, 6, 5, 2, 100, 0, 0), (4, 1, 6, 6, -1, 100, 0, 0), (4, 1, 6, 6, 3, 100, 0, 2),
                  (4, 1, 6, 6, 2, 100, 0, 8), (4, 1, 6, 6, 0, 0, 0, 0), (4, 0, 6, 6, 2, 100, 0, 0), (4, 1, 6, 6, 2, -1, 0, 0)):
         assert call(*args) == wh.WH_EINVAL, args
+
+
+@pytest.mark.parametrize("max_own", range(1, 97))
+def test_short_own_caches_take_one_launch(max_own):
+    """Fewer warps than four take an item only where it is short, or where items fill the device: one range either way."""
+    for batch, heads in ((1, 1), (2, 6), (5, 20), (80, 20)):
+        plan = wh.wh_prefix_attention_plan(batch, 1, heads, max_own=max_own, needs=wh.WH_OWN_WEIGHT)
+        assert (plan["own_ranges"], plan["own_cluster"], plan["merge"], plan["launches"]) == (1, 1, 0, 1), (batch, heads, plan)
+
+
+def test_short_own_caches_fill_the_device_or_take_four_warps():
+    for batch in range(1, 400, 7):
+        for max_own in (1, 32, 33, 64, 96, 97, 200, 448, 3000):
+            for prefix in (0, 100):
+                plan = wh.wh_prefix_attention_plan(batch, 1, 6, n_prefix=1 if prefix else 0, max_prefix=prefix, max_own=max_own)
+                assert plan["own_warps"] == 4 or plan["own_ranges"] == 1, plan

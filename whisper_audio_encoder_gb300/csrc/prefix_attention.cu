@@ -678,8 +678,9 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
            (items * a.own_wpi > PA_BLOCKS * PA_WARPS ||
             ((a.own_wpi - 1) * PA_KEYS >= a.own.max_keys && 32 * (a.own_wpi - 1) >= pieces)))
         a.own_wpi /= 2;
+    // (with fewer than four warps the items fill the device or are short: one range, which needs no joining)
     split_keys(a.own, items, PA_BLOCKS * (PA_WARPS / a.own_wpi), a.own_wpi * PA_KEYS,
-               ranges(a.own, has_pre ? OWN_LEAST : STEP));
+               a.own_wpi < PA_WARPS ? 1 : ranges(a.own, has_pre ? OWN_LEAST : STEP));
     a.own_items = items * a.own.splits;
     const bool one_launch = a.own_wpi == PA_WARPS && a.own.splits <= PA_CLUSTER && !has_pre;
     a.own_cluster = has_own && (a.own.splits == 1 || one_launch) ? a.own.splits : 0;
