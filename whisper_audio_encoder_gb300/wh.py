@@ -355,6 +355,17 @@ def _stream_handle(dev, stream):
     return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream, s):
+    """An uninitialised tensor in the order of the launching stream (handle s): memory that the current stream's work may
+    still hold is not in it, and it is not handed out again before the current stream's reads of it are done."""
+    if stream is None or s == _torch._C._cuda_getCurrentRawStream(device.index):
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        t = _torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(_torch.cuda.current_stream(device))
+    return t
+
+
 @functools.lru_cache(maxsize=4096)
 def _workspace_bytes(name, *args):
     return getattr(lib(), name)(*args)
@@ -380,7 +391,11 @@ def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_
     own keys.  q: bf16 [batch * n_query][64 n_head] (any row stride); prefix, own: Keys or None;
     group_start: int32 device [prefix sets + 1] or None (equal groups in order).  Adds the attention
     weight of every key to prefix.weight / own.weight where given.  Returns bf16
-    [batch * n_query][64 n_head]."""
+    [batch * n_query][64 n_head].
+
+    stream: launched there and ordered only after what is on it: a caller with work on the current stream that the call
+    reads (or whose memory `out` or the accumulators are) lets the stream wait for it, and waits for the stream before
+    reading the result elsewhere.  Memory that the call takes itself belongs to that stream."""
     if _torch is None:
         _load_torch()
     what = "wh_prefix_attention"
@@ -408,12 +423,12 @@ def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_
             _refuse("wh_prefix_attention: group_start int32 [prefix sets + 1]")
         table = group_start.data_ptr()
         needs |= WH_GROUP_TABLE
+    s = _stream_handle(dev, stream)
     if out is None:
-        out = _torch.empty(rows, 64 * n_head, dtype=_torch.bfloat16, device=q.device)
+        out = _empty((rows, 64 * n_head), _torch.bfloat16, q.device, stream, s)
     elif not (out.dtype is _torch.bfloat16 and out.shape == (rows, 64 * n_head) and out.is_contiguous() and
               out.get_device() == dev):
         _refuse("wh_prefix_attention: out bf16 [batch * n_query][64 n_head]")
-    s = _stream_handle(dev, stream)
     if workspace is None:
         need = _workspace_bytes("wh_prefix_attention_workspace", batch, n_query, n_head, n_kv_head, n_pre, max_pre, max_own,
                                 needs)
@@ -446,7 +461,8 @@ def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, worksp
     and the older ones of largest accumulated weight, in order.  They go to `out` (Keys with weight)
     or, without one, to the front of the cache itself.  kept: optional int32
     [n_set][n_kv_head][budget], the former index of every key that stays.  Returns the new counts:
-    out.n_keys or cache.n_keys, updated, or a new int32 [n_set] where that is None."""
+    out.n_keys or cache.n_keys, updated, or a new int32 [n_set] where that is None.  stream: as for
+    wh_prefix_attention."""
     what = "wh_cache_evict"
     to = cache if out is None else out
     dev, n_set = cache.device, cache.n_set
@@ -466,11 +482,11 @@ def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, worksp
             _refuse("wh_cache_evict: kept int32 [n_set][n_kv_head][budget]")
         indices = kept.data_ptr()
     n_out = to.n_keys
-    if n_out is None:
-        n_out = _torch.empty(n_set, dtype=_torch.int32, device=cache.k.device)
     if n_set == 0 and to.n_set == 0:
-        return n_out
+        return _torch.empty(0, dtype=_torch.int32, device=cache.k.device) if n_out is None else n_out
     s = _stream_handle(dev, stream)
+    if n_out is None:
+        n_out = _empty((n_set,), _torch.int32, cache.k.device, stream, s)
     if workspace is None:
         need = _workspace_bytes("wh_cache_evict_workspace", n_set, n_kv_head, cache.max_keys, budget)
         scratch = _Scratch(need, s) if need else None
