@@ -76,8 +76,8 @@ __device__ __forceinline__ void load_q(const PaArgs &p, const Rows &rw, int r0, 
             int qrow, head, qi;
             rw.locate(p, r, qrow, head, qi);
             const uint4 *s = reinterpret_cast<const uint4 *>(p.q + (long long)qrow * p.q_stride + head * 64) + c;
-            u0 = __ldg(s);
-            u1 = __ldg(s + 4);
+            u0 = ld_live(s);
+            u1 = ld_live(s + 4);
         }
         a[0][half] = u0.x, a[0][half + 2] = u0.y, a[1][half] = u0.z, a[1][half + 2] = u0.w;
         a[2][half] = u1.x, a[2][half + 2] = u1.y, a[3][half] = u1.z, a[3][half + 2] = u1.w;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) k_prefix_attention(const PaArgs
         rw.seq0 = set;
         rw.n = p.nq * p.rep;
         r0 = tile * PA_TILE;
-        const int count = ks.n_keys ? __ldg(ks.n_keys + set) : ks.max_keys;
+        const int count = ks.n_keys ? ld_live(ks.n_keys + set) : ks.max_keys;
         nk = min(max(count, 0), ks.max_keys);
         if (count != nk && rw.hk == 0 && split == 0 && r0 == 0 && iw == 0 && lane == 0) set_status(p.ctl, WH_EBOUNDS);
     } else {

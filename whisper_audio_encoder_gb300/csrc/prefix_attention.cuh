@@ -50,7 +50,7 @@ struct PaArgs {
 };
 
 __device__ __forceinline__ int clamp_count(const PaSet &s, int set) {
-    return s.n_keys ? min(max(__ldg(s.n_keys + set), 0), s.max_keys) : s.max_keys;
+    return s.n_keys ? min(max(ld_live(s.n_keys + set), 0), s.max_keys) : s.max_keys;
 }
 
 // Largest g in [0, n) with start[g] * mul / 2^shift + g * add <= x, by the whole warp, 32 probes at a time.
@@ -62,7 +62,7 @@ __device__ __forceinline__ int warp_search(const int *start, int n, int mul, int
         bool le = false;
         if (i < len) {
             const int g = lo + i;
-            le = ((long long)__ldg(start + g) * mul >> shift) + (long long)g * add <= x;
+            le = ((long long)ld_live(start + g) * mul >> shift) + (long long)g * add <= x;
         }
         const uint32_t m = __ballot_sync(0xffffffffu, le) | 1u;
         const int top = (31 - __clz(m)) * step;
@@ -75,8 +75,8 @@ __device__ __forceinline__ int warp_search(const int *start, int n, int mul, int
 // Sequences [s, e) of group g, cut to 0 .. batch.
 __device__ __forceinline__ void group_range(const PaArgs &p, int g, int &s, int &e) {
     if (p.group_start) {
-        s = min(max(__ldg(p.group_start + g), 0), p.batch);
-        e = min(max(__ldg(p.group_start + g + 1), s), p.batch);
+        s = min(max(ld_live(p.group_start + g), 0), p.batch);
+        e = min(max(ld_live(p.group_start + g + 1), s), p.batch);
     } else {
         s = g * p.gsize;
         e = s + p.gsize;
@@ -120,8 +120,8 @@ __device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report
     if (p.group_start && p.pre.n_set <= 32) {
         // a lane a group: bounds and counts arrive together, after one load's latency
         const int g = min(lane, p.pre.n_set - 1);
-        const int a = __ldg(p.group_start + g), b = __ldg(p.group_start + g + 1);
-        const int c = p.pre.n_keys ? __ldg(p.pre.n_keys + g) : p.pre.max_keys;
+        const int a = ld_live(p.group_start + g), b = ld_live(p.group_start + g + 1);
+        const int c = p.pre.n_keys ? ld_live(p.pre.n_keys + g) : p.pre.max_keys;
         const bool le = lane < p.pre.n_set && ((long long)a * per >> p.tile_shift) + g <= slot;
         set = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
         const bool bad = __any_sync(0xffffffffu, lane == slot && lane < p.pre.n_set &&
@@ -133,15 +133,15 @@ __device__ __forceinline__ bool find_tile(const PaArgs &p, int slot, bool report
     } else {
         if (p.group_start) {
             if (report && slot < p.pre.n_set && threadIdx.x == 0) {
-                const int a = __ldg(p.group_start + slot), b = __ldg(p.group_start + slot + 1);
-                const int c = p.pre.n_keys ? __ldg(p.pre.n_keys + slot) : 0;
+                const int a = ld_live(p.group_start + slot), b = ld_live(p.group_start + slot + 1);
+                const int c = p.pre.n_keys ? ld_live(p.pre.n_keys + slot) : 0;
                 if (a < 0 || b < a || b > p.batch || c < 0 || c > p.pre.max_keys) set_status(p.ctl, WH_EBOUNDS);
             }
             set = warp_search(p.group_start, p.pre.n_set, per, p.tile_shift, 1, slot);
         } else {
             set = p.by_group_tiles.of(slot);
         }
-        count = p.pre.n_keys ? __ldg(p.pre.n_keys + set) : p.pre.max_keys;
+        count = p.pre.n_keys ? ld_live(p.pre.n_keys + set) : p.pre.max_keys;
         group_range(p, set, s, e);
     }
     r0 = (slot - (p.group_start ? (int)((long long)s * per >> p.tile_shift) + set : set * p.group_tiles)) * p.tile;
@@ -257,8 +257,8 @@ __device__ __forceinline__ void finish_outside(const PaArgs &p, int slot, int hk
         if (slot != (end ? p.slots - 1 : 0)) continue;
         Rows rw;
         rw.hk = hk;
-        rw.seq0 = end ? min(max(__ldg(p.group_start + p.pre.n_set), 0), p.batch) : 0;
-        rw.n = ((end ? p.batch : min(max(__ldg(p.group_start), 0), p.batch)) - rw.seq0) * p.nq * p.rep;
+        rw.seq0 = end ? min(max(ld_live(p.group_start + p.pre.n_set), 0), p.batch) : 0;
+        rw.n = ((end ? p.batch : min(max(ld_live(p.group_start), 0), p.batch)) - rw.seq0) * p.nq * p.rep;
         for (long long i = threadIdx.x; i < 8LL * rw.n; i += blockDim.x) {
             float none[8] = {};
             finish_row(p, rw, (int)(i >> 3), 8 * (int)(i & 7), -INFINITY, 0.0f, none, 0);

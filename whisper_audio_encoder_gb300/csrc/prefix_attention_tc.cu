@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(PT_THREADS, 2) k_prefix_tc(const __grid_consta
             rw.locate(p, r, qrow, head, qi);
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (long long)qrow * p.q_stride + head * 64);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = __ldg(src + i);
+            for (int i = 0; i < 8; ++i) u[i] = ld_live(src + i);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(sQ + a * 128 + ((i ^ (a & 7)) << 4)) = u[i];
