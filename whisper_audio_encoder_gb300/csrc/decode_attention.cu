@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(DA_THREADS) k_decode_attention(const DecAttnAr
     float q[16];
     {
         const uint4 *qp = reinterpret_cast<const uint4 *>(p.q + (long long)b * p.n_head * 64 + h * 64 + 16 * sub);
-        bf16x8_to_f32(__ldg(qp), q);
-        bf16x8_to_f32(__ldg(qp + 1), q + 8);
+        bf16x8_to_f32(ld_live(qp), q);
+        bf16x8_to_f32(ld_live(qp + 1), q + 8);
         const float sc = 0.125f * 1.4426950408889634f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) q[i] *= sc;
@@ -107,10 +107,10 @@ __global__ void __launch_bounds__(DA_THREADS) k_decode_attention(const DecAttnAr
             if (live[u]) {
                 const uint4 *kp = reinterpret_cast<const uint4 *>(kb + (long long)t * p.row_stride);
                 const uint4 *vp = reinterpret_cast<const uint4 *>(vb + (long long)t * p.row_stride);
-                kr[u][0] = __ldg(kp);
-                kr[u][1] = __ldg(kp + 1);
-                vr[u][0] = __ldg(vp);
-                vr[u][1] = __ldg(vp + 1);
+                kr[u][0] = ld_live(kp);
+                kr[u][1] = ld_live(kp + 1);
+                vr[u][0] = ld_live(vp);
+                vr[u][1] = ld_live(vp + 1);
             }
         }
 #pragma unroll

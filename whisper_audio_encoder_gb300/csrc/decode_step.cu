@@ -72,7 +72,7 @@ __device__ __forceinline__ void sk_finish(const SkArgs &p, int b, int n, float b
     if constexpr (MODE == SK_QKV) {
         const int seg = n / p.seg_n, nin = n - seg * p.seg_n;
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(seg == 0 ? p.out[0] : (seg == 1 ? p.out[1] : p.out[2]));
-        const long long row = seg == 0 ? b : (long long)b * p.cap + __ldg(p.pos + b);
+        const long long row = seg == 0 ? b : (long long)b * p.cap + ld_live(p.pos + b);
         o[row * p.seg_n + nin] = __float2bfloat16_rn(v);
     } else if constexpr (MODE == SK_BF16 || MODE == SK_GELU) {
         if constexpr (MODE == SK_GELU) v = gelu_erf(v);

@@ -19,7 +19,7 @@ constexpr int MAXV = 16;  // float4 per lane: d <= 2048
 // reverse: blocks take the rows from the last one down (the rows a GEMM stored last are the ones
 // still in L2).
 template <int NV, bool OUT_BF16>
-__global__ void __launch_bounds__(LN_THREADS) k_layernorm(const float *__restrict__ x, int rows, int d,
+__global__ void __launch_bounds__(LN_THREADS) k_layernorm(const float *x, int rows, int d,
                                                           const float *__restrict__ g,
                                                           const float *__restrict__ b, void *__restrict__ y,
                                                           int reverse) {
@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(LN_THREADS) k_layernorm(const float *__restric
     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
     for (int i = 0; i < CAP; ++i)
-        if (i < nv) v[i] = __ldg(xr + i * 32 + lane);
+        if (i < nv) v[i] = ld_live(xr + i * 32 + lane);
 #pragma unroll
     for (int i = 0; i < CAP; ++i)
         if (i < nv) {
@@ -98,7 +98,7 @@ cudaError_t launch_ln(int grid, cudaStream_t s, bool pdl, const float *x, int ro
 
 // d a multiple of 64 but not of 128: float2 per lane.
 template <bool OUT_BF16>
-__global__ void __launch_bounds__(LN_THREADS) k_layernorm64(const float *__restrict__ x, int rows, int d,
+__global__ void __launch_bounds__(LN_THREADS) k_layernorm64(const float *x, int rows, int d,
                                                             const float *__restrict__ g,
                                                             const float *__restrict__ b, void *__restrict__ y,
                                                             int reverse) {
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(LN_THREADS) k_layernorm64(const float *__restr
 #pragma unroll
     for (int i = 0; i < 2 * MAXV; ++i)
         if (i < nv) {
-            v[i] = __ldg(xr + i * 32 + lane);
+            v[i] = ld_live(xr + i * 32 + lane);
             s += v[i].x + v[i].y;
         }
     const float mean = warp_sum(s) / (float)d;
