@@ -384,7 +384,7 @@ int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch, int n_que
  *   may overlap (sets one after the other or side by side in a row; [K | V] rows are fine).
  *   workspace >= wh_cache_evict_workspace(n_set, n_kv_head, cache->max_keys, budget) bytes, 256-byte
  *           aligned, contents need not be initialised; not shared by concurrent calls.  May be NULL
- *           where that is 0.
+ *           where that is 0; with kept given, 4 n_set bytes rounded up to 256 are enough.
  * A count outside 0 .. max_keys is clamped and recorded as WH_EBOUNDS.  All layers' caches
  * [n_layer][batch][...] are n_layer * batch sets of one call.
  * Errors: WH_EINVAL, WH_ENOSPC, WH_ECUDA.

@@ -93,3 +93,13 @@ def test_interleaved_layouts_by_their_rows(L):
         assert _call(L, _keys(v=P + 2 * W, set_stride=128, **beside)) == wh.WH_ENODEV   # K0 K1 V0 V1
         assert _call(L, _keys(v=P - W, k=P, n_set=2, row_stride=512, set_stride=256)) == wh.WH_ENODEV   # V0 K0 V1 K1
         assert _call(L, _keys(v=P + W, n_set=2, row_stride=256, set_stride=100 * 256 + 128)) == wh.WH_ENODEV
+
+
+def test_workspace_holds_what_can_stay_and_no_more(L):
+    size = L.wh_cache_evict_workspace
+    assert size(3, 300, 100, 1 << 30) == size(3, 300, 100, 100) > 3 * 300 * 100 * 4      # a budget past the cache
+    wide = dict(row_stride=19200, set_stride=1920000, v=P + (1 << 26), weight=P + (1 << 27))
+    # the indices go to kept: the counts are all that is left
+    assert _call(L, _keys(**wide), n_kv=300, kept=FAKE, ws_bytes=255) == wh.WH_ENOSPC
+    if not torch.cuda.is_available():
+        assert _call(L, _keys(**wide), n_kv=300, kept=FAKE, ws_bytes=256) == wh.WH_ENODEV

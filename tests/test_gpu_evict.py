@@ -326,3 +326,22 @@ def test_no_sets_and_single_rows_of_odd_width():
     assert wh.wh_cache_evict(wh.Keys(k, v, None, w), 2, 1, 0).tolist() == [1]
     out = wh.wh_prefix_attention(torch.zeros(1, 128, dtype=torch.bfloat16, device="cuda"), 2, own=wh.Keys(k, v, None, w))
     assert torch.equal(out, v[:, 0, :128]) and w.tolist() == [[[2.0], [2.0]]] and wh.wh_status() == wh.WH_OK
+
+
+@pytest.mark.parametrize("in_place", [False, True], ids=["out", "in_place"])
+@pytest.mark.parametrize("budget", [33, 64, 65, 1000])
+def test_budgets_up_to_and_past_the_cache_without_indices(budget, in_place):
+    """The indices then stand in the workspace, as many a head as can stay."""
+    Case(heads=20, cap=64, counts=[(7 * i) % 65 for i in range(40)], budget=budget, recent=4, kind="ties",
+         seed=9).check(in_place, cap_out=64, with_kept=False)
+
+
+def test_a_budget_of_any_size_needs_no_more_memory_than_the_cache():
+    c = Case(heads=20, cap=64, counts=[(7 * i) % 65 for i in range(40)], budget=1 << 30, recent=1 << 30, seed=9)
+    k, v, w = torch.zeros_like(c.k), torch.zeros_like(c.v), torch.zeros_like(c.w)
+    n = torch.zeros_like(c.n)
+    wh.wh_cache_evict(wh.Keys(c.k, c.v, c.n, c.w), 20, 1 << 30, 1 << 30, out=wh.Keys(k, v, n, w))
+    assert torch.equal(n, c.n) and wh.wh_status() == wh.WH_OK
+    for i, x in enumerate(c.counts):
+        assert same(k[i, :x], c.k[i, :x]) and same(v[i, :x], c.v[i, :x]) and same(w[i, :, :x], c.w[i, :, :x])
+        assert not k[i, x:].any() and not v[i, x:].any() and not w[i, :, x:].any()

@@ -59,7 +59,8 @@ struct EvArgs {
     float *weight_out;
     const int *n_keys;
     int *n_out;
-    int *kept;                 // [n_set][n_head][budget]: source index of every key that stays
+    int *kept;                 // [n_set][n_head][kept_stride]: source index of every key that stays
+    long long kept_stride;     // the caller's: budget; the workspace's: what can stay
     int *count;                // [n_set]: keys before, as clamped
     int max_keys, out_keys, n_set, n_head, budget, recent, in_place;
     Divisor by_row;            // 16-byte pieces of a row
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(SM_THREADS) k_evict_small(const EvArgs p) {
     const long long sh = (long long)set * p.n_head + h;
     const float *w = p.weight + sh * p.max_keys;
     float *wo = p.weight_out + sh * p.out_keys;
-    int *kept = p.kept ? p.kept + sh * p.budget : nullptr;
+    int *kept = p.kept ? p.kept + sh * p.kept_stride : nullptr;
     const bool all = n <= p.budget;   // everything stays
     if (all) {
         for (int i = tid; i < n; i += SM_THREADS) {
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(CHOOSERS == 32 ? 128 : CHOOSERS, CTAS == 1 ? 0
     if (h == 0 && tid == 0) p.count[set] = n;
     const float *w = p.weight + sh * p.max_keys;
     float *wo = p.weight_out + sh * p.out_keys;
-    int *src = p.kept + sh * p.budget;
+    int *src = p.kept + sh * p.kept_stride;
     if (n <= p.budget) {   // everything stays
         for (int i = tid; i < n; i += team.ALL) {
             src[i] = i;
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(MV_THREADS) k_evict_move(const EvArgs p) {
         if (i < todo) {
             j[u] = sizeof(I) == 4 ? p.by_row.of((int)i) : (int)(i / per_row);
             x[u] = (int)(i - (I)j[u] * per_row);
-            t[u] = __ldcg(p.kept + ((long long)set * p.n_head + (x[u] >> 3)) * p.budget + j[u]);
+            t[u] = __ldcg(p.kept + ((long long)set * p.n_head + (x[u] >> 3)) * p.kept_stride + j[u]);
         }
     }
 #pragma unroll
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(SH_THREADS, SH_RESIDENT) k_evict_shift(const E
     if (h == 0 && blockIdx.y == 0 && place == 0) p.n_out[set] = n;
     if (n0 <= p.budget) return;
     __nv_bfloat16 *x = (blockIdx.y ? p.v_out : p.k_out) + (long long)set * p.set_stride + h * 64 + 8 * (threadIdx.x & 7);
-    const int *src = p.kept + ((long long)set * p.n_head + h) * p.budget;
+    const int *src = p.kept + ((long long)set * p.n_head + h) * p.kept_stride;
     constexpr int U = SH_ROWS, STEP = CTAS * SH_THREADS / 8;
     for (int base = place >> 3; base < (n + U * STEP - 1) / (U * STEP) * (U * STEP); base += U * STEP) {
         int t[U];
@@ -638,7 +639,7 @@ extern "C" size_t wh_cache_evict_workspace(int n_set, int n_kv_head, int max_key
     if (n_set < 1 || n_set > 65535 || n_kv_head < 1 || n_kv_head > 1024 || max_keys < 1 || max_keys > (1 << 30) ||
         budget < 1 || budget > (1 << 30) || one_kernel(n_set, n_kv_head, max_keys, budget, false))
         return 0;
-    return up256e((size_t)n_set * 4) + up256e((size_t)n_set * n_kv_head * budget * 4);
+    return up256e((size_t)n_set * 4) + up256e((size_t)n_set * n_kv_head * std::min(budget, max_keys) * 4);
 }
 
 extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, int recent, const wh_keys *out, int *n_out,
@@ -668,8 +669,9 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
     }
     if (cache->n_keys && n_out != cache->n_keys && meet(span_of(n_out, cache->n_set, 4), span_of(cache->n_keys, cache->n_set, 4)))
         return WH_EINVAL;
-    if ((workspace ? ws_bytes : 0) < wh_cache_evict_workspace(cache->n_set, n_kv_head, cache->max_keys, budget))
-        return WH_ENOSPC;
+    size_t need = wh_cache_evict_workspace(cache->n_set, n_kv_head, cache->max_keys, budget);
+    if (kept && need) need = up256e((size_t)cache->n_set * 4);   // the indices go there
+    if ((workspace ? ws_bytes : 0) < need) return WH_ENOSPC;
     DevCtl ctl;
     int num_sms = 0;
     if (int rc = device_ctl(&ctl, &num_sms)) return rc;
@@ -688,6 +690,7 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
     a.n_keys = cache->n_keys;
     a.n_out = n_out;
     a.count = static_cast<int *>(workspace);
+    a.kept_stride = kept ? budget : std::min(budget, cache->max_keys);
     a.max_keys = cache->max_keys;
     a.out_keys = o->max_keys;
     a.n_set = cache->n_set;

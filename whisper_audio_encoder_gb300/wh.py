@@ -489,6 +489,8 @@ def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, worksp
         n_out = _empty((n_set,), _torch.int32, cache.k.device, stream, s)
     if workspace is None:
         need = _workspace_bytes("wh_cache_evict_workspace", n_set, n_kv_head, cache.max_keys, budget)
+        if need and indices is not None:
+            need = (4 * n_set + 255) & ~255
         scratch = _Scratch(need, s) if need else None
         at = scratch.ptr if need else None
     else:
