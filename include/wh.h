@@ -328,7 +328,8 @@ int wh_decode_attention(const wh_bf16 *q, const wh_bf16 *k, const wh_bf16 *v, in
  *           256-byte aligned, contents need not be initialised; not shared by concurrent calls.
  *           May be NULL where that is 0.
  *   row_stride >= 64 n_kv_head, q_stride >= 64 n_head, set_stride >= 0, all multiples of 8; q, k, v,
- *   out 16-byte aligned; batch, n_set <= 65535, n_query, n_head <= 1024, 1 <= max_keys <= 2^30.
+ *   out 16-byte aligned; batch, n_set <= 65535, n_query, n_head <= 1024, batch x n_query x n_head < 2^31,
+ *   1 <= max_keys <= 2^30.
  * group_start is checked on the device: a group that does not lie in 0 .. batch is cut to it and
  * recorded as WH_EBOUNDS; the outputs of the sequences concerned are then unspecified.
  * The same inputs give the same bits (sums have one order).
@@ -380,7 +381,7 @@ int wh_prefix_attention(const wh_bf16 *q, int64_t q_stride, int batch, int n_que
  *   n_out   device int32 [n_set]: the new counts, min(n, budget); may be cache->n_keys
  *   kept    device int32 [n_set][n_kv_head][budget] or NULL: the former index of every key that
  *           stays; entries past the new count are left as they were
- *   1 <= n_set <= 65535, 0 <= recent <= budget, 1 <= budget <= 2^30; within a wh_keys no two sets and no keys and values
+ *   1 <= n_set <= 65535, n_kv_head <= 1024, 0 <= recent <= budget, 1 <= budget <= 2^30; within a wh_keys no two sets and no keys and values
  *   may overlap (sets one after the other or side by side in a row; [K | V] rows are fine).
  *   workspace >= wh_cache_evict_workspace(n_set, n_kv_head, cache->max_keys, budget) bytes, 256-byte
  *           aligned, contents need not be initialised; not shared by concurrent calls.  May be NULL
