@@ -49,8 +49,8 @@ PATHS = {
     "64 rows, own keys, one set for all groups": _case(_tc(64, 1, 0), 2, [40] * 3, 200, n_pre=[200] * 3, own=5, table=False, layout="one"),
     "64 rows, own keys, sets beside each other": _case(_tc(64, 1, 0), 2, [40] * 3, 200, own=5, table=False, layout="beside"),
     "64 rows, own keys, odd set stride": _case(_tc(64, 1, 0), 2, [40] * 3, 200, own=5, table=False, layout="odd"),
-    "128 rows, own keys, ranges": _case(_tc(128, 12, 0), 2, [130, 70], 6000, own=9, weigh=True),
-    "128 rows, own keys in ranges": _case(_tc(128, 6, 0, 1), 1, [33, 34], 3000, nq=3, own=1300, weigh=True),
+    "128 rows, own keys, ranges": _case(_tc(128, 16, 0), 2, [130, 70], 6000, own=9, weigh=True),
+    "128 rows, own keys in ranges": _case(_tc(128, 8, 0, 1), 1, [33, 34], 3000, nq=3, own=1300, weigh=True),
     # 32 rows without own keys in the layouts of tensor maps
     "32 rows, [K | V] rows": _case(_tc(32, 8, 0, 1), 8, [20] * 4, 6000, table=False, layout="kv"),
     "32 rows, one set for all groups": _case(_tc(32, 8, 0, 1), 8, [20] * 4, 6000, n_pre=[6000] * 4, table=False, layout="one"),

@@ -577,23 +577,25 @@ constexpr long long PA_BLOCKS = 3 * 152;   // k_prefix_attention: 3 blocks on ea
 constexpr long long PT_BLOCKS = 2 * 152;   // k_prefix_tc: 2 on each
 // The prefix part goes to k_prefix_tc when its sets have more than PT_MIN_ROWS rows on average and there are at
 // least PT_MIN_WORK products of a 16-row tile with a key (k_prefix_attention's units) to do: below that its
-// blocks' longer set-up (TMEM, tensor maps) does not pay.  Measured, us a call, 20 key heads:
+// blocks' longer set-up (TMEM, tensor maps) does not pay.  Measured, us a replayed call, 20 key heads:
 //   rows x keys x sets   products   k_prefix_attention   k_prefix_tc
-//    40 x  400 x  1         24 k           9.3              10.9
-//   128 x 1500 x  1        240 k          16.4              17.7
-//    40 x 1500 x  4        360 k          18.4              18.1
-//    64 x 1500 x  4        480 k          20.6              18.1
-//    40 x 8000 x  1        480 k          22.6              20.3
-//   128 x 1500 x 16        3.8 M          96                45
-// Beside own keys, whose blocks hide the set-up, more than twice PT_MIN_ROWS rows are enough: 200 rows x 400
-// keys, 8 heads, with up to 224 own keys 20.5 and 18.7.
+//    40 x  400 x  1         24 k           9.4              12.2
+//   128 x 1500 x  1        240 k          16.4              19.0
+//    40 x 1500 x  4        360 k          18.4              18.5
+//    64 x 1500 x  4        480 k          20.6              18.5
+//    40 x 8000 x  1        480 k          22.6              21.0
+//   128 x 1500 x 16        3.8 M          94                49
+// Beside own keys, whose blocks hide the set-up, more than twice PT_MIN_ROWS rows are taken: 200 rows x 400 keys, 8
+// heads, with up to 224 own keys 20.5 and 18.5; 64 rows x 1200 keys, 20 heads 20.4 and 16.5; 40 rows x 400 keys, 8 heads
+// 10.2 and 14.3, the same for the host, whose two launches take longer.
 constexpr int PT_MIN_ROWS = 16;
 constexpr long long PT_MIN_WORK = 300000;
 // Ranges of at least PT_LEAST keys (rounded down): a shorter block does not make up for joining one range more.
-// 128 rows x 800 keys x 4 sets: 16.4 us with one range, 20.5 with the three that would fill the device;
-// 40 rows x 8000 keys: 20.9 with 15, 58.8 with one.  Beside own keys, whose blocks join them anyway, PT_LEAST_BESIDE: 256
-// rows x 900 keys, 8 heads, 24.0 us and 20.7; 8 groups of 45 queries x 2 heads x 1000 keys, 6 key heads, 20.5 and 18.1.
-constexpr int PT_LEAST = 512, PT_LEAST_BESIDE = 384;
+// 128 rows x 800 keys x 4 sets: 17.8 us with one range, 19.9 with the three that would fill the device;
+// 40 rows x 8000 keys: 20.3 with 15, 63.4 with one.  Beside own keys, whose blocks join them anyway, PT_LEAST_BESIDE: 256
+// rows x 900 keys, 8 heads, 26.6 us with 512, 22.2 with 384, 20.8 with 256; 8 groups of 45 queries x 2 heads x 1000 keys,
+// 6 key heads, 22.5, 20.4 and 18.5; with 128 the same as with 256.
+constexpr int PT_LEAST = 512, PT_LEAST_BESIDE = 256;
 constexpr int PA_CLUSTER = 16, PT_CLUSTER = 2;   // ranges that a cluster's blocks join by themselves
 // Up to this many keys a block, one cluster instead of more ranges and the merge kernel: 5 rows x 2 heads x
 // 30000 keys 17.8 us in clusters of 16, 30 us in 228 ranges; 5 x 6 x 1500: 8.2 in 16, 11.7 in 24.
@@ -649,7 +651,7 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     const bool much = slots(PA_TILE) * a.n_kv * a.pre.max_keys >= PT_MIN_WORK;
     pl.tc = may_tc && rows_a_set > PT_MIN_ROWS && (much || (has_own && rows_a_set > 2 * PT_MIN_ROWS));
     // the smallest tile that holds an average group (us a call with tiles of 32, 64, 128 rows, 4 prefixes of 1500
-    // keys: 20 rows 16.4, 16.5, 16.6; 40 rows 18.9, 18.1, 18.5; 100 rows 30.8, 22.1, 20.7)
+    // keys: 20 rows 16.4, 16.5, 16.5; 40 rows 21.1, 18.5, 20.5; 100 rows 33.6, 23.9, 22.6)
     a.tile = !pl.tc ? PA_TILE : rows_a_set > 64 ? 128 : rows_a_set > 32 ? 64 : 32;
     a.slots = has_pre ? (int)slots(a.tile) : 0;
     a.own_tiles = (int)((per + PA_TILE - 1) / PA_TILE);

@@ -16,12 +16,15 @@
 //
 // Warp 0 loads (TMA), warp 1 issues the products (2 and 3 idle), warps 4 .. 7 are the rows' (warp w reads the
 // TMEM lanes 32 (w % 4) and up).  Two blocks are resident on an SM, so one's softmax runs beside the other's products.
-// What bounds it: the arrival of keys and values (the products' thread waits for them 2000 to 2800 of about 3600
-// cycles a step with two blocks on the SM), less than the softmax (1400) and the products (about 700).
-//   32 rows, 20 heads, 30000 keys: 31 us, 154 MB, 5.0 TB/s (a TMA read alone takes 26)
-//   256 rows, 20 heads, 15000 keys: 31 us, 19.7 GFLOP, 630 TFLOP/s; both tiles read every key
-//   rings of keys and values with their own barriers (38 -> 40 us at 32 rows) and pairs of blocks that load for
-//   each other by multicast (51.5 -> 55 us at 256 rows) were slower; two stages instead of three 38 -> 44.
+// What bounds it, in cycles of a step with two blocks on the SM: 32 rows wait for keys and values, 1200 of 2500 (exponentials
+// 310); with 256 rows the rows' warps are busy, 2250 of 2970 (exponentials and their two parts 1300, maximum 400, TMEM reads
+// and writes 365, rescaling 190), and the products' warp issues for 710.
+//   32 rows, 20 heads, 30000 keys: 33 us, 154 MB, 4.7 TB/s (a TMA read alone takes 26)
+//   256 rows, 20 heads, 15000 keys: 39 us, 19.7 GFLOP, 505 TFLOP/s; both tiles read every key
+// Not kept (these and the comparisons below with one bf16 a weight): rings of keys and values with their own barriers, 38 ->
+// 40 us at 32 rows; pairs of blocks that load for each other by multicast, 51.5 -> 55 us at 256 rows; two stages instead of
+// three, 38 -> 44.  With two: P's low parts in S's columns, read by then, and the next scores after the products, 59.1 ->
+// 62.8 us (256 rows beside own keys); the next scores between the halves, 61.5.
 // Every wait is bounded; when one runs out the block records WH_ETIMEOUT and winds down.
 #include "prefix_attention.cuh"
 
