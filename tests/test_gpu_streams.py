@@ -117,3 +117,38 @@ def test_recorded_without_a_workspace():
     assert torch.equal(out, ref) and wh.wh_status() == wh.WH_OK
     for a, b in ((to.k, ref_to.k), (to.v, ref_to.v), (to.weight, ref_to.weight), (to.n_keys, ref_to.n_keys)):
         assert torch.equal(a, b)
+
+
+def _older():
+    """The calls that take their results' and their workspace's memory themselves."""
+    pcm = torch.randn(2, 16000, device="cuda")
+    x, g, w = torch.randn(64, 384, device="cuda"), torch.ones(384, device="cuda"), _bf(384, 384)
+    kv, rows = _bf(2, 1500, 768), _bf(200, 576)
+    cross = wh.CrossKV(384, [{"wk": _bf(384, 384).float().cpu().numpy(), "wv": _bf(384, 384).float().cpu().numpy(), "bv": None}])
+    mem = torch.randn(1, 100, 384, device="cuda")
+    return {
+        "wh_frontend": lambda s=None: wh.wh_frontend(pcm, 80, stream=s),
+        "wh_frontend_long": lambda s=None: wh.wh_frontend_long(pcm[0], 80, stream=s),
+        "wh_resample": lambda s=None: wh.wh_resample(pcm, 44100, stream=s),
+        "wh_layer_norm": lambda s=None: wh.wh_layer_norm(x, g, g, stream=s),
+        "wh_linear": lambda s=None: wh.wh_linear(w, w, stream=s),
+        "wh_attention": lambda s=None: wh.wh_attention(rows, 1, 200, 3, stream=s),
+        "wh_decode_attention": lambda s=None: wh.wh_decode_attention(w[:2], kv, kv[..., 384:], 768, 768 * 1500, 1500, 6, stream=s),
+        "wh_prepare_cross": lambda s=None: cross.wh_prepare_cross(mem, stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", ["wh_frontend", "wh_frontend_long", "wh_resample", "wh_layer_norm", "wh_linear", "wh_attention",
+                                  "wh_decode_attention", "wh_prepare_cross"])
+def test_older_calls_take_the_launching_stream_s_memory_too(name, monkeypatch):
+    call = _older()[name]
+    ref = call()                                       # (with whatever a class keeps)
+    torch.cuda.synchronize()
+    s, taken, empty = torch.cuda.Stream(), [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: (taken.append(torch.cuda.current_stream().cuda_stream), empty(*a, **kw))[1])
+    s.wait_stream(torch.cuda.current_stream())
+    got = call(s)
+    monkeypatch.undo()
+    assert taken and set(taken) == {s.cuda_stream} and stream_of(got) == s.cuda_stream
+    s.synchronize()
+    assert torch.equal(got, ref) and wh.wh_status() == wh.WH_OK

@@ -172,6 +172,31 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+
+
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor in the order of the stream that a call is launched on: memory that the current stream's work
+    may still hold is not in it, what is dropped after the call is not handed out before the call is done, and what is
+    returned not before the current stream's reads are."""
+    if _torch is None:
+        _load_torch()
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    current = _torch.cuda.current_stream(device)
+    with _torch.cuda.stream(stream):
+        t = _torch.empty(shape, dtype=dtype, device=device)
+    if stream.cuda_stream != current.cuda_stream:
+        t.record_stream(current)
+    return t
+
+
 def _stream(stream=None):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
@@ -179,7 +204,8 @@ def _stream(stream=None):
 
 
 # ---------------------------------------------------------------------------------------
-# Entry points (same names as the C ABI), taking torch tensors
+# Entry points (same names as the C ABI), taking torch tensors.  stream: a call is launched there and ordered only after
+# what is on it; the caller orders it with the current stream's work.  Memory that a call takes itself is that stream's.
 # ---------------------------------------------------------------------------------------
 def wh_frontend_workspace(batch: int) -> int:
     return lib().wh_frontend_workspace(batch)
@@ -191,9 +217,9 @@ def wh_frontend(pcm, n_mels: int, mel=None, workspace=None, stream=None):
     assert pcm.dtype == torch.float32 and pcm.dim() == 2 and pcm.is_contiguous()
     batch, n = pcm.shape
     if mel is None:
-        mel = torch.empty(batch, N_FRAMES, n_mels, dtype=torch.float32, device=pcm.device)
+        mel = _empty((batch, N_FRAMES, n_mels), torch.float32, pcm.device, stream)
     if workspace is None:
-        workspace = torch.empty(max(16, wh_frontend_workspace(batch)), dtype=torch.uint8, device=pcm.device)
+        workspace = _empty((max(16, wh_frontend_workspace(batch)),), torch.uint8, pcm.device, stream)
     rc = lib().wh_frontend(_ptr(pcm), n, batch, n_mels, _ptr(mel), _ptr(workspace), workspace.numel(),
                            _stream(stream))
     _check(rc, "wh_frontend")
@@ -208,9 +234,9 @@ def wh_frontend_long(pcm, n_mels: int, mel=None, workspace=None, stream=None):
     n = pcm.shape[0]
     windows = lib().wh_frontend_windows(n)
     if mel is None:
-        mel = torch.empty(max(windows, 0), N_FRAMES, n_mels, dtype=torch.float32, device=pcm.device)
+        mel = _empty((max(windows, 0), N_FRAMES, n_mels), torch.float32, pcm.device, stream)
     if workspace is None:
-        workspace = torch.empty(max(16, wh_frontend_workspace(max(windows, 1))), dtype=torch.uint8, device=pcm.device)
+        workspace = _empty((max(16, wh_frontend_workspace(max(windows, 1))),), torch.uint8, pcm.device, stream)
     _check(lib().wh_frontend_long(_ptr(pcm), n, n_mels, _ptr(mel), _ptr(workspace), workspace.numel(),
                                   _stream(stream)), "wh_frontend_long")
     return mel
@@ -225,10 +251,10 @@ def wh_resample(x, rate_in: int, y=None, workspace=None, stream=None):
     if n_out < 0:
         raise WhError(WH_EINVAL, "wh_resample_length")
     if y is None:
-        y = torch.empty(batch, n_out, dtype=torch.float32, device=x.device)
+        y = _empty((batch, n_out), torch.float32, x.device, stream)
     need = max(256, lib().wh_resample_workspace(rate_in))
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty((need,), torch.uint8, x.device, stream)
     _check(lib().wh_resample(_ptr(x), n, batch, rate_in, _ptr(y), _ptr(workspace), workspace.numel(), _stream(stream)),
            "wh_resample")
     return y
@@ -238,7 +264,7 @@ def wh_layer_norm(x, g, b, out_bf16=True, y=None, stream=None):
     import torch
     rows, d = x.shape
     if y is None:
-        y = torch.empty(rows, d, dtype=torch.bfloat16 if out_bf16 else torch.float32, device=x.device)
+        y = _empty((rows, d), torch.bfloat16 if out_bf16 else torch.float32, x.device, stream)
     _check(lib().wh_layer_norm(_ptr(x), rows, d, _ptr(g), _ptr(b), _ptr(y), int(out_bf16), _stream(stream)),
            "wh_layer_norm")
     return y
@@ -250,7 +276,7 @@ def wh_linear(a, w, bias=None, epilogue=WH_EPI_BF16, y=None, stream=None):
     rows, k = a.shape
     n = w.shape[0]
     if y is None:
-        y = torch.empty(rows, n, dtype=torch.bfloat16, device=a.device)
+        y = _empty((rows, n), torch.bfloat16, a.device, stream)
     _check(lib().wh_linear(_ptr(a), rows, k, _ptr(w), n, _ptr(bias), epilogue, _ptr(y), _stream(stream)),
            "wh_linear")
     return y
@@ -259,7 +285,7 @@ def wh_linear(a, w, bias=None, epilogue=WH_EPI_BF16, y=None, stream=None):
 def wh_attention(qkv, batch, n_ctx, n_head, out=None, stream=None):
     import torch
     if out is None:
-        out = torch.empty(batch * n_ctx, n_head * 64, dtype=torch.bfloat16, device=qkv.device)
+        out = _empty((batch * n_ctx, n_head * 64), torch.bfloat16, qkv.device, stream)
     _check(lib().wh_attention(_ptr(qkv), batch, n_ctx, n_head, _ptr(out), _stream(stream)), "wh_attention")
     return out
 
@@ -272,23 +298,14 @@ def wh_decode_attention(q, k, v, row_stride, seq_stride, max_keys, n_head, n_key
     import torch
     batch = q.shape[0]
     if out is None:
-        out = torch.empty(batch, 64 * n_head, dtype=torch.bfloat16, device=q.device)
+        out = _empty((batch, 64 * n_head), torch.bfloat16, q.device, stream)
     need = max(256, lib().wh_decode_attention_workspace(batch, n_head, max_keys))
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty((need,), torch.uint8, q.device, stream)
     rc = lib().wh_decode_attention(_ptr(q), _ptr(k), _ptr(v), row_stride, seq_stride, _ptr(n_keys), max_keys, batch,
                                    n_head, _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "wh_decode_attention")
     return out
-
-
-_torch = None
-
-
-def _load_torch():
-    global _torch
-    import torch
-    _torch = torch
 
 
 def _refuse(what):
@@ -355,17 +372,6 @@ def _stream_handle(dev, stream):
     return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _empty(shape, dtype, device, stream, s):
-    """An uninitialised tensor in the order of the launching stream (handle s): memory that the current stream's work may
-    still hold is not in it, and it is not handed out again before the current stream's reads of it are done."""
-    if stream is None or s == _torch._C._cuda_getCurrentRawStream(device.index):
-        return _torch.empty(shape, dtype=dtype, device=device)
-    with _torch.cuda.stream(stream):
-        t = _torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(_torch.cuda.current_stream(device))
-    return t
-
-
 @functools.lru_cache(maxsize=4096)
 def _workspace_bytes(name, *args):
     return getattr(lib(), name)(*args)
@@ -425,7 +431,7 @@ def wh_prefix_attention(q, n_head, prefix=None, own=None, n_kv_head=None, group_
         needs |= WH_GROUP_TABLE
     s = _stream_handle(dev, stream)
     if out is None:
-        out = _empty((rows, 64 * n_head), _torch.bfloat16, q.device, stream, s)
+        out = _empty((rows, 64 * n_head), _torch.bfloat16, q.device, stream)
     elif not (out.dtype is _torch.bfloat16 and out.shape == (rows, 64 * n_head) and out.is_contiguous() and
               out.get_device() == dev):
         _refuse("wh_prefix_attention: out bf16 [batch * n_query][64 n_head]")
@@ -486,7 +492,7 @@ def wh_cache_evict(cache, n_kv_head, budget, recent, out=None, kept=None, worksp
         return _torch.empty(0, dtype=_torch.int32, device=cache.k.device) if n_out is None else n_out
     s = _stream_handle(dev, stream)
     if n_out is None:
-        n_out = _empty((n_set,), _torch.int32, cache.k.device, stream, s)
+        n_out = _empty((n_set,), _torch.int32, cache.k.device, stream)
     if workspace is None:
         need = _workspace_bytes("wh_cache_evict_workspace", n_set, n_kv_head, cache.max_keys, budget)
         if need and indices is not None:
@@ -589,7 +595,7 @@ class Encoder:
         import torch
         batch = mel.shape[0]
         if out is None:
-            out = torch.empty(batch, N_CTX, self.cfg.d_model, dtype=torch.float32, device=self.device)
+            out = _empty((batch, N_CTX, self.cfg.d_model), torch.float32, self.device, stream)
         ws = self.workspace(batch)
         rc = lib().wh_encode(_ptr(mel), batch, ctypes.byref(self.c_cfg), ctypes.byref(self.c_w), _ptr(out),
                              _ptr(ws), ws.numel(), _stream(stream))
@@ -602,7 +608,7 @@ class Encoder:
         import torch
         batch = mel.shape[0]
         if out is None:
-            out = torch.empty(batch, n_ctx, self.cfg.d_model, dtype=torch.float32, device=self.device)
+            out = _empty((batch, n_ctx, self.cfg.d_model), torch.float32, self.device, stream)
         ws = self.workspace(batch, n_ctx)
         rc = lib().wh_encode_ctx(_ptr(mel), batch, n_ctx, ctypes.byref(self.c_cfg), ctypes.byref(self.c_w),
                                  _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
@@ -714,7 +720,7 @@ class CrossKV:
         batch, n_ctx, d = mem.shape
         assert d == self.d_model and mem.dtype == torch.float32 and mem.is_contiguous()
         if kv is None:
-            kv = torch.empty(self.n_layer, batch * n_ctx, 2 * d, dtype=torch.bfloat16, device=self.device)
+            kv = _empty((self.n_layer, batch * n_ctx, 2 * d), torch.bfloat16, self.device, stream)
         need = max(256, lib().wh_prepare_cross_workspace(batch, n_ctx, d))
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
