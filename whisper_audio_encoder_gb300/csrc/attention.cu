@@ -57,23 +57,6 @@ struct AttnArgs {
 };
 
 __device__ __forceinline__ float ex2(float x) { return ex2_approx(x); }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-// MN-major operand (V: rows = keys (the K dimension), 64 contiguous head dims = one 128-byte
-// swizzle atom along N): 8-row K groups 1024 bytes apart.  Only one atom along N, so the
-// leading offset is never used; it is set to the same 1024 bytes.
-__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(1024 >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
 
 __global__ void __launch_bounds__(THREADS, 1) k_attention_tc(const __grid_constant__ CUtensorMap tm, const AttnArgs p) {
     extern __shared__ uint8_t smem_raw[];

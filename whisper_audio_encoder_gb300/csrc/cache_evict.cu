@@ -590,10 +590,6 @@ bool one_kernel(int n_set, int n_head, int max_keys, int budget, bool in_place) 
            (budget <= SM_ROWS || max_keys <= SM_ROWS || (in_place && 2 * items >= SM_HEADS));
 }
 
-size_t up256e(size_t x) { return (x + 255) & ~(size_t)255; }
-
-bool fits(const void *p, size_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // Whether no row of one set's keys (row t at t * row) meets a row of another's (at d + t * row).
 bool rows_apart(int64_t d, int64_t row, int64_t width, int64_t span) {
     const int64_t at = (d % row + row) % row;
@@ -639,7 +635,7 @@ extern "C" size_t wh_cache_evict_workspace(int n_set, int n_kv_head, int max_key
     if (n_set < 1 || n_set > 65535 || n_kv_head < 1 || n_kv_head > 1024 || max_keys < 1 || max_keys > (1 << 30) ||
         budget < 1 || budget > (1 << 30) || one_kernel(n_set, n_kv_head, max_keys, budget, false))
         return 0;
-    return up256e((size_t)n_set * 4) + up256e((size_t)n_set * n_kv_head * std::min(budget, max_keys) * 4);
+    return up256((size_t)n_set * 4) + up256((size_t)n_set * n_kv_head * std::min(budget, max_keys) * 4);
 }
 
 extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, int recent, const wh_keys *out, int *n_out,
@@ -670,7 +666,7 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
     if (cache->n_keys && n_out != cache->n_keys && meet(span_of(n_out, cache->n_set, 4), span_of(cache->n_keys, cache->n_set, 4)))
         return WH_EINVAL;
     size_t need = wh_cache_evict_workspace(cache->n_set, n_kv_head, cache->max_keys, budget);
-    if (kept && need) need = up256e((size_t)cache->n_set * 4);   // the indices go there
+    if (kept && need) need = up256((size_t)cache->n_set * 4);   // the indices go there
     if ((workspace ? ws_bytes : 0) < need) return WH_ENOSPC;
     DevCtl ctl;
     int num_sms = 0;
@@ -714,7 +710,7 @@ extern "C" int wh_cache_evict(const wh_keys *cache, int n_kv_head, int budget, i
         rc = launch_ex(kernel, heads, SM_THREADS, most * (int)sizeof(int), 1, true, s, a);
         if (!rc && same) rc = launch_ex(k_evict_counts, dim3((a.n_set + 255) / 256), 256, 0, 1, true, s, a, n_out);
     } else {
-        a.kept = kept ? kept : reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + up256e((size_t)cache->n_set * 4));
+        a.kept = kept ? kept : reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + up256((size_t)cache->n_set * 4));
         const dim3 warps((unsigned)((items + 3) / 4)), blocks((unsigned)items);
         if (a.max_keys <= 512)
             rc = launch_ex(k_evict_select<32, 16>, warps, 128, 0, 1, true, s, a);

@@ -531,8 +531,6 @@ namespace {
 
 constexpr int DEC_MAX_CROSS = 1500;   // encoder positions
 
-size_t up256d(size_t x) { return (x + 255) & ~(size_t)255; }
-
 struct DecLayout {
     size_t x, xn, q, ao, h, pos_c, n_self, amax, da_self, da_cross, total;
 };
@@ -541,18 +539,18 @@ DecLayout dec_layout(const wh_dec_config *c, int batch) {
     const size_t B = batch, d = c->d_model, f = c->d_ff;
     DecLayout L;
     size_t off = 0;
-    L.x = off;      off += up256d(B * d * 4);
-    L.xn = off;     off += up256d(B * d * 2);
-    L.q = off;      off += up256d(B * d * 2);
-    L.ao = off;     off += up256d(B * d * 2);
-    L.h = off;      off += up256d(B * f * 2);
-    L.pos_c = off;  off += up256d(B * 4);
-    L.n_self = off; off += up256d(B * 4);
-    L.amax = off;   off += up256d(B * 8);
+    L.x = off;      off += up256(B * d * 4);
+    L.xn = off;     off += up256(B * d * 2);
+    L.q = off;      off += up256(B * d * 2);
+    L.ao = off;     off += up256(B * d * 2);
+    L.h = off;      off += up256(B * f * 2);
+    L.pos_c = off;  off += up256(B * 4);
+    L.n_self = off; off += up256(B * 4);
+    L.amax = off;   off += up256(B * 8);
     // one region each for the self- and the cross-attention, so that each keeps its merge
     // tickets zero between calls
-    L.da_self = off;  off += up256d(decode_attention_workspace(batch, c->n_head, c->n_text_ctx));
-    L.da_cross = off; off += up256d(decode_attention_workspace(batch, c->n_head, DEC_MAX_CROSS));
+    L.da_self = off;  off += up256(decode_attention_workspace(batch, c->n_head, c->n_text_ctx));
+    L.da_cross = off; off += up256(decode_attention_workspace(batch, c->n_head, DEC_MAX_CROSS));
     L.total = off;
     return L;
 }
@@ -566,17 +564,16 @@ int check_dec_config(const wh_dec_config *c) {
     return WH_OK;
 }
 
-bool al(const void *p, size_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_dec_weights(const wh_dec_config *c, const wh_dec_weights *w) {
-    if (!w || !al(w->tok_embd, 16) || !al(w->pos, 16) || !al(w->lnf_g, 16) || !al(w->lnf_b, 16)) return WH_EINVAL;
+    if (!w || !fits(w->tok_embd, 16) || !fits(w->pos, 16) || !fits(w->lnf_g, 16) || !fits(w->lnf_b, 16)) return WH_EINVAL;
     if (c->n_layer > 0 && !w->layers) return WH_EINVAL;
     for (int l = 0; l < c->n_layer; ++l) {
         const wh_dec_layer_weights &L = w->layers[l];
         const void *need[] = {L.ln1_g, L.ln1_b, L.wq, L.wk, L.wv, L.bq, L.bv, L.wo, L.bo, L.lnx_g, L.lnx_b,
                               L.xwq, L.xbq, L.xwo, L.xbo, L.ln2_g, L.ln2_b, L.w1, L.b1, L.w2, L.b2};
         for (const void *p : need)
-            if (!al(p, 16)) return WH_EINVAL;
+            if (!fits(p, 16)) return WH_EINVAL;
     }
     return WH_OK;
 }
@@ -598,9 +595,9 @@ extern "C" int wh_decode_step(const int *tok, const int *pos, int batch, const w
     if (int rc = check_dec_config(cfg)) return rc;
     if (batch < 0 || batch > SK_MAX_B || n_ctx < 1 || n_ctx > DEC_MAX_CROSS) return WH_EINVAL;
     if (batch == 0) return WH_OK;
-    if (!al(tok, 4) || !al(pos, 4) || !al(logits, 16) || !al(workspace, 256) || (next_tok && !al(next_tok, 4)))
+    if (!fits(tok, 4) || !fits(pos, 4) || !fits(logits, 16) || !fits(workspace, 256) || (next_tok && !fits(next_tok, 4)))
         return WH_EINVAL;
-    if (cfg->n_layer > 0 && (!al(kcache, 16) || !al(vcache, 16) || !al(cross_kv, 16))) return WH_EINVAL;
+    if (cfg->n_layer > 0 && (!fits(kcache, 16) || !fits(vcache, 16) || !fits(cross_kv, 16))) return WH_EINVAL;
     if (int rc = check_dec_weights(cfg, w)) return rc;
     const DecLayout L = dec_layout(cfg, batch);
     if (ws_bytes < L.total) return WH_ENOSPC;

@@ -122,6 +122,11 @@ void trace_begin(int cls, cudaStream_t s);
 void trace_end(int cls, cudaStream_t s, double flops, double bytes);
 void count_launch(int n = 1);
 
+// Workspace parts start on 256-byte boundaries.
+inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+// Whether p is a pointer aligned to a bytes.
+inline bool fits(const void *p, size_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
 // One launch with optional programmatic serialization and cluster size along x.
 template <class... F, class... A>
 int launch_ex(void (*kernel)(F...), dim3 grid, int threads, int smem, int cluster, bool pdl, cudaStream_t s, A... args) {

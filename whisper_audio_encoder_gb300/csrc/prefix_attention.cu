@@ -571,8 +571,6 @@ __global__ void __launch_bounds__(32 * PW_WARPS, 4) k_prefix_weight(const PaArgs
     }
 }
 
-size_t up256p(size_t x) { return (x + 255) & ~(size_t)255; }
-
 constexpr long long PA_BLOCKS = 3 * 152;   // k_prefix_attention: 3 blocks on each of GB300's 152 SMs
 constexpr long long PT_BLOCKS = 2 * 152;   // k_prefix_tc: 2 on each
 // The prefix part goes to k_prefix_tc when its sets have more than PT_MIN_ROWS rows on average and there are at
@@ -696,14 +694,12 @@ PaPlan plan(PaArgs &a, bool may_tc, bool pre_weight, bool own_weight) {
     a.score_floats = own_weight && a.own_cluster == 1 && a.own_tiles == 1 && room ? (int)scores : 0;
     const size_t rows = (size_t)a.batch * a.nq * a.n_head;
     size_t off = 0;
-    pl.part_o = off;  off += up256p(rows * a.n_part * 64 * 4);
-    pl.part_ml = off; off += up256p(rows * a.n_part * 8);
-    pl.stats = off;   off += pre_weight || (own_weight && !a.score_floats) ? up256p(rows * 8) : 0;
+    pl.part_o = off;  off += up256(rows * a.n_part * 64 * 4);
+    pl.part_ml = off; off += up256(rows * a.n_part * 8);
+    pl.stats = off;   off += pre_weight || (own_weight && !a.score_floats) ? up256(rows * 8) : 0;
     pl.total = off;
     return pl;
 }
-
-bool fits(const void *p, size_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_keys(const wh_keys *s, int n_kv, PaSet *o) {
     *o = PaSet{};

@@ -221,13 +221,11 @@ __device__ __forceinline__ void finish_cluster(const PaArgs &p, const Rows &rw, 
     const int rank = (int)cluster_ctarank();
     for (int i = rank * THREADS + tid; i < rows * 8; i += ranks * THREADS) {
         const int r = i >> 3, d0 = 8 * (i & 7);
-        const uint32_t la = smem_u32(sml) + r * 8, oa = smem_u32(so) + (r * so_row + d0) * 4;
+        const uint8_t *la = static_cast<const uint8_t *>(sml) + r * 8, *oa = static_cast<const uint8_t *>(so) + (r * so_row + d0) * 4;
         float mt = -INFINITY, lt = 0.0f, v[8] = {};
         for (int c = 0; c < ranks; ++c) {
             float m, l;
-            uint32_t ra, rb;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(la), "r"(c));
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(oa), "r"(c));
+            const uint32_t ra = mapa_shared(la, c), rb = mapa_shared(oa, c);
             asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(m), "=f"(l) : "r"(ra) : "memory");
             float u[8];
             asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"

@@ -76,8 +76,6 @@ DevCtl ctl_of(const DevState *st, unsigned long long wait_ns = DEFAULT_WAIT_NS) 
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 // ---- tracing ---------------------------------------------------------------------------
 struct TraceRec {
     int cls;
