@@ -109,6 +109,7 @@ def test_recorded_without_a_workspace():
         calls(out, to, q)
     other, other_to = torch.empty_like(q), fresh()
     s = torch.cuda.Stream()
+    torch.cuda.synchronize()
     for i in range(10):
         graph.replay()
         with torch.cuda.stream(s):                     # eager calls of the same sizes beside the replay
